@@ -432,6 +432,225 @@ nvfp4_status nvfp4_moe_down_combine(const nvfp4_moe_down_args *args, nvfp4_strea
 size_t nvfp4_moe_down_workspace_bytes(const nvfp4_moe_down_args *args);
 
 /* ------------------------------------------------------------------------ *
+ * nvfp4_route_topk -- expert routing: scores, top-k choice, weights.
+ *
+ * Makes the expert_ids and route_weights that nvfp4_grouped_gemm and
+ * nvfp4_moe_down_combine (and their MXFP4 forms below) take ("GLM-5.2-NVFP4"
+ * card: 256 routed experts, 8 per token).  Per token, with logits x_e:
+ *   s_e   = 1 / (1 + exp(-x_e))  (SIGMOID)  or  softmax_e(x)  (SOFTMAX), fp32;
+ *   key_e = s_e + bias_e with a bias (a balancing term that takes part in the
+ *           choice only), x_e without one;
+ *   groups (num_groups > 1): the experts form num_groups equal runs; only the
+ *           topk_groups runs with the largest group score stay, the score being
+ *           the largest key (group_top = 1) or the sum of the two largest
+ *           s_e + bias_e (group_top = 2; a run with one choosable expert: its
+ *           s_e + bias_e);
+ *   the top_k largest keys, in descending order; among experts and groups
+ *           equal values go to the lowest index;
+ *   weight_j = scale * s_j / (renormalize ? sum of the chosen s : 1).
+ * A logit of -inf masks its expert, as does NaN (or a key that is one of
+ * them): it is never chosen, and its softmax score is 0.  A logit of +inf
+ * counts as the largest finite fp32.  Where fewer than top_k experts can be
+ * chosen the remaining ids are -1 and their weights 0 (nvfp4_grouped_gemm
+ * drops such pairs); chosen weights are 0 if their scores sum to 0.
+ *   logits [num_tokens][ld] bf16 or fp32 (logits_dtype), expert_ids and
+ *   route_weights [num_tokens][top_k].
+ * Requirements: num_experts <= 1024, top_k <= 32, num_groups <= 32 and a
+ *   divisor of num_experts, top_k <= topk_groups * num_experts / num_groups;
+ *   pointers aligned to their element.  Rows that start on 16 bytes with a
+ *   multiple of 16 bytes of experts are read in vectors.  No workspace.
+ * ------------------------------------------------------------------------ */
+typedef enum { NVFP4_SCORE_SIGMOID = 0, NVFP4_SCORE_SOFTMAX = 1 } nvfp4_score;
+
+typedef struct {
+  int64_t num_tokens, num_experts, top_k;
+  const void *logits;
+  int64_t ld;                    /* elements */
+  int32_t logits_dtype;          /* nvfp4_out_dtype */
+  int32_t score;                 /* nvfp4_score */
+  const float *bias;             /* [num_experts] or NULL */
+  int32_t num_groups, topk_groups, group_top;   /* num_groups <= 1: no groups */
+  int32_t renormalize;
+  float scale;
+  int32_t *expert_ids;
+  float *route_weights;
+} nvfp4_route_topk_args;
+
+nvfp4_status nvfp4_route_topk(const nvfp4_route_topk_args *args, nvfp4_stream stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_route_topk_backward -- gradient of the routing weights.
+ *
+ * grad_logits [num_tokens][ld_grad] (type of the logits, every element of a
+ * row's num_experts written) from grad_weights [num_tokens][top_k], with the
+ * choice expert_ids held fixed (ids outside [0, num_experts) contribute
+ * nothing; an id appears once in a row).  With d_j = scale * grad_weights_j,
+ * w_j = s_j / S, S = sum of the chosen s:
+ *   SIGMOID: ds_j = renormalize ? (d_j - sum_i d_i w_i) / S : d_j and
+ *            grad x_j = ds_j s_j (1 - s_j) for the chosen, 0 elsewhere;
+ *   SOFTMAX, renormalize: grad x_j = w_j (d_j - sum_i d_i w_i) for the chosen,
+ *            0 elsewhere (the weights are the softmax over the chosen logits);
+ *   SOFTMAX: grad x_e = s_e (d_e - sum_j d_j s_j) for every expert.
+ * The bias has no gradient.  Requirements as nvfp4_route_topk.  No workspace.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t num_tokens, num_experts, top_k;
+  const void *logits;
+  int64_t ld;
+  int32_t logits_dtype;          /* nvfp4_out_dtype, of logits and grad_logits */
+  int32_t score;                 /* nvfp4_score */
+  int32_t renormalize;
+  float scale;
+  const int32_t *expert_ids;
+  const float *grad_weights;
+  void *grad_logits;
+  int64_t ld_grad;
+} nvfp4_route_topk_backward_args;
+
+nvfp4_status nvfp4_route_topk_backward(const nvfp4_route_topk_backward_args *args, nvfp4_stream stream);
+
+/* ------------------------------------------------------------------------ *
+ * MXFP4 -- the OCP Microscaling form of the 4-bit linear (OCP Microscaling
+ * Formats (MX) Specification v1.0: E2M1 elements, one E8M0 scale, a power of
+ * two, per 32 consecutive elements along the contraction axis, no global
+ * scale).  Codes are packed as above.  Scales are E8M0 bytes (value
+ * 2^(byte - 127), 255 = NaN), linear [rows][cols/32] or in the swizzled layout
+ * above with cols/32 scale columns; pad bytes are written as 0 and must not be
+ * 255 where a caller packs its own.
+ *
+ * nvfp4_mxfp4_quantize: bf16 -> MXFP4, `batch` matrices src[b] = [rows][ld].
+ *   amax = max |x| of a block, X = 2^(floor(log2 amax) - 2) (byte at least 0),
+ *   code = sign(x) | E2M1_rn_satfinite(|x| / X); an all-zero block has byte 0;
+ *   a block that holds an infinity or a NaN has byte 255 and codes 0.
+ * nvfp4_mxfp4_dequantize: MXFP4 -> bf16 [rows][cols] (or transposed
+ *   [cols][rows]), E2M1(code) * 2^(byte - 127): exact for bytes <= 252.
+ * Requirements: cols % 32 == 0, batch <= 65535, rows, cols <= 2^31; src / codes /
+ *   sf / out 16-byte aligned, ld, ldo and the batch strides % 8 == 0
+ *   (transposed: ldo and its batch stride % 2).  Codes and scales of a batch are packed,
+ *   nvfp4_codes_bytes and nvfp4_mxfp4_sf_bytes per matrix.  No workspace.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const void *src;               /* bf16 */
+  int64_t batch, rows, cols, ld, batch_stride;  /* strides in elements */
+  int32_t sf_layout;             /* nvfp4_sf_layout */
+  uint8_t *codes, *sf;
+} nvfp4_mxfp4_quant_args;
+
+nvfp4_status nvfp4_mxfp4_quantize(const nvfp4_mxfp4_quant_args *args, nvfp4_stream stream);
+
+typedef struct {
+  const uint8_t *codes, *sf;
+  int32_t sf_layout;             /* nvfp4_sf_layout */
+  int64_t batch, rows, cols;     /* of the packed matrices */
+  int32_t transpose;
+  void *out;                     /* bf16 */
+  int64_t ldo, out_batch_stride; /* elements */
+} nvfp4_mxfp4_dequant_args;
+
+nvfp4_status nvfp4_mxfp4_dequantize(const nvfp4_mxfp4_dequant_args *args, nvfp4_stream stream);
+/* Bytes of the MXFP4 scales of a [rows][cols] matrix (1x32 blocks). */
+size_t nvfp4_mxfp4_sf_bytes(int64_t rows, int64_t cols, int32_t sf_layout);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_mxfp4_gemm -- D = A B^T of two MXFP4 operands.
+ *
+ * nvfp4_gemm's product on kind::mxf4 tensor-core MMAs, fp32 accumulation.
+ *   A [M][K]: packed (a_codes [M][K/2] + a_sf swizzled), or bf16 a_bf16
+ *     [M][lda] quantized in the call (nvfp4_mxfp4_quantize's arithmetic).
+ *   B [N][K]: b_codes [N][K/2], b_sf swizzled.
+ *   D [M][ldd] bf16 or fp32, written (not accumulated).
+ * M <= 32 rows run with the operands swapped; larger M as in nvfp4_gemm.
+ * Requirements: K % 32 == 0; ldd % 8 == 0 (bf16 out) or % 4 (fp32 out);
+ *   lda % 8 == 0; every pointer 16-byte aligned.
+ * Workspace: nvfp4_mxfp4_gemm_workspace_bytes(&args).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t M, N, K;
+  const uint8_t *a_codes, *a_sf;
+  const void *a_bf16;
+  int64_t lda;                   /* elements */
+  const uint8_t *b_codes, *b_sf;
+  int32_t out_dtype;             /* nvfp4_out_dtype */
+  void *d;
+  int64_t ldd;                   /* elements */
+  void *workspace;
+  size_t workspace_bytes;
+  void *prof_begin, *prof_end;   /* optional cudaEvent_t pair around the GEMM */
+} nvfp4_mxfp4_gemm_args;
+
+nvfp4_status nvfp4_mxfp4_gemm(const nvfp4_mxfp4_gemm_args *args, nvfp4_stream stream);
+size_t nvfp4_mxfp4_gemm_workspace_bytes(const nvfp4_mxfp4_gemm_args *args);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_mxfp4_dgrad -- input gradient of the frozen MXFP4 linear: dX = dY W.
+ *
+ * dY bf16 [M][lddy] (N columns), W [N][K] packed (swizzled scales), dX [M][K]
+ * (lddx).  W is rebuilt in bf16, transposed, in the workspace (exact) for a
+ * bf16 tensor-core GEMM with fp32 accumulation.
+ * Requirements: K % 32 == 0; dy 16-byte aligned, lddy % 8 == 0; dx 16-byte
+ *   aligned, lddx % 8 (bf16) or % 4 (fp32); w_codes, w_sf 16-byte aligned.
+ * Workspace: nvfp4_mxfp4_dgrad_workspace_bytes(&args).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t M, N, K;
+  const void *dy;
+  int64_t lddy;
+  const uint8_t *w_codes, *w_sf;
+  int32_t out_dtype;             /* nvfp4_out_dtype */
+  void *dx;
+  int64_t lddx;
+  void *workspace;
+  size_t workspace_bytes;
+  void *prof_begin, *prof_end;   /* optional cudaEvent_t pair around the GEMM */
+} nvfp4_mxfp4_dgrad_args;
+
+nvfp4_status nvfp4_mxfp4_dgrad(const nvfp4_mxfp4_dgrad_args *args, nvfp4_stream stream);
+size_t nvfp4_mxfp4_dgrad_workspace_bytes(const nvfp4_mxfp4_dgrad_args *args);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_mxfp4_grouped_gemm, nvfp4_mxfp4_moe_down_combine -- the routed
+ * experts' products with MXFP4 experts: nvfp4_grouped_gemm and
+ * nvfp4_moe_down_combine with MXFP4 in place of NVFP4 (no global scales, no
+ * LoRA); the routing forms, the row order, the handling of ids outside
+ * [0, num_experts) and the other requirements are theirs.  x_sf is linear
+ * [num_tokens][K/32], w_sf [E][swizzled N x K/32].
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t num_tokens, top_k, num_experts, N, K;
+  const int32_t *expert_ids;
+  const int32_t *offsets_in, *perm_in;   /* precomputed routing; NULL = route expert_ids */
+  const void *x_bf16;                    /* or packed rows: */
+  const uint8_t *x_codes, *x_sf;
+  const uint8_t *w_codes, *w_sf;
+  int32_t out_dtype;                     /* nvfp4_out_dtype of d */
+  void *d;
+  int32_t *perm_out;
+  int32_t *expert_offsets_out;
+  void *workspace;
+  size_t workspace_bytes;
+  void *prof_begin, *prof_end;           /* optional cudaEvent_t pair around the grouped GEMM */
+} nvfp4_mxfp4_grouped_args;
+
+nvfp4_status nvfp4_mxfp4_grouped_gemm(const nvfp4_mxfp4_grouped_args *args, nvfp4_stream stream);
+size_t nvfp4_mxfp4_grouped_workspace_bytes(const nvfp4_mxfp4_grouped_args *args);
+
+typedef struct {
+  int64_t num_tokens, top_k, num_experts, N, K;
+  const void *h;                 /* bf16 [num_tokens*top_k][K], expert-grouped rows */
+  const int32_t *perm;           /* [P]: grouped row -> token*top_k + slot */
+  const int32_t *expert_offsets; /* [E+1] */
+  const float *route_weights;    /* [num_tokens][top_k] */
+  const uint8_t *w_codes, *w_sf;
+  void *y;                       /* bf16 [num_tokens][N] */
+  void *workspace;
+  size_t workspace_bytes;
+  void *prof_begin, *prof_end;   /* optional cudaEvent_t pair around the grouped GEMM */
+} nvfp4_mxfp4_moe_down_args;
+
+nvfp4_status nvfp4_mxfp4_moe_down_combine(const nvfp4_mxfp4_moe_down_args *args, nvfp4_stream stream);
+size_t nvfp4_mxfp4_moe_down_workspace_bytes(const nvfp4_mxfp4_moe_down_args *args);
+
+/* ------------------------------------------------------------------------ *
  * Size queries and status.
  * ------------------------------------------------------------------------ */
 /* Bytes of packed codes of a [rows][cols] matrix: rows * cols / 2. */

@@ -13,9 +13,11 @@ import ctypes as C
 import torch
 
 from ._binding import (DGRAD_DEQUANT_BF16, DGRAD_FP4_COLPACK, EXPORTS, DequantArgs, DgradArgs,
-                       GemmArgs, GroupedArgs, LoraArgs, MoeDownArgs, NVFP4Error, OUT_BF16, OUT_FP32,
-                       PACK_BOTH, PACK_COL, PACK_ROW, QuantArgs, SF_LINEAR, SF_SWIZZLED, WgradArgs,
-                       check, load)
+                       GemmArgs, GroupedArgs, LoraArgs, MoeDownArgs, MxDequantArgs, MxDgradArgs,
+                       MxGemmArgs, MxGroupedArgs, MxMoeDownArgs, MxQuantArgs, NVFP4Error, OUT_BF16,
+                       OUT_FP32, PACK_BOTH, PACK_COL, PACK_ROW, QuantArgs, RouteTopkArgs,
+                       RouteTopkBackwardArgs, SCORE_SIGMOID, SCORE_SOFTMAX, SF_LINEAR, SF_SWIZZLED,
+                       WgradArgs, check, load)
 
 __all__ = [
     "load", "NVFP4Error", "nvfp4_quantize", "nvfp4_gemm", "nvfp4_grouped_gemm",
@@ -24,10 +26,18 @@ __all__ = [
     "SF_LINEAR", "SF_SWIZZLED", "PACK_ROW", "PACK_COL", "PACK_BOTH", "EXPORTS",
     "nvfp4_dequantize", "nvfp4_dgrad", "prepare_dgrad", "nvfp4_wgrad", "prepare_wgrad",
     "nvfp4_moe_down_combine", "prepare_moe_down",
+    "nvfp4_route_topk", "prepare_route_topk", "nvfp4_route_topk_backward",
+    "prepare_route_topk_backward", "nvfp4_mxfp4_quantize", "prepare_mxfp4_quantize",
+    "nvfp4_mxfp4_dequantize", "prepare_mxfp4_dequantize", "nvfp4_mxfp4_sf_bytes",
+    "nvfp4_mxfp4_gemm", "prepare_mxfp4_gemm", "nvfp4_mxfp4_dgrad", "prepare_mxfp4_dgrad",
+    "nvfp4_mxfp4_grouped_gemm", "prepare_mxfp4_grouped", "nvfp4_mxfp4_moe_down_combine",
+    "prepare_mxfp4_moe_down",
 ]
 
 _PACK = {"row": PACK_ROW, "col": PACK_COL, "both": PACK_BOTH}
 _SF = {"linear": SF_LINEAR, "swizzled": SF_SWIZZLED}
+_SCORE = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
+_OUT = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
 
 
 def _p(t):
@@ -393,4 +403,357 @@ def nvfp4_moe_down_combine(h, perm, expert_offsets, route_weights, w_codes, w_sf
     call, out = prepare_moe_down(h, perm, expert_offsets, route_weights, w_codes, w_sf,
                                  w_global_scale, N, K, num_experts, h_global_scale, lora, out)
     call(stream)
+    return out
+
+
+# ------------------------------------------------------------------ routing --
+
+def _need(t, what: str, dtypes, shape=None, numel: int | None = None):
+    """A CUDA tensor of one of `dtypes`, of `shape` (contiguous rows) or at least
+    `numel` contiguous elements; raises otherwise (the library sees only its pointer)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{what} must be a CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if shape is not None:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{what} must have unit stride along its last dimension")
+    if numel is not None and (not t.is_contiguous() or t.numel() < numel):
+        raise ValueError(f"{what} must be contiguous with at least {numel} elements")
+    return t
+
+
+def _ld(t) -> int:
+    """Row stride of a 2-D tensor; a single row's is its width (torch leaves it arbitrary)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _same_device(*tensors):
+    dev = {t.device for t in tensors if t is not None}
+    if len(dev) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, dev))}")
+
+
+def _run(call: Prepared, stream):
+    """One call.  On a stream other than the current one it waits for the work
+    queued so far (the inputs, the zero-filled workspace), and the tensors'
+    memory is not reused before that stream is done with them."""
+    cur = torch.cuda.current_stream()
+    if stream is not None and stream != cur:
+        stream.wait_stream(cur)
+        for t in call.keep:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    call(stream)
+
+
+def prepare_route_topk(logits, top_k: int, *, bias=None, score: str = "sigmoid", num_groups: int = 1,
+                       topk_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+                       scale: float = 1.0) -> tuple[Prepared, dict]:
+    """Expert routing.  logits [T, E] bf16 or fp32 (rows may be strided), bias
+    fp32 [E]; returns (Prepared call, dict of expert_ids int32 [T, k] and weights
+    fp32 [T, k]), the expert_ids / route_weights of the grouped calls.
+
+    The top_k experts of a token by score (+ bias), from the topk_groups best of
+    num_groups equal runs (ranked by their group_top largest); weights = scale *
+    score (without bias), divided by their sum with renormalize.  A logit of
+    -inf or NaN masks its expert; missing choices get id -1 and weight 0."""
+    lib = load()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [tokens, experts] tensor")
+    _need(logits, "logits", (torch.bfloat16, torch.float32), logits.shape)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", (torch.float32,), (E,))
+    _same_device(logits, bias)
+    out = {"expert_ids": torch.empty((T, top_k), dtype=torch.int32, device=logits.device),
+           "weights": torch.empty((T, top_k), dtype=torch.float32, device=logits.device)}
+    a = RouteTopkArgs(num_tokens=T, num_experts=E, top_k=top_k, logits=logits.data_ptr(), ld=_ld(logits),
+                      logits_dtype=_OUT[logits.dtype], score=_SCORE[score],
+                      bias=None if bias is None else bias.data_ptr(), num_groups=num_groups,
+                      topk_groups=topk_groups, group_top=group_top, renormalize=1 if renormalize else 0,
+                      scale=float(scale), expert_ids=out["expert_ids"].data_ptr(),
+                      route_weights=out["weights"].data_ptr())
+    keep = (logits, bias, out["expert_ids"], out["weights"])
+    return Prepared(lib.nvfp4_route_topk, a, keep, "nvfp4_route_topk"), out
+
+
+def nvfp4_route_topk(logits, top_k: int, *, stream=None, **form) -> dict:
+    """See prepare_route_topk."""
+    call, out = prepare_route_topk(logits, top_k, **form)
+    _run(call, stream)
+    return out
+
+
+def prepare_route_topk_backward(logits, expert_ids, grad_weights, *, score: str = "sigmoid",
+                                renormalize: bool = True, scale: float = 1.0,
+                                out=None) -> tuple[Prepared, torch.Tensor]:
+    """Gradient of nvfp4_route_topk's weights with respect to the logits, the
+    choice held fixed: grad_logits [T, E] in the logits' type from grad_weights
+    fp32 [T, k] and the call's expert_ids (ids outside [0, E) contribute
+    nothing); score, renormalize and scale as in the forward call."""
+    lib = load()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [tokens, experts] tensor")
+    _need(logits, "logits", (torch.bfloat16, torch.float32), logits.shape)
+    T, E = logits.shape
+    k = expert_ids.shape[-1]
+    _need(expert_ids, "expert_ids", (torch.int32,), (T, k), T * k)
+    _need(grad_weights, "grad_weights", (torch.float32,), (T, k), T * k)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _need(out, "out", (logits.dtype,), (T, E))
+    _same_device(logits, expert_ids, grad_weights, out)
+    a = RouteTopkBackwardArgs(num_tokens=T, num_experts=E, top_k=k, logits=logits.data_ptr(), ld=_ld(logits),
+                              logits_dtype=_OUT[logits.dtype], score=_SCORE[score],
+                              renormalize=1 if renormalize else 0, scale=float(scale),
+                              expert_ids=expert_ids.data_ptr(), grad_weights=grad_weights.data_ptr(),
+                              grad_logits=out.data_ptr(), ld_grad=_ld(out))
+    keep = (logits, expert_ids, grad_weights, out)
+    return Prepared(lib.nvfp4_route_topk_backward, a, keep, "nvfp4_route_topk_backward"), out
+
+
+def nvfp4_route_topk_backward(logits, expert_ids, grad_weights, *, stream=None, **form) -> torch.Tensor:
+    """See prepare_route_topk_backward."""
+    call, out = prepare_route_topk_backward(logits, expert_ids, grad_weights, **form)
+    _run(call, stream)
+    return out
+
+
+# -------------------------------------------------------------------- MXFP4 --
+
+def nvfp4_mxfp4_sf_bytes(rows: int, cols: int, sf_layout: str = "swizzled") -> int:
+    return int(load().nvfp4_mxfp4_sf_bytes(rows, cols, _SF[sf_layout]))
+
+
+def prepare_mxfp4_quantize(src, sf_layout: str = "swizzled") -> tuple[Prepared, dict]:
+    """bf16 [rows, cols] (or [batch, rows, cols]) -> MXFP4: codes uint8 [.., rows,
+    cols/2] and E8M0 scales sf, linear [.., rows, cols/32] or swizzled (flat)."""
+    lib = load()
+    if not isinstance(src, torch.Tensor) or src.dim() not in (2, 3):
+        raise ValueError("src must be a [rows, cols] or [batch, rows, cols] tensor")
+    _need(src, "src", (torch.bfloat16,), src.shape)
+    s3 = src if src.dim() == 3 else src.unsqueeze(0)
+    B, R, Cc = s3.shape
+    sl = _SF[sf_layout]
+    codes = torch.empty((B, R, Cc // 2), dtype=torch.uint8, device=src.device)
+    sf = torch.empty((B, R, Cc // 32) if sl == SF_LINEAR else (B, lib.nvfp4_mxfp4_sf_bytes(R, Cc, sl)),
+                     dtype=torch.uint8, device=src.device)
+    ld = s3.stride(1) if R > 1 else max(s3.stride(1), Cc)
+    a = MxQuantArgs(src=s3.data_ptr(), batch=B, rows=R, cols=Cc, ld=ld, batch_stride=s3.stride(0),
+                    sf_layout=sl, codes=codes.data_ptr(), sf=sf.data_ptr())
+    out = {"codes": codes, "sf": sf} if src.dim() == 3 else {"codes": codes[0], "sf": sf[0]}
+    return Prepared(lib.nvfp4_mxfp4_quantize, a, (src, codes, sf), "nvfp4_mxfp4_quantize"), out
+
+
+def nvfp4_mxfp4_quantize(src, sf_layout: str = "swizzled", stream=None) -> dict:
+    """See prepare_mxfp4_quantize."""
+    call, out = prepare_mxfp4_quantize(src, sf_layout)
+    _run(call, stream)
+    return out
+
+
+def prepare_mxfp4_dequantize(codes, sf, transpose: bool = False, sf_layout: str = "swizzled",
+                             out=None) -> tuple[Prepared, torch.Tensor]:
+    """MXFP4 codes [.., rows, cols/2] with their scales -> bf16 [.., rows, cols]
+    (exact), or [.., cols, rows] with transpose."""
+    lib = load()
+    if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
+        raise ValueError("codes must be a [rows, cols/2] or [batch, rows, cols/2] tensor")
+    B = codes.shape[0] if codes.dim() == 3 else 1
+    R, Cc = codes.shape[-2], 2 * codes.shape[-1]
+    sl = _SF[sf_layout]
+    _need(codes, "codes", (torch.uint8,), numel=B * R * Cc // 2)
+    _need(sf, "sf", (torch.uint8,), numel=B * lib.nvfp4_mxfp4_sf_bytes(R, Cc, sl))
+    shape = (Cc, R) if transpose else (R, Cc)
+    if out is None:
+        pitch = shape[1] + shape[1] % 2          # transposed rows are written in bf16 pairs
+        out = torch.empty((B, shape[0], pitch), dtype=torch.bfloat16, device=codes.device)[..., :shape[1]]
+        out = out if codes.dim() == 3 else out[0]
+    _need(out, "out", (torch.bfloat16,), (B, *shape) if codes.dim() == 3 else shape)
+    _same_device(codes, sf, out)
+    o3 = out if out.dim() == 3 else out.unsqueeze(0)
+    ldo = o3.stride(1) if shape[0] > 1 else max(o3.stride(1), shape[1])
+    a = MxDequantArgs(codes=codes.data_ptr(), sf=sf.data_ptr(), sf_layout=sl, batch=B, rows=R, cols=Cc,
+                      transpose=1 if transpose else 0, out=out.data_ptr(), ldo=ldo,
+                      out_batch_stride=o3.stride(0))
+    return Prepared(lib.nvfp4_mxfp4_dequantize, a, (codes, sf, out), "nvfp4_mxfp4_dequantize"), out
+
+
+def nvfp4_mxfp4_dequantize(codes, sf, transpose: bool = False, sf_layout: str = "swizzled", out=None,
+                           stream=None) -> torch.Tensor:
+    """See prepare_mxfp4_dequantize."""
+    call, out = prepare_mxfp4_dequantize(codes, sf, transpose, sf_layout, out)
+    _run(call, stream)
+    return out
+
+
+def _mx_weight(lib, codes, sf, rows: int, K: int, what: str):
+    _need(codes, f"{what}_codes", (torch.uint8,), numel=rows * (K // 2))
+    _need(sf, f"{what}_sf", (torch.uint8,), numel=lib.nvfp4_mxfp4_sf_bytes(rows, K, SF_SWIZZLED))
+
+
+def _workspace(call_args, query, device) -> torch.Tensor:
+    ws = _ws(query(C.byref(call_args)), device)
+    call_args.workspace, call_args.workspace_bytes = ws.data_ptr(), ws.numel()
+    return ws
+
+
+def prepare_mxfp4_gemm(b_codes, b_sf, N: int, K: int, *, a_codes=None, a_sf=None, a_bf16=None,
+                       out_dtype=torch.bfloat16, out=None) -> tuple[Prepared, torch.Tensor]:
+    """D [M, N] = A B^T of MXFP4 operands.  A: a_bf16 [M, K] quantized in the call,
+    or packed a_codes [M, K/2] + a_sf (swizzled); B: b_codes [N, K/2], b_sf
+    (swizzled)."""
+    lib = load()
+    _mx_weight(lib, b_codes, b_sf, N, K, "b")
+    if (a_bf16 is None) == (a_codes is None):
+        raise ValueError("give a_bf16, or a_codes with a_sf")
+    if a_bf16 is not None:
+        _need(a_bf16, "a_bf16", (torch.bfloat16,), (a_bf16.shape[0], K))
+    else:
+        _mx_weight(lib, a_codes, a_sf, a_codes.shape[0], K, "a")
+    M = (a_codes if a_bf16 is None else a_bf16).shape[0]
+    if out is None:
+        step = 8 if out_dtype == torch.bfloat16 else 4
+        out = torch.empty((M, (N + step - 1) // step * step), dtype=out_dtype, device=b_codes.device)[:, :N]
+    _need(out, "out", tuple(_OUT), (M, N))
+    _same_device(b_codes, b_sf, a_codes, a_sf, a_bf16, out)
+    a = MxGemmArgs(M=M, N=N, K=K, b_codes=b_codes.data_ptr(), b_sf=b_sf.data_ptr(), out_dtype=_OUT[out.dtype],
+                   d=out.data_ptr(), ldd=_ld(out))
+    if a_bf16 is not None:
+        a.a_bf16, a.lda = a_bf16.data_ptr(), _ld(a_bf16)
+    else:
+        a.a_codes, a.a_sf = a_codes.data_ptr(), a_sf.data_ptr()
+    ws = _workspace(a, lib.nvfp4_mxfp4_gemm_workspace_bytes, b_codes.device)
+    call = Prepared(lib.nvfp4_mxfp4_gemm, a, (b_codes, b_sf, a_codes, a_sf, a_bf16, out, ws), "nvfp4_mxfp4_gemm")
+    call.workspace = ws
+    return call, out
+
+
+def nvfp4_mxfp4_gemm(b_codes, b_sf, N: int, K: int, *, stream=None, **form) -> torch.Tensor:
+    """See prepare_mxfp4_gemm."""
+    call, out = prepare_mxfp4_gemm(b_codes, b_sf, N, K, **form)
+    _run(call, stream)
+    return out
+
+
+def prepare_mxfp4_dgrad(dy, w_codes, w_sf, N: int, K: int, *, out_dtype=torch.bfloat16,
+                        out=None) -> tuple[Prepared, torch.Tensor]:
+    """dX [M, K] = dY [M, N] W [N, K] with W packed as MXFP4 (swizzled scales)."""
+    lib = load()
+    _mx_weight(lib, w_codes, w_sf, N, K, "w")
+    _need(dy, "dy", (torch.bfloat16,), (dy.shape[0], N))
+    M = dy.shape[0]
+    if out is None:
+        out = torch.empty((M, K), dtype=out_dtype, device=dy.device)
+    _need(out, "out", tuple(_OUT), (M, K))
+    _same_device(dy, w_codes, w_sf, out)
+    a = MxDgradArgs(M=M, N=N, K=K, dy=dy.data_ptr(), lddy=_ld(dy), w_codes=w_codes.data_ptr(),
+                    w_sf=w_sf.data_ptr(), out_dtype=_OUT[out.dtype], dx=out.data_ptr(), lddx=_ld(out))
+    ws = _workspace(a, lib.nvfp4_mxfp4_dgrad_workspace_bytes, dy.device)
+    call = Prepared(lib.nvfp4_mxfp4_dgrad, a, (dy, w_codes, w_sf, out, ws), "nvfp4_mxfp4_dgrad")
+    call.workspace = ws
+    return call, out
+
+
+def nvfp4_mxfp4_dgrad(dy, w_codes, w_sf, N: int, K: int, *, stream=None, **form) -> torch.Tensor:
+    """See prepare_mxfp4_dgrad."""
+    call, out = prepare_mxfp4_dgrad(dy, w_codes, w_sf, N, K, **form)
+    _run(call, stream)
+    return out
+
+
+def prepare_mxfp4_grouped(expert_ids, x_bf16, w_codes, w_sf, N: int, K: int, num_experts: int, *,
+                          x_packed=None, routing=None, top_k: int | None = None,
+                          out_dtype=torch.bfloat16):
+    """Routed MXFP4 experts, the forms of prepare_grouped: expert_ids int32 [T, k]
+    or routing = (offsets [E+1], perm [T*k]) with top_k; x_bf16 [T, K] or
+    x_packed = (codes [T, K/2], linear sf [T, K/32]); weights stacked codes
+    [E, N, K/2] and swizzled scales.  Returns (Prepared call, (d [T*k, N] grouped
+    by expert, perm, offsets))."""
+    lib = load()
+    _mx_weight(lib, w_codes, w_sf, num_experts * N, K, "w")
+    if (expert_ids is None) == (routing is None):
+        raise ValueError("give expert_ids, or routing=(offsets, perm) with top_k")
+    if (x_bf16 is None) == (x_packed is None):
+        raise ValueError("give x_bf16, or x_packed=(codes, sf)")
+    if expert_ids is not None:
+        T, topk = expert_ids.shape
+        _need(expert_ids, "expert_ids", (torch.int32,), numel=T * topk)
+    else:
+        if top_k is None:
+            raise ValueError("routing=(offsets, perm) needs top_k")
+        topk = int(top_k)
+        T = routing[1].numel() // topk
+        _need(routing[0], "offsets", (torch.int32,), numel=num_experts + 1)
+        _need(routing[1], "perm", (torch.int32,), numel=T * topk)
+    if x_bf16 is not None:
+        _need(x_bf16, "x_bf16", (torch.bfloat16,), (T, K), T * K)
+    else:
+        _need(x_packed[0], "x codes", (torch.uint8,), numel=T * (K // 2))
+        _need(x_packed[1], "x sf", (torch.uint8,), numel=T * (K // 32))
+    dev = w_codes.device
+    P = T * topk
+    d = torch.empty((P, N), dtype=out_dtype, device=dev)
+    offs = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    perm = torch.empty(P, dtype=torch.int32, device=dev) if routing is None else routing[1]
+    keep = [expert_ids, x_bf16, w_codes, w_sf, d, perm, offs, *(routing or ()), *(x_packed or ())]
+    _same_device(*keep)
+    a = MxGroupedArgs(num_tokens=T, top_k=topk, num_experts=num_experts, N=N, K=K, w_codes=w_codes.data_ptr(),
+                      w_sf=w_sf.data_ptr(), out_dtype=_OUT[out_dtype], d=d.data_ptr(),
+                      expert_offsets_out=offs.data_ptr())
+    if routing is None:
+        a.expert_ids, a.perm_out = expert_ids.data_ptr(), perm.data_ptr()
+    else:
+        a.offsets_in, a.perm_in = routing[0].data_ptr(), routing[1].data_ptr()
+    if x_bf16 is not None:
+        a.x_bf16 = x_bf16.data_ptr()
+    else:
+        a.x_codes, a.x_sf = x_packed[0].data_ptr(), x_packed[1].data_ptr()
+    ws = _workspace(a, lib.nvfp4_mxfp4_grouped_workspace_bytes, dev)
+    call = Prepared(lib.nvfp4_mxfp4_grouped_gemm, a, (*keep, ws), "nvfp4_mxfp4_grouped_gemm")
+    call.workspace = ws
+    return call, (d, perm, offs)
+
+
+def nvfp4_mxfp4_grouped_gemm(expert_ids, x_bf16, w_codes, w_sf, N: int, K: int, num_experts: int, *,
+                             stream=None, **form):
+    """See prepare_mxfp4_grouped; returns (d, perm, offsets)."""
+    call, res = prepare_mxfp4_grouped(expert_ids, x_bf16, w_codes, w_sf, N, K, num_experts, **form)
+    _run(call, stream)
+    return res
+
+
+def prepare_mxfp4_moe_down(h, perm, expert_offsets, route_weights, w_codes, w_sf, N: int, K: int,
+                           num_experts: int, out=None) -> tuple[Prepared, torch.Tensor]:
+    """y [T, N] = sum_j route_weights[t, j] * (MXFP4 product of h's grouped row of
+    (t, j) with its expert): prepare_moe_down with MXFP4 experts."""
+    lib = load()
+    _mx_weight(lib, w_codes, w_sf, num_experts * N, K, "w")
+    T, k = route_weights.shape
+    _need(route_weights, "route_weights", (torch.float32,), numel=T * k)
+    _need(h, "h", (torch.bfloat16,), (T * k, K), T * k * K)
+    _need(perm, "perm", (torch.int32,), numel=T * k)
+    _need(expert_offsets, "expert_offsets", (torch.int32,), numel=num_experts + 1)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=h.device)
+    _need(out, "out", (torch.bfloat16,), (T, N), T * N)
+    keep = (h, perm, expert_offsets, route_weights, w_codes, w_sf, out)
+    _same_device(*keep)
+    a = MxMoeDownArgs(num_tokens=T, top_k=k, num_experts=num_experts, N=N, K=K, h=h.data_ptr(),
+                      perm=perm.data_ptr(), expert_offsets=expert_offsets.data_ptr(),
+                      route_weights=route_weights.data_ptr(), w_codes=w_codes.data_ptr(), w_sf=w_sf.data_ptr(),
+                      y=out.data_ptr())
+    ws = _workspace(a, lib.nvfp4_mxfp4_moe_down_workspace_bytes, h.device)
+    call = Prepared(lib.nvfp4_mxfp4_moe_down_combine, a, (*keep, ws), "nvfp4_mxfp4_moe_down_combine")
+    call.workspace = ws
+    return call, out
+
+
+def nvfp4_mxfp4_moe_down_combine(h, perm, expert_offsets, route_weights, w_codes, w_sf, N: int, K: int,
+                                 num_experts: int, out=None, stream=None) -> torch.Tensor:
+    """See prepare_mxfp4_moe_down."""
+    call, out = prepare_mxfp4_moe_down(h, perm, expert_offsets, route_weights, w_codes, w_sf, N, K,
+                                       num_experts, out)
+    _run(call, stream)
     return out

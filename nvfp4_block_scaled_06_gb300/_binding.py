@@ -31,10 +31,15 @@ EXPORTS = [
     "nvfp4_set_wait_timeout_ns", "nvfp4_version", "nvfp4_quantize_noalloc",
     "nvfp4_last_cuda_error", "nvfp4_dequantize", "nvfp4_dgrad", "nvfp4_dgrad_workspace_bytes",
     "nvfp4_wgrad", "nvfp4_wgrad_workspace_bytes", "nvfp4_moe_down_combine",
-    "nvfp4_moe_down_workspace_bytes",
+    "nvfp4_moe_down_workspace_bytes", "nvfp4_route_topk", "nvfp4_route_topk_backward",
+    "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_dequantize", "nvfp4_mxfp4_sf_bytes", "nvfp4_mxfp4_gemm",
+    "nvfp4_mxfp4_gemm_workspace_bytes", "nvfp4_mxfp4_dgrad", "nvfp4_mxfp4_dgrad_workspace_bytes",
+    "nvfp4_mxfp4_grouped_gemm", "nvfp4_mxfp4_grouped_workspace_bytes",
+    "nvfp4_mxfp4_moe_down_combine", "nvfp4_mxfp4_moe_down_workspace_bytes",
 ]
 
 DGRAD_DEQUANT_BF16, DGRAD_FP4_COLPACK = 0, 1
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 
 
 class QuantArgs(C.Structure):
@@ -150,6 +155,101 @@ class MoeDownArgs(C.Structure):
     ]
 
 
+class RouteTopkArgs(C.Structure):
+    _fields_ = [
+        ("num_tokens", C.c_int64), ("num_experts", C.c_int64), ("top_k", C.c_int64),
+        ("logits", C.c_void_p), ("ld", C.c_int64),
+        ("logits_dtype", C.c_int32), ("score", C.c_int32),
+        ("bias", C.c_void_p),
+        ("num_groups", C.c_int32), ("topk_groups", C.c_int32), ("group_top", C.c_int32),
+        ("renormalize", C.c_int32), ("scale", C.c_float),
+        ("expert_ids", C.c_void_p), ("route_weights", C.c_void_p),
+    ]
+
+
+class RouteTopkBackwardArgs(C.Structure):
+    _fields_ = [
+        ("num_tokens", C.c_int64), ("num_experts", C.c_int64), ("top_k", C.c_int64),
+        ("logits", C.c_void_p), ("ld", C.c_int64),
+        ("logits_dtype", C.c_int32), ("score", C.c_int32), ("renormalize", C.c_int32),
+        ("scale", C.c_float),
+        ("expert_ids", C.c_void_p), ("grad_weights", C.c_void_p),
+        ("grad_logits", C.c_void_p), ("ld_grad", C.c_int64),
+    ]
+
+
+class MxQuantArgs(C.Structure):
+    _fields_ = [
+        ("src", C.c_void_p),
+        ("batch", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+        ("ld", C.c_int64), ("batch_stride", C.c_int64),
+        ("sf_layout", C.c_int32),
+        ("codes", C.c_void_p), ("sf", C.c_void_p),
+    ]
+
+
+class MxDequantArgs(C.Structure):
+    _fields_ = [
+        ("codes", C.c_void_p), ("sf", C.c_void_p),
+        ("sf_layout", C.c_int32),
+        ("batch", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+        ("transpose", C.c_int32),
+        ("out", C.c_void_p), ("ldo", C.c_int64), ("out_batch_stride", C.c_int64),
+    ]
+
+
+class MxGemmArgs(C.Structure):
+    _fields_ = [
+        ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64),
+        ("a_codes", C.c_void_p), ("a_sf", C.c_void_p),
+        ("a_bf16", C.c_void_p), ("lda", C.c_int64),
+        ("b_codes", C.c_void_p), ("b_sf", C.c_void_p),
+        ("out_dtype", C.c_int32),
+        ("d", C.c_void_p), ("ldd", C.c_int64),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+        ("prof_begin", C.c_void_p), ("prof_end", C.c_void_p),
+    ]
+
+
+class MxDgradArgs(C.Structure):
+    _fields_ = [
+        ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64),
+        ("dy", C.c_void_p), ("lddy", C.c_int64),
+        ("w_codes", C.c_void_p), ("w_sf", C.c_void_p),
+        ("out_dtype", C.c_int32),
+        ("dx", C.c_void_p), ("lddx", C.c_int64),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+        ("prof_begin", C.c_void_p), ("prof_end", C.c_void_p),
+    ]
+
+
+class MxGroupedArgs(C.Structure):
+    _fields_ = [
+        ("num_tokens", C.c_int64), ("top_k", C.c_int64), ("num_experts", C.c_int64),
+        ("N", C.c_int64), ("K", C.c_int64),
+        ("expert_ids", C.c_void_p), ("offsets_in", C.c_void_p), ("perm_in", C.c_void_p),
+        ("x_bf16", C.c_void_p), ("x_codes", C.c_void_p), ("x_sf", C.c_void_p),
+        ("w_codes", C.c_void_p), ("w_sf", C.c_void_p),
+        ("out_dtype", C.c_int32),
+        ("d", C.c_void_p), ("perm_out", C.c_void_p), ("expert_offsets_out", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+        ("prof_begin", C.c_void_p), ("prof_end", C.c_void_p),
+    ]
+
+
+class MxMoeDownArgs(C.Structure):
+    _fields_ = [
+        ("num_tokens", C.c_int64), ("top_k", C.c_int64), ("num_experts", C.c_int64),
+        ("N", C.c_int64), ("K", C.c_int64),
+        ("h", C.c_void_p), ("perm", C.c_void_p), ("expert_offsets", C.c_void_p),
+        ("route_weights", C.c_void_p),
+        ("w_codes", C.c_void_p), ("w_sf", C.c_void_p),
+        ("y", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+        ("prof_begin", C.c_void_p), ("prof_end", C.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -174,13 +274,26 @@ def load(path: str | None = None):
                         ("nvfp4_lora_epilogue", "nvfp4_lora_workspace_bytes", LoraArgs),
                         ("nvfp4_dgrad", "nvfp4_dgrad_workspace_bytes", DgradArgs),
                         ("nvfp4_wgrad", "nvfp4_wgrad_workspace_bytes", WgradArgs),
-                        ("nvfp4_moe_down_combine", "nvfp4_moe_down_workspace_bytes", MoeDownArgs)]:
+                        ("nvfp4_moe_down_combine", "nvfp4_moe_down_workspace_bytes", MoeDownArgs),
+                        ("nvfp4_mxfp4_gemm", "nvfp4_mxfp4_gemm_workspace_bytes", MxGemmArgs),
+                        ("nvfp4_mxfp4_dgrad", "nvfp4_mxfp4_dgrad_workspace_bytes", MxDgradArgs),
+                        ("nvfp4_mxfp4_grouped_gemm", "nvfp4_mxfp4_grouped_workspace_bytes", MxGroupedArgs),
+                        ("nvfp4_mxfp4_moe_down_combine", "nvfp4_mxfp4_moe_down_workspace_bytes",
+                         MxMoeDownArgs)]:
         f = getattr(lib, fn)
         f.argtypes = [C.POINTER(st), vp]
         f.restype = C.c_int
         w = getattr(lib, wsq)
         w.argtypes = [C.POINTER(st)]
         w.restype = C.c_size_t
+    for fn, st in [("nvfp4_route_topk", RouteTopkArgs),
+                   ("nvfp4_route_topk_backward", RouteTopkBackwardArgs),
+                   ("nvfp4_mxfp4_quantize", MxQuantArgs), ("nvfp4_mxfp4_dequantize", MxDequantArgs)]:
+        f = getattr(lib, fn)
+        f.argtypes = [C.POINTER(st), vp]
+        f.restype = C.c_int
+    lib.nvfp4_mxfp4_sf_bytes.argtypes = [C.c_int64, C.c_int64, C.c_int32]
+    lib.nvfp4_mxfp4_sf_bytes.restype = C.c_size_t
     lib.nvfp4_dequantize.argtypes = [C.POINTER(DequantArgs), vp]
     lib.nvfp4_dequantize.restype = C.c_int
     lib.nvfp4_quantize_noalloc.argtypes = [C.POINTER(QuantArgs), vp]

@@ -611,6 +611,7 @@ struct GroupedProducts {
   __nv_bfloat16 *t;               // [prow_max][rank] T' scratch
   void *d;                        // [P][N], bf16 or fp32
   int out_fp32;
+  int mx = 0;                     // MXFP4 operands (no global scales, no LoRA)
   void *prof_begin, *prof_end;
 };
 
@@ -659,7 +660,8 @@ nvfp4_status run_grouped_products(const GroupedProducts &g, int *status, uint64_
   p.nk64 = (int)ceil_div(g.K, 64);
   p.a_sf = g.asf;
   p.b_sf = static_cast<const uint8_t *>(g.w_sf);
-  p.a_sf_katoms = pad_up(g.K / 16, 4) / 4;
+  p.mx = g.mx;
+  p.a_sf_katoms = pad_up(g.K / (g.mx ? 32 : 16), 4) / 4;
   p.b_sf_katoms = p.a_sf_katoms;
   p.b_sf_row_chunks = g.E * g.N / 128;
   p.g_a = g.g_a;
@@ -721,7 +723,7 @@ nvfp4_status run_grouped(const nvfp4_grouped_args *a, const GroupedPlan &pl, int
   }
   if (a->x_codes) {
     // activations already quantized per token row (linear scales) with x_global_scale
-    if (cudaError_t e_ = launch_gather_packed(a->x_codes, a->x_sf, pl.row_map, pl.prow_max, pl.nmt, a->K, pl.xq,
+    if (cudaError_t e_ = launch_gather_packed(a->x_codes, a->x_sf, pl.row_map, pl.prow_max, pl.nmt, a->K, 16, pl.xq,
                                               pl.xsf, sms, st, a->num_tokens, status);
         e_ != cudaSuccess)
       return cuda_status(e_);
@@ -777,7 +779,7 @@ nvfp4_status run_grouped(const nvfp4_grouped_args *a, const GroupedPlan &pl, int
     if (cudaError_t e_ = launch_amax(q, st); e_ != cudaSuccess) return cuda_status(e_);
   }
   if (cudaError_t e_ = launch_quant_rows(q, sms, st); e_ != cudaSuccess) return cuda_status(e_);
-  if (cudaError_t e_ = launch_gather_packed(pl.xq_tok, pl.xsf_tok, pl.row_map, pl.prow_max, pl.nmt, a->K, pl.xq,
+  if (cudaError_t e_ = launch_gather_packed(pl.xq_tok, pl.xsf_tok, pl.row_map, pl.prow_max, pl.nmt, a->K, 16, pl.xq,
                                             pl.xsf, sms, st, a->num_tokens, status);
       e_ != cudaSuccess)
     return cuda_status(e_);
@@ -1254,6 +1256,486 @@ nvfp4_status run_wgrad(const nvfp4_wgrad_args *a, const WgradPlan &pl, int sms, 
   return run_gemm(&g, gp, sms, st);
 }
 
+// --------------------------------------------------------- expert selection --
+nvfp4_status validate_route_sizes(int64_t T, int64_t E, int64_t k, const void *logits, int64_t ld, int32_t dtype,
+                                  int32_t score) {
+  if (!logits || T < 1 || E < 1 || k < 1 || ld < E) return NVFP4_ERR_INVALID_ARG;
+  if (dtype != NVFP4_OUT_BF16 && dtype != NVFP4_OUT_FP32) return NVFP4_ERR_INVALID_ARG;
+  if (score != NVFP4_SCORE_SIGMOID && score != NVFP4_SCORE_SOFTMAX) return NVFP4_ERR_INVALID_ARG;
+  if (E > 1024 || k > 32 || k > E || T > (1ll << 31)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(logits, dtype == NVFP4_OUT_FP32 ? 4 : 2)) return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status validate_route_topk(const nvfp4_route_topk_args *a) {
+  if (!a || !a->expert_ids || !a->route_weights) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status s = validate_route_sizes(a->num_tokens, a->num_experts, a->top_k, a->logits, a->ld,
+                                            a->logits_dtype, a->score);
+      s != NVFP4_OK)
+    return s;
+  if (a->num_groups > 1) {
+    if (a->topk_groups < 1 || a->topk_groups > a->num_groups || a->group_top < 1 || a->group_top > 2)
+      return NVFP4_ERR_INVALID_ARG;
+    if (a->num_groups > 32 || a->num_experts % a->num_groups != 0 ||
+        a->top_k > a->topk_groups * (a->num_experts / a->num_groups))
+      return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (!aligned(a->expert_ids, 4) || !aligned(a->route_weights, 4) || (a->bias && !aligned(a->bias, 4)))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status run_route_topk(const nvfp4_route_topk_args *a, int sms, cudaStream_t st) {
+  RouteTopkParams p{};
+  p.logits = a->logits;
+  p.tokens = a->num_tokens;
+  p.ld = a->ld;
+  p.num_experts = (int)a->num_experts;
+  p.top_k = (int)a->top_k;
+  p.bias = a->bias;
+  p.softmax = a->score == NVFP4_SCORE_SOFTMAX;
+  // all groups kept is no restriction
+  p.num_groups = a->num_groups > 1 && a->topk_groups < a->num_groups ? a->num_groups : 1;
+  p.topk_groups = a->topk_groups;
+  p.group_top = a->group_top;
+  p.group_size = p.num_experts / p.num_groups;
+  int lanes = 32;
+  while (lanes * p.num_groups > 32) lanes /= 2;
+  p.group_lanes = lanes;
+  p.group_magic = (uint32_t)(((1u << 22) + p.group_size - 1) / p.group_size);
+  p.index_mask = 1;
+  while ((int)p.index_mask + 1 < p.num_experts) p.index_mask = 2 * p.index_mask + 1;
+  p.rank_by_score = p.num_groups > 1 && a->group_top == 2;
+  p.renormalize = a->renormalize != 0;
+  p.need_row_sum = p.softmax && (a->bias || p.rank_by_score || !p.renormalize);
+  p.scale = a->scale;
+  p.expert_ids = a->expert_ids;
+  p.weights = a->route_weights;
+  return cuda_status(launch_route_topk(p, a->logits_dtype == NVFP4_OUT_BF16, sms, st));
+}
+
+nvfp4_status validate_route_topk_backward(const nvfp4_route_topk_backward_args *a) {
+  if (!a || !a->expert_ids || !a->grad_weights || !a->grad_logits || a->ld_grad < a->num_experts)
+    return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status s = validate_route_sizes(a->num_tokens, a->num_experts, a->top_k, a->logits, a->ld,
+                                            a->logits_dtype, a->score);
+      s != NVFP4_OK)
+    return s;
+  if (!aligned(a->expert_ids, 4) || !aligned(a->grad_weights, 4) ||
+      !aligned(a->grad_logits, a->logits_dtype == NVFP4_OUT_FP32 ? 4 : 2))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status run_route_topk_backward(const nvfp4_route_topk_backward_args *a, int sms, cudaStream_t st) {
+  RouteGradParams p{};
+  p.logits = a->logits;
+  p.tokens = a->num_tokens;
+  p.ld = a->ld;
+  p.ld_grad = a->ld_grad;
+  p.num_experts = (int)a->num_experts;
+  p.top_k = (int)a->top_k;
+  p.expert_ids = a->expert_ids;
+  p.grad_weights = a->grad_weights;
+  p.softmax = a->score == NVFP4_SCORE_SOFTMAX;
+  p.renormalize = a->renormalize != 0;
+  p.scale = a->scale;
+  p.grad_logits = a->grad_logits;
+  return cuda_status(launch_route_topk_backward(p, a->logits_dtype == NVFP4_OUT_BF16, sms, st));
+}
+
+// -------------------------------------------------------------------- MXFP4 --
+size_t mx_sf_swizzled_bytes(int64_t rows, int64_t cols) {
+  return (size_t)pad_up(rows, 128) * (size_t)pad_up(cols / 32, 4);
+}
+
+nvfp4_status validate_mx_quant(const nvfp4_mxfp4_quant_args *a) {
+  if (!a || !a->src || !a->codes || !a->sf) return NVFP4_ERR_INVALID_ARG;
+  if (a->batch < 1 || a->rows < 1 || a->cols < 1) return NVFP4_ERR_INVALID_ARG;
+  if (a->sf_layout != NVFP4_SF_LINEAR && a->sf_layout != NVFP4_SF_SWIZZLED) return NVFP4_ERR_INVALID_ARG;
+  if (a->ld < a->cols || (a->batch > 1 && a->batch_stride < (a->rows - 1) * a->ld + a->cols))
+    return NVFP4_ERR_INVALID_ARG;
+  if (a->cols % 32 != 0 || a->batch > 65535 || a->rows > (1ll << 31) || a->cols > (1ll << 31))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(a->src, 16) || !aligned(a->codes, 16) || !aligned(a->sf, 16) || a->ld % 8 != 0 ||
+      (a->batch > 1 && a->batch_stride % 8 != 0))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status validate_mx_dequant(const nvfp4_mxfp4_dequant_args *a) {
+  if (!a || !a->codes || !a->sf || !a->out) return NVFP4_ERR_INVALID_ARG;
+  if (a->batch < 1 || a->rows < 1 || a->cols < 1) return NVFP4_ERR_INVALID_ARG;
+  if (a->sf_layout != NVFP4_SF_LINEAR && a->sf_layout != NVFP4_SF_SWIZZLED) return NVFP4_ERR_INVALID_ARG;
+  const int64_t orows = a->transpose ? a->cols : a->rows, ocols = a->transpose ? a->rows : a->cols;
+  if (a->ldo < ocols || (a->batch > 1 && a->out_batch_stride < (orows - 1) * a->ldo + ocols))
+    return NVFP4_ERR_INVALID_ARG;
+  if (a->cols % 32 != 0 || a->batch > 65535 || a->rows > (1ll << 31) || a->cols > (1ll << 31))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t step = a->transpose ? 2 : 8;   // bf16 pairs, or 16-byte vectors
+  if (!aligned(a->codes, 16) || !aligned(a->sf, 16) || !aligned(a->out, 16) || a->ldo % step != 0 ||
+      (a->batch > 1 && a->out_batch_stride % step != 0))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+struct MxGemmPlan {
+  size_t ws = 0;
+  uint8_t *aq_codes = nullptr, *aq_sf = nullptr;   // in-call quantization of A
+  int bn = 256, ksplit = 1;
+  bool pair = false, skinny = false;
+  float *partial = nullptr;                        // split-K partials [ksplit][M][N]
+};
+
+// The kernels of nvfp4_gemm: the operand-swapped one up to 32 rows (whether A
+// comes packed or not), then the 1-SM and the pair kernel by the same rules.
+void plan_mx_gemm(const nvfp4_mxfp4_gemm_args *a, MxGemmPlan *pl) {
+  Carve c(a->workspace);
+  if (a->a_bf16) {
+    pl->aq_codes = c.take<uint8_t>((size_t)pad_up(a->M, 128) * a->K / 2);
+    pl->aq_sf = c.take<uint8_t>(mx_sf_swizzled_bytes(a->M, a->K));
+  }
+  const int sms = plan_sms();
+  pl->bn = pick_bn(a->M, a->N, sms);
+  pl->skinny = a->M <= 32;
+  pl->ksplit = pl->skinny ? pick_skinny_ksplit(a->N, a->K, sms) : pick_ksplit(a->M, a->N, a->K, pl->bn, sms, false);
+  pl->pair = !pl->skinny && use_pair(a->M, pl->ksplit);
+  if (pl->ksplit > 1) pl->partial = c.take<float>((size_t)pl->ksplit * a->M * a->N * 4);
+  pl->ws = c.off;
+}
+
+nvfp4_status validate_mx_gemm(const nvfp4_mxfp4_gemm_args *a) {
+  if (!a || !a->b_codes || !a->b_sf || !a->d) return NVFP4_ERR_INVALID_ARG;
+  if (a->M < 1 || a->N < 1 || a->K < 1 || a->ldd < a->N) return NVFP4_ERR_INVALID_ARG;
+  if (a->out_dtype != NVFP4_OUT_BF16 && a->out_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_INVALID_ARG;
+  // one form of A: bf16 rows, or codes with their scales
+  const bool packed = a->a_codes || a->a_sf;
+  if (packed == (a->a_bf16 != nullptr) || (packed && (!a->a_codes || !a->a_sf))) return NVFP4_ERR_INVALID_ARG;
+  if (a->a_bf16 && a->lda < a->K) return NVFP4_ERR_INVALID_ARG;
+  if (a->K % 32 != 0 || a->M > (1ll << 31) - 256 || a->N > (1ll << 31) - 256 || a->K > (1ll << 24))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t dalign = a->out_dtype == NVFP4_OUT_BF16 ? 8 : 4;
+  if (!aligned(a->d, 16) || a->ldd % dalign != 0 || !aligned(a->b_codes, 16) || !aligned(a->b_sf, 16))
+    return NVFP4_ERR_ALIGNMENT;
+  if (packed && (!aligned(a->a_codes, 16) || !aligned(a->a_sf, 16))) return NVFP4_ERR_ALIGNMENT;
+  if (a->a_bf16 && (!aligned(a->a_bf16, 16) || a->lda % 8 != 0)) return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status run_mx_gemm(const nvfp4_mxfp4_gemm_args *a, const MxGemmPlan &pl, int sms, cudaStream_t st) {
+  const uint64_t tmo = g_timeout_ns.load();
+  const uint8_t *a_codes = a->a_codes, *a_sf = a->a_sf;
+  if (a->a_bf16) {
+    MxQuantParams q{};
+    q.src = static_cast<const __nv_bfloat16 *>(a->a_bf16);
+    q.rows = q.dst_rows = a->M;
+    q.cols = a->K;
+    q.ld = a->lda;
+    q.batch = 1;
+    q.codes = pl.aq_codes;
+    q.sf = pl.aq_sf;
+    q.sf_swizzled = 1;
+    if (cudaError_t e_ = launch_mx_quant(q, sms, st); e_ != cudaSuccess) return cuda_status(e_);
+    a_codes = pl.aq_codes;
+    a_sf = pl.aq_sf;
+  }
+  // A quantized in the call spans the padded rows of its buffer: whatever codes
+  // they hold, with scale byte 0, stay in accumulator rows that are not stored
+  const int64_t a_rows = a->a_bf16 ? pad_up(a->M, 128) : a->M;
+  const int b_box = pl.pair || pl.skinny ? 128 : pl.bn;
+  GemmMaps maps;
+  if (!map2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, a->K / 2, a_rows, a->K / 2, 128, pl.skinny ? 32 : 128) ||
+      !map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, b_box))
+    return NVFP4_ERR_CUDA;
+  maps.t = maps.a;
+  maps.lb = maps.b;
+  GemmParams p{};
+  p.M = a->M;
+  p.N = a->N;
+  p.K = a->K;
+  p.num_kt = (int)ceil_div(a->K, 256);
+  p.nk64 = (int)ceil_div(a->K, 64);
+  p.mx = 1;
+  p.a_sf = a_sf;
+  p.b_sf = a->b_sf;
+  p.a_sf_katoms = pad_up(a->K / 32, 4) / 4;
+  p.b_sf_katoms = p.a_sf_katoms;
+  p.b_sf_row_chunks = ceil_div(a->N, 128);
+  p.d = a->d;
+  p.ldd = a->ldd;
+  p.out_fp32 = a->out_dtype == NVFP4_OUT_FP32;
+  p.tiles_m = (int)ceil_div(a->M, 128);
+  p.tiles_n = (int)ceil_div(a->N, pl.skinny ? 128 : pl.pair ? 256 : pl.bn);
+  p.ksplit = pl.ksplit;
+  p.partial = pl.partial;
+  p.status = static_cast<int *>(a->workspace);
+  p.timeout_ns = tmo;
+  p.stall_probe = tmo == 0;
+  if (pl.pair) {
+    map_pair_d(&maps, &p);
+    // 64-row B boxes for the half units of a short last wave
+    maps.has_half = map2d(&maps.bh, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, 64);
+    maps.lbh = maps.bh;
+  }
+  if (cudaError_t e_ = mark(a->prof_begin, st); e_ != cudaSuccess) return cuda_status(e_);
+  cudaError_t e = pl.skinny ? launch_gemm_fp4_skinny(p, maps.a, maps.b, sms, st)
+                  : pl.pair ? launch_gemm_fp4_pair(p, maps, sms, st)
+                            : launch_gemm_fp4(p, maps, pl.bn, sms, st);
+  if (e == cudaSuccess && pl.ksplit > 1) e = launch_splitk_reduce(p, sms, st);
+  if (e == cudaSuccess) e = mark(a->prof_end, st);
+  return cuda_status(e);
+}
+
+nvfp4_status validate_mx_dgrad(const nvfp4_mxfp4_dgrad_args *a) {
+  if (!a || !a->dy || !a->dx || !a->w_codes || !a->w_sf) return NVFP4_ERR_INVALID_ARG;
+  if (a->M < 1 || a->N < 1 || a->K < 1 || a->lddy < a->N || a->lddx < a->K) return NVFP4_ERR_INVALID_ARG;
+  if (a->out_dtype != NVFP4_OUT_BF16 && a->out_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_INVALID_ARG;
+  if (a->K % 32 != 0 || a->M > (1ll << 31) - 256 || a->N > (1ll << 24) || a->K > (1ll << 31) - 256)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t dalign = a->out_dtype == NVFP4_OUT_BF16 ? 8 : 4;
+  if (!aligned(a->dy, 16) || a->lddy % 8 != 0 || !aligned(a->dx, 16) || a->lddx % dalign != 0 ||
+      !aligned(a->w_codes, 16) || !aligned(a->w_sf, 16))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+size_t plan_mx_dgrad(const nvfp4_mxfp4_dgrad_args *a, void *workspace, __nv_bfloat16 **wt) {
+  Carve c(workspace);
+  *wt = c.take<__nv_bfloat16>((size_t)a->K * pad_up(a->N, 8) * 2);   // W^T in bf16, rows on 16 bytes
+  return c.off;
+}
+
+nvfp4_status run_mx_dgrad(const nvfp4_mxfp4_dgrad_args *a, int sms, cudaStream_t st) {
+  __nv_bfloat16 *wt = nullptr;
+  plan_mx_dgrad(a, a->workspace, &wt);
+  const int64_t ldw = pad_up(a->N, 8);
+  if (cudaError_t e_ = launch_mx_dequant(a->w_codes, a->w_sf, 1, 1, a->N, a->K, 0, 1, wt, ldw, 0, sms, st);
+      e_ != cudaSuccess)
+    return cuda_status(e_);
+  return run_bf16_gemm(a->M, a->K, a->N, a->dy, a->lddy, wt, ldw, a->dx, a->lddx, a->out_dtype == NVFP4_OUT_FP32,
+                       static_cast<int *>(a->workspace), a->prof_begin, a->prof_end, sms, st);
+}
+
+struct MxGroupedPlan {
+  size_t ws = 0;
+  int nchunks = 0;
+  int64_t prow_max = 0;
+  int32_t *hist = nullptr, *counts = nullptr, *offsets = nullptr, *poffsets = nullptr;
+  int32_t *row_map = nullptr, *nmt = nullptr;
+  GroupTile *gtiles = nullptr;
+  uint8_t *xq = nullptr, *xsf = nullptr;          // grouped, padded A operand
+  uint8_t *xq_tok = nullptr, *xsf_tok = nullptr;  // X quantized once per token (linear scales)
+};
+
+void plan_mx_grouped(const nvfp4_mxfp4_grouped_args *a, MxGroupedPlan *pl) {
+  Carve c(a->workspace);
+  const int64_t P = a->num_tokens * a->top_k;
+  pl->nchunks = (int)ceil_div(P, 1024);
+  pl->prow_max = pad_up(P + a->num_experts * 127, 128);
+  if (a->expert_ids) {
+    pl->hist = c.take<int32_t>((size_t)pl->nchunks * a->num_experts * 4);
+    pl->counts = c.take<int32_t>((size_t)a->num_experts * 4);
+  }
+  pl->offsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
+  pl->poffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
+  pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
+  pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
+  pl->nmt = c.take<int32_t>(4);
+  if (!a->x_codes) {
+    pl->xq_tok = c.take<uint8_t>((size_t)a->num_tokens * a->K / 2);
+    pl->xsf_tok = c.take<uint8_t>((size_t)a->num_tokens * (a->K / 32));
+  }
+  pl->xq = c.take<uint8_t>((size_t)pl->prow_max * a->K / 2);
+  pl->xsf = c.take<uint8_t>(mx_sf_swizzled_bytes(pl->prow_max, a->K));
+  pl->ws = c.off;
+}
+
+// The sizes that both routed MXFP4 calls take.
+nvfp4_status validate_mx_experts(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+  if (T < 1 || k < 1 || E < 1 || N < 1 || K < 1) return NVFP4_ERR_INVALID_ARG;
+  if (E > 1024 || k > E || N % 256 != 0 || K % 32 != 0 || K > (1ll << 24)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (T > (1ll << 30) || T * k > (1ll << 30) || E * N > (1ll << 31) - 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  return NVFP4_OK;
+}
+
+nvfp4_status validate_mx_grouped(const nvfp4_mxfp4_grouped_args *a) {
+  if (!a || !a->w_codes || !a->w_sf || !a->d) return NVFP4_ERR_INVALID_ARG;
+  const bool ids = a->expert_ids != nullptr, given = a->offsets_in && a->perm_in;
+  if (ids == given || (!given && (a->offsets_in || a->perm_in))) return NVFP4_ERR_INVALID_ARG;
+  if (ids && !a->perm_out) return NVFP4_ERR_INVALID_ARG;
+  const bool packed = a->x_codes || a->x_sf;
+  if (packed == (a->x_bf16 != nullptr) || (packed && (!a->x_codes || !a->x_sf))) return NVFP4_ERR_INVALID_ARG;
+  if (a->out_dtype != NVFP4_OUT_BF16 && a->out_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status s = validate_mx_experts(a->num_tokens, a->top_k, a->num_experts, a->N, a->K); s != NVFP4_OK)
+    return s;
+  const void *ptrs[] = {a->x_bf16, a->w_codes, a->w_sf, a->d, a->x_codes, a->x_sf, a->offsets_in, a->perm_in};
+  for (const void *q : ptrs)
+    if (q && !aligned(q, 16)) return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPlan &pl, int sms, cudaStream_t st) {
+  int *status = static_cast<int *>(a->workspace);
+  const int64_t P = a->num_tokens * a->top_k;
+  if (a->expert_ids) {
+    RouteParams r{};
+    r.expert_ids = a->expert_ids;
+    r.pairs = P;
+    r.top_k = (int)a->top_k;
+    r.num_experts = (int)a->num_experts;
+    r.chunk = 1024;
+    r.nchunks = pl.nchunks;
+    r.hist = pl.hist;
+    r.counts = pl.counts;
+    r.offsets = pl.offsets;
+    r.poffsets = pl.poffsets;
+    r.perm = a->perm_out;
+    r.row_map = pl.row_map;
+    r.padded_rows_max = pl.prow_max;
+    r.gtiles = pl.gtiles;
+    r.gnum_mtiles = pl.nmt;
+    r.offsets_out = a->expert_offsets_out;
+    r.status = status;
+    if (cudaError_t e_ = launch_route(r, st); e_ != cudaSuccess) return cuda_status(e_);
+  } else {
+    // the caller's grouping: padded layout from its offsets, row_map -> token through its perm
+    if (cudaError_t e_ = launch_layout_from_offsets(a->offsets_in, (int)a->num_experts, P, pl.prow_max, pl.offsets,
+                                                    pl.poffsets, pl.gtiles, pl.nmt, pl.row_map, a->perm_in,
+                                                    (int)a->top_k, sms, st, status);
+        e_ != cudaSuccess)
+      return cuda_status(e_);
+    if (a->perm_out && a->perm_out != a->perm_in)
+      if (cudaError_t e_ = cudaMemcpyAsync(a->perm_out, a->perm_in, (size_t)P * 4, cudaMemcpyDeviceToDevice, st);
+          e_ != cudaSuccess)
+        return cuda_status(e_);
+    if (a->expert_offsets_out)
+      if (cudaError_t e_ = cudaMemcpyAsync(a->expert_offsets_out, pl.offsets, (size_t)(a->num_experts + 1) * 4,
+                                           cudaMemcpyDeviceToDevice, st);
+          e_ != cudaSuccess)
+        return cuda_status(e_);
+  }
+  const uint8_t *codes = a->x_codes, *sf = a->x_sf;
+  if (a->x_bf16) {
+    // every token row is quantized once, then its codes and scales are copied
+    // to each of its top_k rows of the grouped operand
+    MxQuantParams q{};
+    q.src = static_cast<const __nv_bfloat16 *>(a->x_bf16);
+    q.rows = q.dst_rows = a->num_tokens;
+    q.cols = q.ld = a->K;
+    q.batch = 1;
+    q.codes = pl.xq_tok;
+    q.sf = pl.xsf_tok;
+    q.status = status;
+    if (cudaError_t e_ = launch_mx_quant(q, sms, st); e_ != cudaSuccess) return cuda_status(e_);
+    codes = pl.xq_tok;
+    sf = pl.xsf_tok;
+  }
+  if (cudaError_t e_ = launch_gather_packed(codes, sf, pl.row_map, pl.prow_max, pl.nmt, a->K, 32, pl.xq, pl.xsf, sms,
+                                            st, a->num_tokens, status);
+      e_ != cudaSuccess)
+    return cuda_status(e_);
+  GroupedProducts gp{};
+  gp.E = a->num_experts;
+  gp.N = a->N;
+  gp.K = a->K;
+  gp.prow_max = pl.prow_max;
+  gp.out_rows = P;
+  gp.aq = pl.xq;
+  gp.asf = pl.xsf;
+  gp.row_map = pl.row_map;
+  gp.gtiles = pl.gtiles;
+  gp.nmt = pl.nmt;
+  gp.w_codes = a->w_codes;
+  gp.w_sf = a->w_sf;
+  gp.d = a->d;
+  gp.out_fp32 = a->out_dtype == NVFP4_OUT_FP32;
+  gp.mx = 1;
+  gp.prof_begin = a->prof_begin;
+  gp.prof_end = a->prof_end;
+  return run_grouped_products(gp, status, g_timeout_ns.load(), sms, st);
+}
+
+struct MxMoeDownPlan {
+  size_t ws = 0;
+  int64_t prow_max = 0;
+  int32_t *goffsets = nullptr, *poffsets = nullptr, *row_map = nullptr, *nmt = nullptr, *inv = nullptr;
+  GroupTile *gtiles = nullptr;
+  uint8_t *hq = nullptr, *hsf = nullptr;
+  __nv_bfloat16 *d = nullptr;
+};
+
+void plan_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, MxMoeDownPlan *pl) {
+  Carve c(a->workspace);
+  const int64_t P = a->num_tokens * a->top_k;
+  pl->prow_max = pad_up(P + a->num_experts * 127, 128);
+  pl->goffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
+  pl->poffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
+  pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
+  pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
+  pl->nmt = c.take<int32_t>(4);
+  pl->inv = c.take<int32_t>((size_t)P * 4);
+  pl->hq = c.take<uint8_t>((size_t)pl->prow_max * a->K / 2);
+  pl->hsf = c.take<uint8_t>(mx_sf_swizzled_bytes(pl->prow_max, a->K));
+  pl->d = c.take<__nv_bfloat16>((size_t)P * a->N * 2);
+  pl->ws = c.off;
+}
+
+nvfp4_status validate_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a) {
+  if (!a || !a->h || !a->perm || !a->expert_offsets || !a->route_weights || !a->w_codes || !a->w_sf || !a->y)
+    return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status s = validate_mx_experts(a->num_tokens, a->top_k, a->num_experts, a->N, a->K); s != NVFP4_OK)
+    return s;
+  if (!aligned(a->h, 16) || !aligned(a->w_codes, 16) || !aligned(a->w_sf, 16) || !aligned(a->y, 16))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDownPlan &pl, int sms, cudaStream_t st) {
+  int *status = static_cast<int *>(a->workspace);
+  const int64_t P = a->num_tokens * a->top_k;
+  if (cudaError_t e_ = launch_layout_from_offsets(a->expert_offsets, (int)a->num_experts, P, pl.prow_max,
+                                                  pl.goffsets, pl.poffsets, pl.gtiles, pl.nmt, pl.row_map,
+                                                  nullptr, 0, sms, st, status);
+      e_ != cudaSuccess)
+    return cuda_status(e_);
+  // h is quantized straight into the padded layout: padded row r takes grouped row row_map[r]
+  MxQuantParams q{};
+  q.src = static_cast<const __nv_bfloat16 *>(a->h);
+  q.rows = P;
+  q.cols = q.ld = a->K;
+  q.batch = 1;
+  q.codes = pl.hq;
+  q.sf = pl.hsf;
+  q.sf_swizzled = 1;
+  q.dst_rows = pl.prow_max;
+  q.row_map = pl.row_map;
+  q.num_mtiles = pl.nmt;   // rows past the routed layout are never read
+  q.status = status;
+  if (cudaError_t e_ = launch_mx_quant(q, sms, st); e_ != cudaSuccess) return cuda_status(e_);
+  GroupedProducts gp{};
+  gp.E = a->num_experts;
+  gp.N = a->N;
+  gp.K = a->K;
+  gp.prow_max = pl.prow_max;
+  gp.out_rows = P;
+  gp.aq = pl.hq;
+  gp.asf = pl.hsf;
+  gp.row_map = pl.row_map;
+  gp.gtiles = pl.gtiles;
+  gp.nmt = pl.nmt;
+  gp.w_codes = a->w_codes;
+  gp.w_sf = a->w_sf;
+  gp.d = pl.d;
+  gp.mx = 1;
+  gp.prof_begin = a->prof_begin;
+  gp.prof_end = a->prof_end;
+  nvfp4_status s = run_grouped_products(gp, status, g_timeout_ns.load(), sms, st);
+  if (s != NVFP4_OK) return s;
+  return cuda_status(launch_moe_combine(pl.d, a->perm, pl.inv, a->route_weights, a->num_tokens,
+                                        (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
+                                        status));
+}
+
 }  // namespace
 
 namespace nvfp4 {
@@ -1519,6 +2001,135 @@ nvfp4_status nvfp4_moe_down_combine(const nvfp4_moe_down_args *a, nvfp4_stream s
   plan_moe_down(a, &pl);
   if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.ws)) != NVFP4_OK) return s;
   return run_moe_down(a, pl, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_route_topk(const nvfp4_route_topk_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_route_topk(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  return run_route_topk(a, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_route_topk_backward(const nvfp4_route_topk_backward_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_route_topk_backward(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  return run_route_topk_backward(a, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t nvfp4_mxfp4_sf_bytes(int64_t rows, int64_t cols, int32_t sf_layout) {
+  if (rows < 0 || cols < 0) return 0;
+  return sf_layout == NVFP4_SF_SWIZZLED ? mx_sf_swizzled_bytes(rows, cols) : (size_t)rows * (size_t)(cols / 32);
+}
+
+nvfp4_status nvfp4_mxfp4_quantize(const nvfp4_mxfp4_quant_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_mx_quant(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  MxQuantParams q{};
+  q.src = static_cast<const __nv_bfloat16 *>(a->src);
+  q.rows = q.dst_rows = a->rows;
+  q.cols = a->cols;
+  q.ld = a->ld;
+  q.bstride = a->batch > 1 ? a->batch_stride : 0;
+  q.batch = a->batch;
+  q.codes = a->codes;
+  q.sf = a->sf;
+  q.codes_bstride = (int64_t)nvfp4_codes_bytes(a->rows, a->cols);
+  q.sf_bstride = (int64_t)nvfp4_mxfp4_sf_bytes(a->rows, a->cols, a->sf_layout);
+  q.sf_swizzled = a->sf_layout == NVFP4_SF_SWIZZLED;
+  return cuda_status(launch_mx_quant(q, d.sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_mxfp4_dequantize(const nvfp4_mxfp4_dequant_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_mx_dequant(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  return cuda_status(launch_mx_dequant(a->codes, a->sf, a->sf_layout == NVFP4_SF_SWIZZLED, a->batch, a->rows, a->cols,
+                                       (int64_t)nvfp4_mxfp4_sf_bytes(a->rows, a->cols, a->sf_layout), a->transpose,
+                                       static_cast<__nv_bfloat16 *>(a->out), a->ldo,
+                                       a->batch > 1 ? a->out_batch_stride : 0, d.sms,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_mxfp4_gemm_workspace_bytes(const nvfp4_mxfp4_gemm_args *a) {
+  if (!a) return 0;
+  nvfp4_mxfp4_gemm_args c = *a;
+  c.workspace = nullptr;
+  MxGemmPlan pl;
+  plan_mx_gemm(&c, &pl);
+  return pl.ws;
+}
+
+nvfp4_status nvfp4_mxfp4_gemm(const nvfp4_mxfp4_gemm_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_mx_gemm(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  MxGemmPlan pl;
+  plan_mx_gemm(a, &pl);
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.ws)) != NVFP4_OK) return s;
+  return run_mx_gemm(a, pl, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t nvfp4_mxfp4_dgrad_workspace_bytes(const nvfp4_mxfp4_dgrad_args *a) {
+  if (!a) return 0;
+  __nv_bfloat16 *wt;
+  return plan_mx_dgrad(a, nullptr, &wt);
+}
+
+nvfp4_status nvfp4_mxfp4_dgrad(const nvfp4_mxfp4_dgrad_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_mx_dgrad(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, nvfp4_mxfp4_dgrad_workspace_bytes(a))) != NVFP4_OK)
+    return s;
+  return run_mx_dgrad(a, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t nvfp4_mxfp4_grouped_workspace_bytes(const nvfp4_mxfp4_grouped_args *a) {
+  if (!a) return 0;
+  nvfp4_mxfp4_grouped_args c = *a;
+  c.workspace = nullptr;
+  MxGroupedPlan pl;
+  plan_mx_grouped(&c, &pl);
+  return pl.ws;
+}
+
+nvfp4_status nvfp4_mxfp4_grouped_gemm(const nvfp4_mxfp4_grouped_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_mx_grouped(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  MxGroupedPlan pl;
+  plan_mx_grouped(a, &pl);
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.ws)) != NVFP4_OK) return s;
+  return run_mx_grouped(a, pl, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t nvfp4_mxfp4_moe_down_workspace_bytes(const nvfp4_mxfp4_moe_down_args *a) {
+  if (!a) return 0;
+  nvfp4_mxfp4_moe_down_args c = *a;
+  c.workspace = nullptr;
+  MxMoeDownPlan pl;
+  plan_mx_moe_down(&c, &pl);
+  return pl.ws;
+}
+
+nvfp4_status nvfp4_mxfp4_moe_down_combine(const nvfp4_mxfp4_moe_down_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_mx_moe_down(a);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  MxMoeDownPlan pl;
+  plan_mx_moe_down(a, &pl);
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.ws)) != NVFP4_OK) return s;
+  return run_mx_moe_down(a, pl, d.sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

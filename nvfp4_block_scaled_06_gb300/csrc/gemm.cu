@@ -117,13 +117,18 @@ __device__ __forceinline__ void signal_abort(volatile int *abort_flag, int *stat
   record_timeout(status);
 }
 
-template <int BN>
+// MX: the operands are MXFP4 (one E8M0 scale per 32 elements).  A 128x4 scale
+// atom then covers 128 elements of K, so a stage has two atoms per 128 rows
+// instead of four, and the MMA (kind::mxf4 scale_vec::2X) of K step j takes
+// half (j & 1) of atom j / 2; everything else is the same.
+template <int BN, bool MX>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmLB,
                const GemmParams p) {
   using C = GemmCfg<BN>;
   constexpr int S = C::kStages;
+  constexpr int kAtoms = MX ? 2 : 4;       // scale atoms of a full stage, per 128 rows
 #ifdef NVFP4_WAIT_STATS
   const long long kernel_t0 = clock64();
 #endif
@@ -202,8 +207,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int c = 0; c < C::kSfbChunks; ++c)
           if (chunk0 + c < p.b_sf_row_chunks) chunks = c + 1;
         const int a_row = (int)ti.a_row0, b_row = (int)ti.b_row0;
-        const uint8_t *sfa_src = p.a_sf + 512 * ((ti.a_row0 >> 7) * p.a_sf_katoms + (int64_t)kt0 * 4);
-        const uint8_t *sfb_src = p.b_sf + 512 * (chunk0 * p.b_sf_katoms + (int64_t)kt0 * 4);
+        const uint8_t *sfa_src = p.a_sf + 512 * ((ti.a_row0 >> 7) * p.a_sf_katoms + (int64_t)kt0 * kAtoms);
+        const uint8_t *sfb_src = p.b_sf + 512 * (chunk0 * p.b_sf_katoms + (int64_t)kt0 * kAtoms);
         const int64_t sfb_chunk_stride = 512 * p.b_sf_katoms;
         const int nsteps = (kt1 - kt0) + p.lora_steps;
         for (int i = 0; i < nsteps; ++i) {
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t a_dst = a_base + stage * C::kABytes, b_dst = b_base + stage * C::kBBytes;
           if (kt < kt1) {
             const int nk = kt == p.num_kt - 1 ? last_nk : 4;
-            const uint32_t sfb = nk * 512;
+            const uint32_t sfb = (MX ? (nk + 1) / 2 : nk) * 512;
             mbar_arrive_expect_tx_u(fb, C::kABytes + C::kBBytes + sfb * (1 + chunks));
             tma_load_2d_u(a_dst, &tmA, fb, kt * 128, a_row);
             tma_load_2d_u(b_dst, &tmB, fb, kt * 128, b_row);
@@ -228,8 +233,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             bulk_load_u(sfb_base + stage * C::kSfbBytes, sfb_src, sfb, fb);
             if (C::kSfbChunks > 1 && chunks > 1)
               bulk_load_u(sfb_base + stage * C::kSfbBytes + 2048, sfb_src + sfb_chunk_stride, sfb, fb);
-            sfa_src += 2048;
-            sfb_src += 2048;
+            sfa_src += 512 * kAtoms;
+            sfb_src += 512 * kAtoms;
           } else {
             const int ls = kt - kt1;
             mbar_arrive_expect_tx_u(fb, C::kABytes + C::kBBytes);
@@ -251,7 +256,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue --
     if (lane == 0) {
-      const uint32_t idesc = idesc_nvfp4(kBM, BN);
+      const uint32_t idesc = MX ? idesc_mxfp4(kBM, BN, 0) : idesc_nvfp4(kBM, BN);
+      const uint32_t idesc_hi = idesc_mxfp4(kBM, BN, 2);   // MX: the upper half of an atom
       const uint32_t idesc_l = idesc_bf16(kBM, BN);
       // stage-0 descriptors; a stage adds its byte offset / 16 to the address field
       const uint64_t adesc0 = sdesc_k_sw128(sA), bdesc0 = sdesc_k_sw128(sB);
@@ -301,8 +307,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               if (j < nk) {
-                tc_mma_nvfp4(tmem, adesc + 2 * j, bdesc + 2 * j, idesc, sfa_col + 4 * j,
-                             sfb_col + j * C::kSfbColsPerK + sfb_lane_col, accumulate);
+                if constexpr (MX)
+                  tc_mma_mxfp4(tmem, adesc + 2 * j, bdesc + 2 * j, j & 1 ? idesc_hi : idesc, sfa_col + 4 * (j >> 1),
+                               sfb_col + (j >> 1) * C::kSfbColsPerK + sfb_lane_col, accumulate);
+                else
+                  tc_mma_nvfp4(tmem, adesc + 2 * j, bdesc + 2 * j, idesc, sfa_col + 4 * j,
+                               sfb_col + j * C::kSfbColsPerK + sfb_lane_col, accumulate);
                 accumulate = 1;
               }
             }
@@ -355,17 +365,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint32_t v[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 w = fa[32 * j];              // atom j, line `lane`
+            const uint4 w = fa[32 * (j % kAtoms)];   // atom j, line `lane` (MX: columns 8..15 are not read)
             v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
           }
           tmem_st_32x32b_x16(tq + stage * C::kSfColsPerStage, v);
 #pragma unroll
-          for (int h = 0; h < C::kSfbChunks; ++h) {
+          for (int h = 0; h < (MX ? 1 : C::kSfbChunks); ++h) {
             // columns 16 + 16h .. : k-steps 2h', 2h'+1 for BN=256 (8 columns per k-step)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const int col = 16 * h + 4 * t;        // column offset inside the B region
-              const int j = col / C::kSfbColsPerK, c = (col % C::kSfbColsPerK) / 4;
+              const int j = col / C::kSfbColsPerK % kAtoms, c = (col % C::kSfbColsPerK) / 4;
               const uint4 w = fb[128 * c + 32 * j];  // chunk c (2048 B), atom j (512 B)
               v[4 * t] = w.x; v[4 * t + 1] = w.y; v[4 * t + 2] = w.z; v[4 * t + 3] = w.w;
             }
@@ -949,10 +959,10 @@ cudaError_t launch_splitk_reduce(const GemmParams &p, int num_sms, cudaStream_t 
 
 // ----------------------------------------------------------------- launch --
 
-template <int BN>
+template <int BN, bool MX>
 static cudaError_t launch_bn(const GemmParams &p, const GemmMaps &m, int num_sms, cudaStream_t st) {
   using C = GemmCfg<BN>;
-  if (cudaError_t e = ensure_dynamic_smem((const void *)k_gemm_fp4<BN>, C::kSmemBytes); e != cudaSuccess) return e;
+  if (cudaError_t e = ensure_dynamic_smem((const void *)k_gemm_fp4<BN, MX>, C::kSmemBytes); e != cudaSuccess) return e;
   int64_t tiles = (int64_t)p.tiles_n * (p.gtiles ? 0 : p.tiles_m) * std::max(1, p.ksplit);
   int grid = num_sms;
 #ifdef NVFP4_WAIT_STATS
@@ -960,14 +970,14 @@ static cudaError_t launch_bn(const GemmParams &p, const GemmMaps &m, int num_sms
 #endif
   if (!p.gtiles) grid = (int)std::min<int64_t>(tiles, grid);
   if (grid <= 0) return cudaSuccess;
-  return launch_pdl(k_gemm_fp4<BN>, dim3(grid), dim3(kGemmThreads), C::kSmemBytes, st, m.a, m.b, m.t, m.lb, p);
+  return launch_pdl(k_gemm_fp4<BN, MX>, dim3(grid), dim3(kGemmThreads), C::kSmemBytes, st, m.a, m.b, m.t, m.lb, p);
 }
 
 cudaError_t launch_gemm_fp4(const GemmParams &p, const GemmMaps &m, int bn, int num_sms,
                             cudaStream_t st) {
   switch (bn) {
-    case 256: return launch_bn<256>(p, m, num_sms, st);
-    case 128: return launch_bn<128>(p, m, num_sms, st);
+    case 256: return p.mx ? launch_bn<256, true>(p, m, num_sms, st) : launch_bn<256, false>(p, m, num_sms, st);
+    case 128: return p.mx ? launch_bn<128, true>(p, m, num_sms, st) : launch_bn<128, false>(p, m, num_sms, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -36,6 +36,9 @@
 //   warps 6..9  epilogue: drain own 128 x 256 accumulator, arrive on the
 //               leader's "accumulator free" barrier, scale, convert, store
 //               (bf16 through shared-memory boxes and tensor stores).
+// MX: the same kernel for MXFP4 operands (one E8M0 scale per 32 elements): a
+// stage has two scale atoms per 128 rows instead of four, and the MMA
+// (kind::mxf4 scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
 // Every wait is bounded; on expiry a CTA records a timeout, drains its own
 // copies (and, in the leader, its MMAs) and leaves its loops; the peer's waits
 // then expire too.  Both CTAs meet at a cluster barrier before freeing TMEM.
@@ -139,12 +142,14 @@ __device__ __forceinline__ void pair_abort(volatile int *abort_flag, int *status
 
 }  // namespace
 
+template <bool MX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_gemm_fp4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmLB,
                     const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmLBh,
                     const __grid_constant__ CUtensorMap tmD, const GemmParams p) {
   constexpr int S = kPairStages;
+  constexpr int kAtoms = MX ? 2 : 4;       // scale atoms of a full stage, per 128 rows
 #ifdef NVFP4_WAIT_STATS
   const long long kernel_t0 = clock64();
 #endif
@@ -270,13 +275,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         } else if (i < p.num_kt) {
           const int nk = i == p.num_kt - 1 ? last_nk : 4;
-          const uint32_t sfb = nk * 512;
+          const uint32_t sfb = (MX ? (nk + 1) / 2 : nk) * 512;
           mbar_arrive_expect_tx_u(sfbar, sfb * ((sfa_ok ? 1 : 0) + chunks));
           if (sfa_ok) bulk_load_u(sfa_base + stage * kPSfaBytes, sfa_src, sfb, sfbar);
           bulk_load_u(sfb_base + stage * kPSfbBytes, sfb_src, sfb, sfbar);
           if (chunks > 1) bulk_load_u(sfb_base + stage * kPSfbBytes + 2048, sfb_src + sfb_chunk_stride, sfb, sfbar);
-          sfa_src += 2048;
-          sfb_src += 2048;
+          sfa_src += 512 * kAtoms;
+          sfb_src += 512 * kAtoms;
         } else {
           mbar_arrive_u(sfbar);                 // no scales in a bf16 step: the phase completes at once
         }
@@ -298,7 +303,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------- MMA issue (leader only) --
     if (lane == 0 && rank == 0) {
-      uint32_t idesc = idesc_nvfp4(256, 256);
+      const auto fp4_desc = [](int n) { return MX ? idesc_mxfp4(256, n, 0) : idesc_nvfp4(256, n); };
+      uint32_t idesc = fp4_desc(256);
       uint32_t idesc_l = idesc_bf16(256, 256);
       const uint64_t adesc0 = sdesc_k_sw128(sA), bdesc0 = sdesc_k_sw128(sB);
       const uint32_t empty_base = smem_u32(empty);
@@ -319,6 +325,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // both stages' barriers are waited first (one barrier per stage: the
       // tiles and the scales), then the eight MMAs go out back to back with
       // a commit after each stage's four, and no flag is read per stage.
+      // K step j of a stage's FP4 product (MX: the descriptor's scale IDs pick
+      // the upper half of the atom for odd steps)
+      auto issue_fp4 = [&](uint64_t adesc, uint64_t bdesc, uint32_t sfa_col, uint32_t sfb_col, int j, uint32_t acc) {
+        if constexpr (MX)
+          tc_mma_mxfp4_pair(tmem, adesc + 2 * j, bdesc + 2 * j, j & 1 ? idesc | (2u << 4) | (2u << 29) : idesc,
+                            sfa_col + 4 * (j >> 1), sfb_col + 8 * (j >> 1), acc);
+        else
+          tc_mma_nvfp4_pair(tmem, adesc + 2 * j, bdesc + 2 * j, idesc, sfa_col + 4 * j, sfb_col + 8 * j, acc);
+      };
       auto issue_stage = [&](int st, int i, uint32_t &accumulate) {
         const uint64_t adesc = adesc0 + (uint64_t)((st * kPABytes) >> 4);
         const uint64_t bdesc = bdesc0 + (uint64_t)((st * kPBBytes) >> 4);
@@ -329,8 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j < nk) {
-              tc_mma_nvfp4_pair(tmem, adesc + 2 * j, bdesc + 2 * j, idesc, sfa_col + 4 * j, sfb_col + 8 * j,
-                                accumulate);
+              issue_fp4(adesc, bdesc, sfa_col, sfb_col, j, accumulate);
               accumulate = 1;
             }
           }
@@ -350,17 +364,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint64_t bdesc = bdesc0 + (uint64_t)((st * kPBBytes) >> 4);
         const uint32_t sfa_col = tmem + 256 + st * kPSfCols;
         const uint32_t sfb_col = sfa_col + kPSfaCols;
-        tc_mma_nvfp4_pair(tmem, adesc, bdesc, idesc, sfa_col, sfb_col, acc_first);
+        issue_fp4(adesc, bdesc, sfa_col, sfb_col, 0, acc_first);
 #pragma unroll
-        for (int j = 1; j < 4; ++j)
-          tc_mma_nvfp4_pair(tmem, adesc + 2 * j, bdesc + 2 * j, idesc, sfa_col + 4 * j, sfb_col + 8 * j, 1u);
+        for (int j = 1; j < 4; ++j) issue_fp4(adesc, bdesc, sfa_col, sfb_col, j, 1u);
         tc_commit_pair_mc(empty_base + 8 * st, 3);   // frees the stage in both CTAs
       };
       const int nfull = p.num_kt - (last_nk < 4 ? 1 : 0);
       for (int u = pair; ok && u < num_units; u += npairs) {
         // a half unit: N = 128 (64 B rows in each CTA, one chunk of B scales)
         const bool half_unit = u >= sched.split_from;
-        idesc = idesc_nvfp4(256, half_unit ? 128 : 256);
+        idesc = fp4_desc(half_unit ? 128 : 256);
         idesc_l = idesc_bf16(256, half_unit ? 128 : 256);
         PSTAT_T0();
         const bool got_acc = !*abort_flag && mbar_wait_u(acce, acc_phase ^ 1, p.timeout_ns);
@@ -458,14 +471,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const uint4 *fa = reinterpret_cast<const uint4 *>(sSFA + stage * kPSfaBytes) + lane;
           const uint4 *fb = reinterpret_cast<const uint4 *>(sSFB + stage * kPSfbBytes) + lane;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < kAtoms; ++j) {
             const uint4 w = fa[32 * j];                  // atom j, line `lane`: word q is row 32q + lane
             tmem_st_32x32b_x1(tq + stage * kPSfCols + 4 * j + q, q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w);
           }
           uint32_t v[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // columns 16h .. 16h+15 of the B region: K steps 2h, 2h+1, both chunks
+          for (int h = 0; h < kAtoms / 2; ++h) {
+            // columns 16h .. 16h+15 of the B region: atoms 2h, 2h+1, both chunks
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const int col = 16 * h + 4 * t;
@@ -638,20 +651,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // How many CTA pairs of this kernel the device holds at once (clusters of two
-// need two SMs of one GPC), queried once per device.
-static int resident_pairs(int num_sms) {
+// need two SMs of one GPC), queried once per device and instance, after its
+// shared-memory limit was raised.
+static int resident_pairs(const void *kernel, bool mx, int num_sms) {
   static std::mutex mu;
-  static int cached[64] = {};
+  static int cached_for[2][64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 2;
   std::lock_guard<std::mutex> lk(mu);
+  int *cached = cached_for[mx ? 1 : 0];
   if (!cached[dev]) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = kPSmemBytes;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, (void *)k_gemm_fp4_pair, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();   // clear: fall back to every SM pair
       n = num_sms / 2;
     }
@@ -661,9 +676,10 @@ static int resident_pairs(int num_sms) {
 }
 
 cudaError_t launch_gemm_fp4_pair(const GemmParams &p, const GemmMaps &m, int num_sms, cudaStream_t st) {
-  if (cudaError_t e = ensure_dynamic_smem((const void *)k_gemm_fp4_pair, kPSmemBytes); e != cudaSuccess) return e;
+  const auto kernel = p.mx ? k_gemm_fp4_pair<true> : k_gemm_fp4_pair<false>;
+  if (cudaError_t e = ensure_dynamic_smem((const void *)kernel, kPSmemBytes); e != cudaSuccess) return e;
   const int64_t tiles = ((p.M + 255) / 256) * (int64_t)p.tiles_n;
-  const int64_t resident = resident_pairs(num_sms);
+  const int64_t resident = resident_pairs((const void *)kernel, p.mx != 0, num_sms);
   GemmParams q = p;
   q.store_tma = p.store_tma && m.has_d;
   // half units need the 64-row B maps, and every half of the last n-tile
@@ -674,7 +690,7 @@ cudaError_t launch_gemm_fp4_pair(const GemmParams &p, const GemmMaps &m, int num
   int64_t pairs = std::min<int64_t>(tiles, resident);
   if (q.pair_half_tail && tiles < resident && 2 * tiles <= resident) pairs = 2 * tiles;
   if (pairs <= 0) return cudaSuccess;
-  return launch_pdl(k_gemm_fp4_pair, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPSmemBytes, st, m.a, m.b, m.t,
+  return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPSmemBytes, st, m.a, m.b, m.t,
                     m.lb, m.has_half ? m.bh : m.b, m.has_half ? m.lbh : m.lb, m.has_d ? m.d : m.a, q);
 }
 

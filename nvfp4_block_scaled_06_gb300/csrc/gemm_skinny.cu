@@ -24,6 +24,10 @@
 //               one store per activation row, coalesced across the warp.
 // Work units are (128-feature tile, K range); K ranges are summed in order by
 // the split-K pass.  Every wait is bounded.
+//
+// MX: the same kernel for MXFP4 operands (one E8M0 scale per 32 elements): a
+// stage has two scale atoms per operand instead of four, and the MMA (kind::mxf4
+// scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -59,6 +63,7 @@ __device__ __forceinline__ void sk_abort(volatile int *abort_flag, int *status) 
 // p.M activation rows (<= 32), p.N features, a_* = activations, b_* = weights
 // (as for k_gemm_fp4); tmX: activation codes, box 128 B x 32 rows; tmW: weight
 // codes, box 128 B x 128 rows.
+template <bool MX>
 __global__ void __launch_bounds__(kSkThreads, 1)
     k_gemm_fp4_skinny(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                       const GemmParams p) {
@@ -114,6 +119,11 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   const int num_units = p.tiles_n * ksplit;          // (128-feature tile, K range)
   const int kt_per = (p.num_kt + ksplit - 1) / ksplit;
   const int last_nk = p.nk64 - (p.num_kt - 1) * 4;   // K steps of the last 256-wide K tile
+  constexpr int kAtoms = MX ? 2 : 4;                 // scale atoms of a full stage
+  const auto sf_bytes = [&](int kt) {                // scale bytes of K tile kt (per 128 rows)
+    const int nk = kt == p.num_kt - 1 ? last_nk : 4;
+    return (uint32_t)((MX ? (nk + 1) / 2 : nk) * 512);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer --
@@ -130,23 +140,23 @@ __global__ void __launch_bounds__(kSkThreads, 1)
         const int nt = blockIdx.x / ksplit;
         const int kt0 = (blockIdx.x % ksplit) * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
         pre = min(S, kt1 - kt0);
-        const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)nt * p.b_sf_katoms + (int64_t)kt0 * 4);
+        const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)nt * p.b_sf_katoms + (int64_t)kt0 * kAtoms);
         for (int i = 0; i < pre; ++i) {
           const int kt = kt0 + i;
           const uint32_t fb = full_base + 8 * i;
-          const uint32_t sfb = (uint32_t)((kt == p.num_kt - 1 ? last_nk : 4) * 512);
+          const uint32_t sfb = sf_bytes(kt);
           mbar_arrive_expect_tx_u(fb, kSkABytes + kSkBBytes + 2 * sfb);
           tma_load_2d_u(w_base + i * kSkABytes, &tmW, fb, kt * 128, nt * 128);
           bulk_load_u(sfw_base + i * kSkSfBytes, sfw_src, sfb, fb);
-          sfw_src += 2048;
+          sfw_src += 512 * kAtoms;
         }
       }
       griddep_wait();
       for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
         const int nt = u / ksplit;
         const int kt0 = (u % ksplit) * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
-        const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)nt * p.b_sf_katoms + (int64_t)kt0 * 4);
-        const uint8_t *sfx_src = p.a_sf + 512 * ((int64_t)kt0 * 4);   // the rows' one 128-row chunk
+        const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)nt * p.b_sf_katoms + (int64_t)kt0 * kAtoms);
+        const uint8_t *sfx_src = p.a_sf + 512 * ((int64_t)kt0 * kAtoms);   // the rows' one 128-row chunk
         for (int kt = kt0; kt < kt1; ++kt) {
           const bool early = u == (int)blockIdx.x && kt - kt0 < pre;   // weights already in flight
           const bool got = early || (!*abort_flag && mbar_wait_u(empty_base + 8 * stage, phase ^ 1, p.timeout_ns));
@@ -156,7 +166,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
             break;
           }
           const uint32_t fb = full_base + 8 * stage;
-          const uint32_t sfb = (uint32_t)((kt == p.num_kt - 1 ? last_nk : 4) * 512);
+          const uint32_t sfb = sf_bytes(kt);
           if (!early) {
             mbar_arrive_expect_tx_u(fb, kSkABytes + kSkBBytes + 2 * sfb);
             tma_load_2d_u(w_base + stage * kSkABytes, &tmW, fb, kt * 128, nt * 128);
@@ -164,8 +174,8 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           }
           tma_load_2d_u(x_base + stage * kSkBBytes, &tmX, fb, kt * 128, 0);
           bulk_load_u(sfx_base + stage * kSkSfBytes, sfx_src, sfb, fb);
-          sfw_src += 2048;
-          sfx_src += 2048;
+          sfw_src += 512 * kAtoms;
+          sfx_src += 512 * kAtoms;
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
@@ -181,7 +191,8 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue --
     if (lane == 0) {
-      const uint32_t idesc = idesc_nvfp4(128, kSkN);
+      const uint32_t idesc = MX ? idesc_mxfp4(128, kSkN, 0) : idesc_nvfp4(128, kSkN);
+      const uint32_t idesc_hi = idesc_mxfp4(128, kSkN, 2);   // MX: the upper half of an atom
       const uint64_t wdesc0 = sdesc_k_sw128(sW), xdesc0 = sdesc_k_sw128(sX);
       const uint32_t sfr_base = smem_u32(sfready), empty_base = smem_u32(empty);
       const uint32_t accf = smem_u32(acc_full), acce = smem_u32(acc_empty);
@@ -215,7 +226,11 @@ __global__ void __launch_bounds__(kSkThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j < nk) {
-              tc_mma_nvfp4(tmem, wdesc + 2 * j, xdesc + 2 * j, idesc, sfw_col + 4 * j, sfx_col + 4 * j, accumulate);
+              if constexpr (MX)
+                tc_mma_mxfp4(tmem, wdesc + 2 * j, xdesc + 2 * j, j & 1 ? idesc_hi : idesc, sfw_col + 4 * (j >> 1),
+                             sfx_col + 4 * (j >> 1), accumulate);
+              else
+                tc_mma_nvfp4(tmem, wdesc + 2 * j, xdesc + 2 * j, idesc, sfw_col + 4 * j, sfx_col + 4 * j, accumulate);
               accumulate = 1;
             }
           }
@@ -255,13 +270,13 @@ __global__ void __launch_bounds__(kSkThreads, 1)
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 w = fw[32 * j];                // atom j, line `lane`
+          const uint4 w = fw[32 * (j % kAtoms)];     // atom j, line `lane` (MX: columns 8..15 are not read)
           v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
         tmem_st_32x32b_x16(tq + kSkN + stage * kSkSfCols, v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 w = fx[32 * j];
+          const uint4 w = fx[32 * (j % kAtoms)];
           v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
         tmem_st_32x32b_x16(tq + kSkN + stage * kSkSfCols + 16, v);
@@ -318,11 +333,12 @@ __global__ void __launch_bounds__(kSkThreads, 1)
 
 cudaError_t launch_gemm_fp4_skinny(const GemmParams &p, const CUtensorMap &x, const CUtensorMap &w, int num_sms,
                                    cudaStream_t st) {
-  if (cudaError_t e = ensure_dynamic_smem((const void *)k_gemm_fp4_skinny, kSkSmemBytes); e != cudaSuccess) return e;
+  const auto kernel = p.mx ? k_gemm_fp4_skinny<true> : k_gemm_fp4_skinny<false>;
+  if (cudaError_t e = ensure_dynamic_smem((const void *)kernel, kSkSmemBytes); e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.tiles_n * std::max(1, p.ksplit);
   const int64_t grid = std::min<int64_t>(units, num_sms);
   if (grid <= 0) return cudaSuccess;
-  return launch_pdl(k_gemm_fp4_skinny, dim3((unsigned)grid), dim3(kSkThreads), kSkSmemBytes, st, x, w, p);
+  return launch_pdl(kernel, dim3((unsigned)grid), dim3(kSkThreads), kSkSmemBytes, st, x, w, p);
 }
 
 }  // namespace nvfp4

@@ -61,10 +61,30 @@ cudaError_t launch_dequant(const uint8_t *codes, const uint8_t *sf, int sf_swz, 
                            int64_t cols, int transpose, __nv_bfloat16 *out, int64_t ldo, int num_sms,
                            cudaStream_t st);
 // Token-row codes + linear scales -> expert-grouped rows + swizzled scales.
-// src_rows: token rows of the source (index checks); status: device status word.
+// block: elements per scale (16, or 32 for MXFP4); src_rows: token rows of the
+// source (index checks); status: device status word.
 cudaError_t launch_gather_packed(const uint8_t *codes_src, const uint8_t *sf_src, const int32_t *row_map,
-                                 int64_t rows, const int32_t *num_mtiles, int64_t K, uint8_t *codes_dst, uint8_t *sf_dst, int num_sms,
-                                 cudaStream_t st, int64_t src_rows, int *status);
+                                 int64_t rows, const int32_t *num_mtiles, int64_t K, int block, uint8_t *codes_dst,
+                                 uint8_t *sf_dst, int num_sms, cudaStream_t st, int64_t src_rows, int *status);
+
+// -------------------------------------------------------------------- MXFP4 --
+struct MxQuantParams {
+  const __nv_bfloat16 *src;
+  int64_t rows, cols, ld, bstride;    // per matrix; strides in elements
+  int64_t batch;
+  uint8_t *codes, *sf;
+  int64_t codes_bstride, sf_bstride;  // bytes
+  int sf_swizzled;
+  int64_t dst_rows;                   // rows written
+  const int32_t *row_map;             // optional gather: dst row -> src row (< 0: left untouched)
+  const int32_t *num_mtiles;          // optional (device, batch 1): only rows < 128 x this are in use
+  int *status;
+};
+cudaError_t launch_mx_quant(const MxQuantParams &p, int num_sms, cudaStream_t st);
+// MXFP4 -> bf16, exact (transpose: out[c][r]).
+cudaError_t launch_mx_dequant(const uint8_t *codes, const uint8_t *sf, int sf_swz, int64_t batch, int64_t rows,
+                              int64_t cols, int64_t sf_bstride, int transpose, __nv_bfloat16 *out, int64_t ldo,
+                              int64_t out_bstride, int num_sms, cudaStream_t st);
 
 // --------------------------------------------------------------------- GEMM --
 // One grouped m-tile: expert, first A row (padded grouped order), valid rows,
@@ -99,6 +119,8 @@ struct GemmParams {
   int stall_probe;            // test hook: first wait on a barrier nothing arrives at
   int store_tma;              // pair kernel, bf16 output: D leaves through GemmMaps::d
   int pair_half_tail;         // pair kernel: a last wave of at most half the pairs runs as 256 x 128 units
+  int mx;                     // MXFP4 operands: one E8M0 scale per 32 elements (a 128x4 scale atom is 128
+                              // elements long), g_a = g_b = null
 };
 
 struct GemmMaps {
@@ -204,6 +226,38 @@ cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pa
 cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,
                                int64_t tokens, int top_k, int64_t N, __nv_bfloat16 *y, int num_sms,
                                cudaStream_t st, int *status);
+
+// ---------------------------------------------------------- expert selection --
+struct RouteTopkParams {
+  const void *logits;         // bf16 or fp32 [tokens][ld]
+  int64_t tokens, ld;
+  int num_experts, top_k;
+  const float *bias;          // [E] or null
+  int softmax;                // else sigmoid
+  int num_groups, topk_groups, group_top, group_size;
+  int group_lanes;            // lanes per group: 32 / (groups up to a power of two)
+  uint32_t group_magic;       // ceil(2^22 / group_size)
+  uint32_t index_mask;        // E up to a power of two, minus 1
+  int rank_by_score;          // groups are ranked by sums of scores (+ bias), not by keys
+  int need_row_sum;           // softmax scores of the whole row are needed
+  int renormalize;
+  float scale;
+  int32_t *expert_ids;        // [tokens][top_k]
+  float *weights;             // [tokens][top_k]
+};
+cudaError_t launch_route_topk(const RouteTopkParams &p, bool bf16, int num_sms, cudaStream_t st);
+struct RouteGradParams {
+  const void *logits;
+  int64_t tokens, ld, ld_grad;
+  int num_experts, top_k;
+  const int32_t *expert_ids;
+  const float *grad_weights;
+  int softmax, renormalize;
+  float scale;
+  void *grad_logits;          // as logits, [tokens][ld_grad]
+  int row_bytes;              // shared memory of one warp's row (set by the launcher)
+};
+cudaError_t launch_route_topk_backward(const RouteGradParams &p, bool bf16, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------- tensor maps --
 // Encodes a 2-D row-major tensor map; returns false on failure.

@@ -1,0 +1,267 @@
+// mx.cu -- MXFP4 (OCP Microscaling Formats v1.0): bf16 <-> E2M1 codes with one
+// E8M0 scale, a power of two, per 32 consecutive elements of a row.
+//
+//   amax = max |x| over the block;  X = 2^(floor(log2 amax) - 2)   (2 = E2M1's largest exponent)
+//   scale byte = log2 X + 127, at least 0; an all-zero block has byte 0
+//   code = sign(x) | E2M1_rn_satfinite(|x| / X)
+//   a block that holds an infinity or a NaN: byte 255 (E8M0 NaN), codes 0
+// x / X is exact in fp32 (a power-of-two scale of a bf16 value; what would
+// fall below 2^-126 encodes to 0 either way), so the only rounding is the
+// code's.  Back: E2M1(code) * 2^(byte - 127) is exact in bf16 for every byte
+// the quantizer writes.
+//
+// HBM-bound, one pass: 2 B read + 0.53125 B written per element, and back.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+// Sixteen 32-bit words (element 2i in the low half of w[i]) -> 32 codes as four
+// words (element 2j in the low nibble of byte j) and the scale byte.
+__device__ __forceinline__ uint4 mx_encode32(const uint32_t (&w)[16], uint32_t &sf) {
+  uint32_t m2 = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+  // the order of |x| is the order of its magnitude bits, infinities and NaNs last
+  const uint32_t be = max(m2 & 0xFFFFu, m2 >> 16) >> 7;     // biased exponent of amax
+  if (be == 255u) {
+    sf = 255u;
+    return make_uint4(0, 0, 0, 0);
+  }
+  const uint32_t byte = be > 2u ? be - 2u : 0u;
+  sf = byte;
+  const uint32_t inv = (254u - byte) << 23;                 // 2^(127 - byte), byte <= 252
+  const uint64_t ss = ((uint64_t)inv << 32) | inv;
+  uint32_t out[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = w[4 * q + i];
+      const uint64_t x = ((uint64_t)(u & 0xFFFF0000u) << 32) | (uint64_t)(u << 16);
+      uint64_t y;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(ss));
+      v[2 * i] = __uint_as_float((uint32_t)y);
+      v[2 * i + 1] = __uint_as_float((uint32_t)(y >> 32));
+    }
+    asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n\t"
+        "mov.b32 %0, {t0, t1, t2, t3};\n\t}"
+        : "=r"(out[q])
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// One 32-element block (64 bytes).
+template <bool kV8>
+__device__ __forceinline__ void load32(const __nv_bfloat16 *src, uint32_t (&w)[16]) {
+  if (kV8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
+                     "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
+                   : "l"(src + 16 * h));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src) + h);
+      w[4 * h] = a.x; w[4 * h + 1] = a.y; w[4 * h + 2] = a.z; w[4 * h + 3] = a.w;
+    }
+  }
+}
+
+constexpr int kMxUnit = 2;   // blocks per lane and step: 128 bytes of loads in flight per lane
+
+// A warp's work item is (row, 64 consecutive blocks), a lane's block one
+// 32-element block.  With the swizzled layout every scale byte of the padded
+// rows and columns is written (0 outside the matrix).
+template <bool kV8>
+__global__ void __launch_bounds__(256) k_mx_quant(const MxQuantParams p) {
+  // The wait comes first: a kernel launched after this one may read what no
+  // earlier kernel writes (the operand-swapped GEMM streams its weights)
+  // before its own wait, which is safe only once every earlier kernel is done.
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const uint32_t warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const uint32_t nwarps = gridDim.x * (blockDim.x >> 5);
+  const int64_t nblk = p.cols / 32, sfc_pad = (nblk + 3) & ~int64_t(3);
+  const __nv_bfloat16 *src = p.src + (int64_t)blockIdx.y * p.bstride;
+  uint8_t *codes = p.codes + (int64_t)blockIdx.y * p.codes_bstride;
+  uint8_t *sf = p.sf + (int64_t)blockIdx.y * p.sf_bstride;
+  int64_t rows_out = p.sf_swizzled ? ((p.dst_rows + 127) & ~int64_t(127)) : p.dst_rows;
+  if (p.num_mtiles) rows_out = min(rows_out, (int64_t)128 * *p.num_mtiles);
+  const uint32_t nch = (uint32_t)((sfc_pad + 32 * kMxUnit - 1) / (32 * kMxUnit));
+  const uint64_t items = (uint64_t)rows_out * nch;
+  uint64_t r = warp / nch;
+  uint32_t ch = warp % nch;
+  const uint32_t dr = nwarps / nch, dch = nwarps % nch;
+  for (uint64_t it = warp; it < items; it += nwarps) {
+    int64_t sr = -1;
+    if ((int64_t)r < p.dst_rows) sr = p.row_map ? (int64_t)p.row_map[r] : (int64_t)r;
+    if (!NVFP4_GUARD(sr < p.rows, p.status)) sr = -1;
+    if (!(p.row_map && sr < 0)) {      // unmapped (padding) rows are left untouched
+      const __nv_bfloat16 *srow = src + sr * p.ld;
+      const int64_t blk0 = (int64_t)ch * (32 * kMxUnit) + lane;
+      uint32_t w[kMxUnit][16];
+#pragma unroll
+      for (int u = 0; u < kMxUnit; ++u)
+        if (sr >= 0 && blk0 + 32 * u < nblk) load32<kV8>(srow + (blk0 + 32 * u) * 32, w[u]);
+#pragma unroll
+      for (int u = 0; u < kMxUnit; ++u) {
+        const int64_t blk = blk0 + 32 * u;
+        uint32_t sb = 0;
+        if (sr >= 0 && blk < nblk)
+          *reinterpret_cast<uint4 *>(codes + (int64_t)r * (p.cols / 2) + blk * 16) = mx_encode32(w[u], sb);
+        if (p.sf_swizzled) {
+          uint32_t v = sb;
+          v |= __shfl_down_sync(0xffffffffu, sb, 1) << 8;
+          v |= __shfl_down_sync(0xffffffffu, sb, 2) << 16;
+          v |= __shfl_down_sync(0xffffffffu, sb, 3) << 24;
+          if ((lane & 3) == 0 && blk < sfc_pad)
+            *reinterpret_cast<uint32_t *>(sf + 512 * ((int64_t)(r >> 7) * (sfc_pad >> 2) + (blk >> 2)) +
+                                          16 * (r & 31) + 4 * ((r & 127) >> 5)) = v;
+        } else if (blk < nblk) {
+          sf[(int64_t)r * nblk + blk] = (uint8_t)sb;
+        }
+      }
+    }
+    r += dr;
+    ch += dch;
+    if (ch >= nch) {
+      ch -= nch;
+      ++r;
+    }
+  }
+}
+
+// 2^(byte - 127); 255 is NaN.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+
+__device__ __forceinline__ uint32_t mx_scale_byte(const uint8_t *sf, int swz, int64_t r, int64_t blk, int64_t nblk) {
+  if (!swz) return __ldg(sf + r * nblk + blk);
+  const int64_t katoms = (nblk + 3) >> 2;
+  return __ldg(sf + 512 * ((r >> 7) * katoms + (blk >> 2)) + 16 * (r & 31) + 4 * ((r & 127) >> 5) + (blk & 3));
+}
+
+// Two codes (low nibble first) times the scale, as a bf16 pair.
+__device__ __forceinline__ uint32_t mx_pair(uint32_t byte, float s) {
+  const uint32_t h2 = e2m1x2_to_h2(byte);
+  const __nv_bfloat162 v =
+      __floats2bfloat162_rn(__fmul_rn(__half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFF))), s),
+                            __fmul_rn(__half2float(__ushort_as_half((unsigned short)(h2 >> 16))), s));
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Row-major: a thread takes one block, 16 bytes of codes in, 64 bytes of bf16
+// out (whole 32-byte sectors where the row allows it).  Grid (ctas, batch).
+__global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ sf,
+                                                    int swz, int64_t rows, int64_t cols, int64_t sf_bstride,
+                                                    __nv_bfloat16 *__restrict__ out, int64_t ldo,
+                                                    int64_t out_bstride) {
+  griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
+  const int64_t nblk = cols / 32, total = rows * nblk;
+  codes += (int64_t)blockIdx.y * rows * (cols / 2);
+  sf += (int64_t)blockIdx.y * sf_bstride;
+  out += (int64_t)blockIdx.y * out_bstride;
+  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = t / nblk, blk = t - r * nblk;
+    const uint4 c = __ldg(reinterpret_cast<const uint4 *>(codes) + t);
+    const float s = mx_scale(mx_scale_byte(sf, swz, r, blk, nblk));
+    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = mx_pair(cw[i >> 2] >> (8 * (i & 3)), s);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + r * ldo + blk * 32);
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+      st_global_v8(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+      st_global_v8(dst + 2, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+  }
+}
+
+// Transposed: thread = (row pair, block).  Consecutive threads take
+// consecutive row pairs, so a store instruction writes 32 consecutive bf16
+// pairs of one output row; a last single row takes two-byte stores.
+__global__ void __launch_bounds__(256) k_mx_dequant_t(const uint8_t *__restrict__ codes,
+                                                      const uint8_t *__restrict__ sf, int swz, int64_t rows,
+                                                      int64_t cols, int64_t sf_bstride,
+                                                      __nv_bfloat16 *__restrict__ out, int64_t ldo,
+                                                      int64_t out_bstride) {
+  griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
+  const int64_t nblk = cols / 32, pairs = (rows + 1) / 2, total = pairs * nblk;
+  codes += (int64_t)blockIdx.y * rows * (cols / 2);
+  sf += (int64_t)blockIdx.y * sf_bstride;
+  out += (int64_t)blockIdx.y * out_bstride;
+  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t blk = t / pairs, r0 = 2 * (t - blk * pairs);
+    const bool two = r0 + 1 < rows;
+    uint4 c[2];
+    float s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      c[h] = make_uint4(0, 0, 0, 0);
+      s[h] = 0.0f;
+      if (h == 0 || two) {
+        c[h] = __ldg(reinterpret_cast<const uint4 *>(codes + (r0 + h) * (cols / 2)) + blk);
+        s[h] = mx_scale(mx_scale_byte(sf, swz, r0 + h, blk, nblk));
+      }
+    }
+    const uint32_t c0[4] = {c[0].x, c[0].y, c[0].z, c[0].w}, c1[4] = {c[1].x, c[1].y, c[1].z, c[1].w};
+    __nv_bfloat16 *dst = out + blk * 32 * ldo + r0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = mx_pair(c0[i >> 2] >> (8 * (i & 3)), s[0]);
+      const uint32_t b = mx_pair(c1[i >> 2] >> (8 * (i & 3)), s[1]);
+      if (two) {
+        *reinterpret_cast<uint32_t *>(dst + (2 * i) * ldo) = __byte_perm(a, b, 0x5410);
+        *reinterpret_cast<uint32_t *>(dst + (2 * i + 1) * ldo) = __byte_perm(a, b, 0x7632);
+      } else {
+        *reinterpret_cast<uint16_t *>(dst + (2 * i) * ldo) = (uint16_t)a;
+        *reinterpret_cast<uint16_t *>(dst + (2 * i + 1) * ldo) = (uint16_t)(a >> 16);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quant(const MxQuantParams &p, int num_sms, cudaStream_t st) {
+  const int64_t nblk = p.cols / 32, sfc_pad = (nblk + 3) & ~int64_t(3);
+  const int64_t rows_out = p.sf_swizzled ? ((p.dst_rows + 127) & ~int64_t(127)) : p.dst_rows;
+  const int64_t items = rows_out * ((sfc_pad + 32 * kMxUnit - 1) / (32 * kMxUnit));
+  const int64_t cap = std::max<int64_t>(1, (int64_t)num_sms * 8 / p.batch);
+  const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 7) / 8, cap)), (unsigned)p.batch);
+  const bool v8 = (reinterpret_cast<uintptr_t>(p.src) & 31) == 0 && p.ld % 16 == 0 && p.bstride % 16 == 0;
+  return v8 ? launch_pdl(k_mx_quant<true>, grid, dim3(256), 0, st, p)
+            : launch_pdl(k_mx_quant<false>, grid, dim3(256), 0, st, p);
+}
+
+cudaError_t launch_mx_dequant(const uint8_t *codes, const uint8_t *sf, int sf_swz, int64_t batch, int64_t rows,
+                              int64_t cols, int64_t sf_bstride, int transpose, __nv_bfloat16 *out, int64_t ldo,
+                              int64_t out_bstride, int num_sms, cudaStream_t st) {
+  const int64_t work = (transpose ? (rows + 1) / 2 : rows) * (cols / 32);
+  const int64_t cap = std::max<int64_t>(1, (int64_t)num_sms * 16 / batch);
+  const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>((work + 255) / 256, cap)), (unsigned)batch);
+  return transpose ? launch_pdl(k_mx_dequant_t, grid, dim3(256), 0, st, codes, sf, sf_swz, rows, cols, sf_bstride, out,
+                                ldo, out_bstride)
+                   : launch_pdl(k_mx_dequant, grid, dim3(256), 0, st, codes, sf, sf_swz, rows, cols, sf_bstride, out,
+                                ldo, out_bstride);
+}
+
+}  // namespace nvfp4

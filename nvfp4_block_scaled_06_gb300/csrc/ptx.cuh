@@ -322,6 +322,17 @@ __device__ __forceinline__ void tc_mma_nvfp4(uint32_t d, uint64_t adesc, uint64_
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
+// The same with E8M0 scales per 32 elements: of each row's 32-bit scale word
+// the instruction takes the two bytes that the descriptor's scale IDs name.
+__device__ __forceinline__ void tc_mma_mxfp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
 // D(tmem) (+)= A(smem) * B(smem), bf16 operands, fp32 accumulation.
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t adesc, uint64_t bdesc,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -408,6 +419,14 @@ __host__ __device__ constexpr uint32_t idesc_nvfp4(int M, int N) {
          | (0u << 23)                    // scale format: UE4M3
          | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
+// Instruction descriptor: kind::mxf4, E2M1 x E2M1, E8M0 scales, K-major; sf_id
+// (0 or 2): the first of the two scale bytes taken from each 32-bit scale word.
+__host__ __device__ constexpr uint32_t idesc_mxfp4(int M, int N, int sf_id) {
+  return idesc_nvfp4(M, N)
+         | ((uint32_t)sf_id << 4)        // B scale ID
+         | (1u << 23)                    // scale format: UE8M0
+         | ((uint32_t)sf_id << 29);      // A scale ID
+}
 // Instruction descriptor: kind::f16 with bf16 A/B, fp32 D, K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
   return (1u << 4)                       // D format: F32
@@ -466,6 +485,15 @@ __device__ __forceinline__ void tc_mma_nvfp4_pair(uint32_t d, uint64_t adesc, ui
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxfp4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                  uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
       " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
