@@ -44,9 +44,17 @@ def _p(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without making a Stream object, where this torch
+# has that call: 0.1 us instead of 2.9 us of the 6 us that a prepared call took.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:

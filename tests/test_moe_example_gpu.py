@@ -50,7 +50,7 @@ def test_layer_against_torch(tokens):
             e = int(ids[t, j])
             d = (up[e] @ xd[t]).to(torch.bfloat16).float()
             h = (torch.nn.functional.silu(d[:H]) * d[H:]).to(torch.bfloat16)
-            want[t] += float(weights[t, j]) * (down[e] @ decoded(h[None])[0])
+            want[t] += float(weights[t, j].detach()) * (down[e] @ decoded(h[None])[0])
     want += xd @ shared.t()
     err = (y.double() - want).norm() / want.norm()
     assert float(err) < 1e-2, float(err)
