@@ -711,7 +711,7 @@ nvfp4_status run_grouped(const nvfp4_grouped_args *a, const GroupedPlan &pl, int
     // the caller's grouping: padded layout from its offsets, row_map -> token through its perm
     if (cudaError_t e_ = launch_layout_from_offsets(a->offsets_in, (int)a->num_experts, P, pl.prow_max, pl.goffsets,
                                                     pl.poffsets, pl.gtiles, pl.nmt, pl.row_map, a->perm_in,
-                                                    (int)a->top_k, sms, st, status);
+                                                    (int)a->top_k, sms, st, status, nullptr);
         e_ != cudaSuccess)
       return cuda_status(e_);
     if (a->perm_out && a->perm_out != a->perm_in &&
@@ -873,7 +873,7 @@ nvfp4_status run_moe_down(const nvfp4_moe_down_args *a, const MoeDownPlan &pl, i
   const int64_t P = a->num_tokens * a->top_k;
   if (cudaError_t e_ = launch_layout_from_offsets(a->expert_offsets, (int)a->num_experts, P, pl.prow_max,
                                                   pl.goffsets, pl.poffsets, pl.gtiles, pl.nmt, pl.row_map,
-                                                  nullptr, 0, sms, st, status);
+                                                  a->perm, 0, sms, st, status, pl.inv);
       e_ != cudaSuccess)
     return cuda_status(e_);
   // h is quantized once (one tensor-wide g) straight into the padded layout:
@@ -930,7 +930,7 @@ nvfp4_status run_moe_down(const nvfp4_moe_down_args *a, const MoeDownPlan &pl, i
   if (s != NVFP4_OK) return s;
   return cuda_status(launch_moe_combine(pl.d, a->perm, pl.inv, a->route_weights, a->num_tokens,
                                         (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
-                                        status));
+                                        status, layout_makes_inverse(pl.prow_max)));
 }
 
 // --------------------------------------------------------------------- LoRA --
@@ -1601,7 +1601,7 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
     // the caller's grouping: padded layout from its offsets, row_map -> token through its perm
     if (cudaError_t e_ = launch_layout_from_offsets(a->offsets_in, (int)a->num_experts, P, pl.prow_max, pl.offsets,
                                                     pl.poffsets, pl.gtiles, pl.nmt, pl.row_map, a->perm_in,
-                                                    (int)a->top_k, sms, st, status);
+                                                    (int)a->top_k, sms, st, status, nullptr);
         e_ != cudaSuccess)
       return cuda_status(e_);
     if (a->perm_out && a->perm_out != a->perm_in)
@@ -1615,7 +1615,24 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
         return cuda_status(e_);
   }
   const uint8_t *codes = a->x_codes, *sf = a->x_sf;
-  if (a->x_bf16) {
+  // few rows: each is quantized where it goes, top_k times over, which saves
+  // the copy's launch; many: once per token, then copied
+  const bool direct = a->x_bf16 && P <= 2048;
+  if (direct) {
+    MxQuantParams q{};
+    q.src = static_cast<const __nv_bfloat16 *>(a->x_bf16);
+    q.rows = a->num_tokens;
+    q.cols = q.ld = a->K;
+    q.batch = 1;
+    q.codes = pl.xq;
+    q.sf = pl.xsf;
+    q.sf_swizzled = 1;
+    q.dst_rows = pl.prow_max;
+    q.row_map = pl.row_map;
+    q.num_mtiles = pl.nmt;
+    q.status = status;
+    if (cudaError_t e_ = launch_mx_quant(q, sms, st); e_ != cudaSuccess) return cuda_status(e_);
+  } else if (a->x_bf16) {
     // every token row is quantized once, then its codes and scales are copied
     // to each of its top_k rows of the grouped operand
     MxQuantParams q{};
@@ -1630,10 +1647,11 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
     codes = pl.xq_tok;
     sf = pl.xsf_tok;
   }
-  if (cudaError_t e_ = launch_gather_packed(codes, sf, pl.row_map, pl.prow_max, pl.nmt, a->K, 32, pl.xq, pl.xsf, sms,
-                                            st, a->num_tokens, status);
-      e_ != cudaSuccess)
-    return cuda_status(e_);
+  if (!direct)
+    if (cudaError_t e_ = launch_gather_packed(codes, sf, pl.row_map, pl.prow_max, pl.nmt, a->K, 32, pl.xq, pl.xsf, sms,
+                                              st, a->num_tokens, status);
+        e_ != cudaSuccess)
+      return cuda_status(e_);
   GroupedProducts gp{};
   gp.E = a->num_experts;
   gp.N = a->N;
@@ -1695,7 +1713,7 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
   const int64_t P = a->num_tokens * a->top_k;
   if (cudaError_t e_ = launch_layout_from_offsets(a->expert_offsets, (int)a->num_experts, P, pl.prow_max,
                                                   pl.goffsets, pl.poffsets, pl.gtiles, pl.nmt, pl.row_map,
-                                                  nullptr, 0, sms, st, status);
+                                                  a->perm, 0, sms, st, status, pl.inv);
       e_ != cudaSuccess)
     return cuda_status(e_);
   // h is quantized straight into the padded layout: padded row r takes grouped row row_map[r]
@@ -1733,7 +1751,7 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
   if (s != NVFP4_OK) return s;
   return cuda_status(launch_moe_combine(pl.d, a->perm, pl.inv, a->route_weights, a->num_tokens,
                                         (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
-                                        status));
+                                        status, layout_makes_inverse(pl.prow_max)));
 }
 
 }  // namespace

@@ -217,15 +217,19 @@ struct RouteParams {
 cudaError_t launch_route(const RouteParams &p, cudaStream_t st);
 // Padded grouped layout (goffsets = the clamped offsets rebuilt, poffsets,
 // m-tiles, row_map -> grouped row, or -> token through perm / top_k) of rows
-// that arrive already grouped with the given expert offsets.
+// that arrive already grouped with the given expert offsets (perm with top_k 0:
+// row_map holds grouped rows).  inv (optional): receives the inverse of perm
+// where layout_makes_inverse(padded_rows_max).
+bool layout_makes_inverse(int64_t padded_rows_max);
 cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pairs, int64_t padded_rows_max,
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,
-                                       int num_sms, cudaStream_t st, int *status);
-// y[t] = sum_j w[t][j] d[inverse perm (t*top_k + j)] (bf16 rows, fp32 sums).
+                                       int num_sms, cudaStream_t st, int *status, int32_t *inv);
+// y[t] = sum_j w[t][j] d[inverse perm (t*top_k + j)] (bf16 rows, fp32 sums);
+// inv holds the inverse already, or is made here.
 cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,
                                int64_t tokens, int top_k, int64_t N, __nv_bfloat16 *y, int num_sms,
-                               cudaStream_t st, int *status);
+                               cudaStream_t st, int *status, bool inv_ready);
 
 // ---------------------------------------------------------- expert selection --
 struct RouteTopkParams {
@@ -255,7 +259,6 @@ struct RouteGradParams {
   int softmax, renormalize;
   float scale;
   void *grad_logits;          // as logits, [tokens][ld_grad]
-  int row_bytes;              // shared memory of one warp's row (set by the launcher)
 };
 cudaError_t launch_route_topk_backward(const RouteGradParams &p, bool bf16, int num_sms, cudaStream_t st);
 

@@ -90,53 +90,19 @@ __device__ __forceinline__ int32_t block_exclusive_scan_capped(int32_t v, int32_
   return min(in_warp, cap - before) + before;
 }
 
-__global__ void __launch_bounds__(1024) k_route_scan(const RouteParams p) {
-  griddep_launch_dependents();
-  griddep_wait();   // inputs may come from the previous kernel in the stream
+// Offsets, 128-padded offsets, the m-tile table and the padding rows of row_map
+// from one expert count per thread of a 1024-thread block; returns the
+// thread's expert's first grouped row and first padded row.
+__device__ __forceinline__ void write_layout(const RouteParams &p, int32_t count, int32_t &off, int32_t &poff) {
   __shared__ int32_t scratch[64];
   const int e = threadIdx.x;
   const bool act = e < p.num_experts;
-  int32_t count = 0;
-  // up to 32 chunks: every chunk count of this expert in registers at once,
-  // and after the scan each chunk's first grouped position is written back
-  // over its count; more chunks: eight loads in flight per step, and the
-  // scatter kernel forms the chunk bases itself
-  const bool few = p.nchunks <= 32;
-  int32_t hv[32];
-  if (act && few) {
-    // unconditional loads (the last chunk repeated, its value masked): all
-    // 32 are in flight together
-#pragma unroll
-    for (int j = 0; j < 32; ++j) hv[j] = p.hist[(int64_t)min(j, p.nchunks - 1) * p.num_experts + e];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) hv[j] = j < p.nchunks ? hv[j] : 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) count += hv[j];
-  } else if (act) {
-    int c = 0;
-    for (; c + 8 <= p.nchunks; c += 8) {
-      int32_t v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p.hist[(int64_t)(c + j) * p.num_experts + e];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) count += v[j];
-    }
-    for (; c < p.nchunks; ++c) count += p.hist[(int64_t)c * p.num_experts + e];
-  }
   const int32_t padded = (count + 127) & ~127;
   const int32_t mt = padded / 128;
   int32_t total, ptotal, mtotal;
-  const int32_t off = block_exclusive_scan(count, scratch, total);
-  const int32_t poff = block_exclusive_scan(padded, scratch, ptotal);
+  off = block_exclusive_scan(count, scratch, total);
+  poff = block_exclusive_scan(padded, scratch, ptotal);
   const int32_t moff = block_exclusive_scan(mt, scratch, mtotal);
-  if (act && few) {
-    int32_t b = off;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j < p.nchunks) p.hist[(int64_t)j * p.num_experts + e] = b;
-      b += hv[j];
-    }
-  }
   __shared__ int32_t s_cnt[1024], s_off[1024], s_poff[1024], s_moff[1024];
   if (act) {
     p.counts[e] = count;
@@ -178,6 +144,80 @@ __global__ void __launch_bounds__(1024) k_route_scan(const RouteParams p) {
   // the layout is bounded by the m-tile count
 }
 
+__global__ void __launch_bounds__(1024) k_route_scan(const RouteParams p) {
+  griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
+  const int e = threadIdx.x;
+  const bool act = e < p.num_experts;
+  int32_t count = 0;
+  // up to 32 chunks: every chunk count of this expert in registers at once,
+  // and after the scan each chunk's first grouped position is written back
+  // over its count; more chunks: eight loads in flight per step, and the
+  // scatter kernel forms the chunk bases itself
+  const bool few = p.nchunks <= 32;
+  int32_t hv[32];
+  if (act && few) {
+    // unconditional loads (the last chunk repeated, its value masked): all
+    // 32 are in flight together
+#pragma unroll
+    for (int j = 0; j < 32; ++j) hv[j] = p.hist[(int64_t)min(j, p.nchunks - 1) * p.num_experts + e];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) hv[j] = j < p.nchunks ? hv[j] : 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) count += hv[j];
+  } else if (act) {
+    int c = 0;
+    for (; c + 8 <= p.nchunks; c += 8) {
+      int32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p.hist[(int64_t)(c + j) * p.num_experts + e];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) count += v[j];
+    }
+    for (; c < p.nchunks; ++c) count += p.hist[(int64_t)c * p.num_experts + e];
+  }
+  int32_t off, poff;
+  write_layout(p, count, off, poff);
+  if (act && few) {
+    int32_t b = off;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < p.nchunks) p.hist[(int64_t)j * p.num_experts + e] = b;
+      b += hv[j];
+    }
+  }
+}
+
+// Stable rank of each of the block's pairs among those with its expert, and
+// their perm and row_map entries.  sh_base: first grouped row of this block's
+// pairs per expert; sh_first, sh_pfirst: the expert's first grouped and padded
+// rows; sh_cnt [32 warps][E] is zero and the block synchronized.
+__device__ __forceinline__ void scatter_pairs(const RouteParams &p, int64_t i, bool in, const int32_t *sh_base,
+                                              uint16_t *sh_cnt, const int32_t *first, const int32_t *pfirst) {
+  const int E = p.num_experts;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int e = -1;
+  if (in) {
+    e = p.expert_ids[i];
+    if (e < 0 || e >= E) e = -1;
+  }
+  const unsigned same = __match_any_sync(0xffffffffu, e);
+  const unsigned lt = (1u << lane) - 1u;
+  const int rank_w = __popc(same & lt);
+  if (e >= 0 && (same & lt) == 0) sh_cnt[w * E + e] = (uint16_t)__popc(same);
+  __syncthreads();
+  if (e >= 0) {
+    int before = 0;
+    for (int v = 0; v < w; ++v) before += sh_cnt[v * E + e];
+    const int32_t pos = sh_base[e] + before + rank_w;
+    const int64_t prow = (int64_t)pfirst[e] + (pos - first[e]);
+    if (NVFP4_GUARD(pos >= 0 && pos < p.pairs && prow >= 0 && prow < p.padded_rows_max, p.status)) {
+      p.perm[pos] = (int32_t)i;
+      p.row_map[prow] = (int32_t)(i / p.top_k);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(1024) k_route_scatter(const RouteParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
@@ -195,31 +235,44 @@ __global__ void __launch_bounds__(1024) k_route_scatter(const RouteParams p) {
     }
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x;
-  int e = -1;
-  if (threadIdx.x < p.chunk && i < p.pairs) {
-    e = p.expert_ids[i];
-    if (e < 0 || e >= E) e = -1;
-  }
-  const unsigned same = __match_any_sync(0xffffffffu, e);
-  const unsigned lt = (1u << lane) - 1u;
-  const int rank_w = __popc(same & lt);
-  if (e >= 0 && (same & lt) == 0) sh_cnt[w * E + e] = (uint16_t)__popc(same);
+  scatter_pairs(p, i, threadIdx.x < p.chunk && i < p.pairs, sh_base, sh_cnt, p.offsets, p.poffsets);
+}
+
+// Up to 1024 pairs (decode): counts, layout and scatter by one block in one
+// launch (the three launches of the general path took 14 us back to back).
+__global__ void __launch_bounds__(1024) k_route_one(const RouteParams p) {
+  griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
+  extern __shared__ int32_t sh_one[];                             // [E] counts, [E] offsets, [E] padded offsets
+  const int E = p.num_experts;
+  int32_t *sh_off = sh_one + E, *sh_poff = sh_off + E;
+  uint16_t *sh_cnt = reinterpret_cast<uint16_t *>(sh_poff + E);   // [32 warps][E]
+  for (int i = threadIdx.x; i < 32 * E; i += blockDim.x) sh_cnt[i] = 0;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) sh_one[e] = 0;
   __syncthreads();
-  if (e >= 0) {
-    int before = 0;
-    for (int v = 0; v < w; ++v) before += sh_cnt[v * E + e];
-    const int32_t pos = sh_base[e] + before + rank_w;
-    const int64_t prow = (int64_t)p.poffsets[e] + (pos - p.offsets[e]);
-    if (NVFP4_GUARD(pos >= 0 && pos < p.pairs && prow >= 0 && prow < p.padded_rows_max, p.status)) {
-      p.perm[pos] = (int32_t)i;
-      p.row_map[prow] = (int32_t)(i / p.top_k);
-    }
+  const bool in = threadIdx.x < p.pairs;
+  if (in) {
+    const int e = p.expert_ids[threadIdx.x];
+    if (NVFP4_NOTE(e >= 0 && e < E, p.status)) atomicAdd(&sh_one[e], 1);   // others are dropped
   }
+  __syncthreads();
+  int32_t off, poff;
+  write_layout(p, (int)threadIdx.x < E ? sh_one[threadIdx.x] : 0, off, poff);
+  if ((int)threadIdx.x < E) {
+    sh_off[threadIdx.x] = off;
+    sh_poff[threadIdx.x] = poff;
+  }
+  __syncthreads();
+  scatter_pairs(p, threadIdx.x, in, sh_off, sh_cnt, sh_off, sh_poff);
 }
 
 cudaError_t launch_route(const RouteParams &p, cudaStream_t st) {
+  if (p.pairs <= 1024) {
+    const size_t one = (size_t)p.num_experts * (3 * sizeof(int32_t) + 32 * sizeof(uint16_t));
+    if (cudaError_t e = ensure_dynamic_smem((const void *)k_route_one, one); e != cudaSuccess) return e;
+    return launch_pdl(k_route_one, dim3(1), dim3(1024), one, st, p);
+  }
   cudaError_t e = launch_pdl(k_route_hist, dim3(p.nchunks), dim3(kRouteChunk), p.num_experts * sizeof(int32_t), st, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_route_scan, dim3(1), dim3(1024), 0, st, p);
@@ -240,12 +293,16 @@ cudaError_t launch_route(const RouteParams &p, cudaStream_t st) {
 // grouped rows or the padded bound.
 __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restrict__ offsets, int E, int64_t pairs,
                                                          int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
-                                                         int32_t *gnum_mtiles, int64_t max_tiles, int *status) {
+                                                         int32_t *gnum_mtiles, int64_t max_tiles, int *status,
+                                                         int32_t *row_map, const int32_t *__restrict__ perm,
+                                                         int top_k, int32_t *inv) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   __shared__ int32_t scratch[64];
   const int e = threadIdx.x;
   const bool act = e < E;
+  if (inv)
+    for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) inv[i] = -1;
   const int64_t diff = act ? (int64_t)offsets[e + 1] - (int64_t)offsets[e] : 0;
   int32_t count = (int32_t)(diff < 0 ? 0 : diff > pairs ? pairs : diff);
   const int32_t before = block_exclusive_scan_capped(count, (int32_t)pairs, scratch);
@@ -274,6 +331,34 @@ __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restri
     goffsets[E] = ctotal;
     poffsets[E] = ptotal;
     *gnum_mtiles = mtotal;
+  }
+  if (row_map) {
+    // few rows: the row map (and the inverse of perm) by the same block, a
+    // warp per expert; rows past ptotal are never read
+    __shared__ int32_t s_cnt[1024], s_off[1024], s_poff[1024];
+    if (act) {
+      s_cnt[e] = count;
+      s_off[e] = off;
+      s_poff[e] = poff;
+    }
+    __syncthreads();   // (orders the fill of inv before its entries below, too)
+    for (int x = threadIdx.x >> 5; x < E; x += blockDim.x >> 5) {
+      const int32_t cnt = s_cnt[x], pad = (cnt + 127) & ~127;
+      for (int32_t i = threadIdx.x & 31; i < pad; i += 32) {
+        int32_t v = i < cnt ? s_off[x] + i : -1;
+        if (perm && top_k && v >= 0) {
+          const int32_t pr = perm[v];
+          v = NVFP4_NOTE(pr >= 0 && pr < pairs, status) ? pr / top_k : -1;
+        }
+        if (NVFP4_GUARD(s_poff[x] + i < 128 * max_tiles, status)) row_map[s_poff[x] + i] = v;
+      }
+    }
+    if (inv) {
+      for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) {
+        const int32_t q = perm[i];
+        if (NVFP4_NOTE(q >= 0 && q < pairs, status)) inv[q] = (int32_t)i;
+      }
+    }
   }
 }
 
@@ -309,16 +394,25 @@ __global__ void k_rowmap_from_offsets(const int32_t *__restrict__ goffsets,
   }
 }
 
+// Up to this many padded rows the one-block kernel writes the row map as well
+// (4352 rows and 256 pairs: 5 us in one launch instead of 8 to 12 in two to four).
+constexpr int64_t kOneBlockRows = 16384;
+
+bool layout_makes_inverse(int64_t padded_rows_max) { return padded_rows_max <= kOneBlockRows; }
+
 cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pairs, int64_t padded_rows_max,
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,
-                                       int num_sms, cudaStream_t st, int *status) {
+                                       int num_sms, cudaStream_t st, int *status, int32_t *inv) {
+  const bool one = layout_makes_inverse(padded_rows_max);
   cudaError_t e = launch_pdl(k_offsets_layout, dim3(1), dim3(1024), 0, st, offsets, E, pairs, goffsets, poffsets,
-                             gtiles, gnum_mtiles, padded_rows_max / 128, status);
-  if (e != cudaSuccess) return e;
+                             gtiles, gnum_mtiles, padded_rows_max / 128, status, one ? row_map : (int32_t *)nullptr,
+                             perm, top_k, one ? inv : (int32_t *)nullptr);
+  if (e != cudaSuccess || one) return e;
   const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>((padded_rows_max + 255) / 256, (int64_t)num_sms * 4));
   return launch_pdl(k_rowmap_from_offsets, dim3((unsigned)ctas), dim3(256), 0, st, (const int32_t *)goffsets,
-                    (const int32_t *)poffsets, E, padded_rows_max, perm, top_k, pairs, row_map, status);
+                    (const int32_t *)poffsets, E, padded_rows_max, top_k ? perm : (const int32_t *)nullptr, top_k, pairs,
+                    row_map, status);
 }
 
 // ----------------------------------------------------------------- combine --
@@ -343,13 +437,16 @@ __global__ void k_fill_i32(int32_t *p, int64_t n, int32_t v) {
     p[i] = v;
 }
 
-// A warp takes a token: its slots' row indices and weights are read once, and
-// for top_k <= 8 the 16-byte loads of all slots are in flight together before
-// the sums (which keep the slot order).
+// A warp takes a token, or with few tokens one of `parts` interleaved column
+// ranges of it (32 tokens of 6144 columns took 22 us with a warp each): its
+// slots' row indices and weights are read once, and for top_k <= 8 the 16-byte
+// loads of all slots are in flight together before the sums (which keep the
+// slot order).
 __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__restrict__ d,
                                                      const int32_t *__restrict__ inv,
                                                      const float *__restrict__ w, int64_t tokens, int top_k,
-                                                     int64_t N, __nv_bfloat16 *__restrict__ y, int *status) {
+                                                     int64_t N, __nv_bfloat16 *__restrict__ y, int parts,
+                                                     int *status) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   constexpr int kMaxK = 8;
@@ -357,7 +454,9 @@ __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__rest
   const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int64_t vecs = N / 8;                       // 16-byte vectors of a row
-  for (int64_t t = warp; t < tokens; t += nwarps) {
+  for (int64_t item = warp; item < tokens * parts; item += nwarps) {
+    const int64_t t = item / parts;
+    const int64_t v0 = (item - t * parts) * 32 + lane, vstep = 32 * (int64_t)parts;
     if (top_k <= kMaxK) {
       const uint4 *rows[kMaxK];
       float wj[kMaxK];
@@ -368,7 +467,7 @@ __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__rest
         rows[j] = g >= 0 ? reinterpret_cast<const uint4 *>(d + (int64_t)g * N) : nullptr;
         wj[j] = g >= 0 ? w[t * top_k + j] : 0.0f;
       }
-      for (int64_t v = lane; v < vecs; v += 32) {
+      for (int64_t v = v0; v < vecs; v += vstep) {
         uint4 q[kMaxK];
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j) q[j] = rows[j] ? __ldg(rows[j] + v) : make_uint4(0, 0, 0, 0);
@@ -395,7 +494,7 @@ __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__rest
       }
       continue;
     }
-    for (int64_t v = lane; v < vecs; v += 32) {
+    for (int64_t v = v0; v < vecs; v += vstep) {
       float acc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
@@ -424,16 +523,20 @@ __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__rest
 
 cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,
                                int64_t tokens, int top_k, int64_t N, __nv_bfloat16 *y, int num_sms,
-                               cudaStream_t st, int *status) {
+                               cudaStream_t st, int *status, bool inv_ready) {
   const int64_t pairs = tokens * top_k;
-  const int64_t c1 = std::max<int64_t>(1, std::min<int64_t>((pairs + 255) / 256, (int64_t)num_sms * 4));
-  cudaError_t e = launch_pdl(k_fill_i32, dim3((unsigned)c1), dim3(256), 0, st, inv, pairs, (int32_t)-1);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(k_invert_perm, dim3((unsigned)c1), dim3(256), 0, st, perm, pairs, inv, status);
-  if (e != cudaSuccess) return e;
-  const int64_t c2 = std::max<int64_t>(1, std::min<int64_t>((tokens + 7) / 8, (int64_t)num_sms * 8));
+  if (!inv_ready) {
+    const int64_t c1 = std::max<int64_t>(1, std::min<int64_t>((pairs + 255) / 256, (int64_t)num_sms * 4));
+    cudaError_t e = launch_pdl(k_fill_i32, dim3((unsigned)c1), dim3(256), 0, st, inv, pairs, (int32_t)-1);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(k_invert_perm, dim3((unsigned)c1), dim3(256), 0, st, perm, pairs, inv, status);
+    if (e != cudaSuccess) return e;
+  }
+  // column ranges until every SM has 32 warps
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((N / 8 + 31) / 32, (int64_t)num_sms * 32 / tokens));
+  const int64_t c2 = std::max<int64_t>(1, std::min<int64_t>((tokens * parts + 7) / 8, (int64_t)num_sms * 8));
   return launch_pdl(k_moe_combine, dim3((unsigned)c2), dim3(256), 0, st, d, (const int32_t *)inv, w, tokens, top_k,
-                    N, y, status);
+                    N, y, (int)parts, status);
 }
 
 }  // namespace nvfp4

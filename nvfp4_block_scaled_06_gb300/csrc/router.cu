@@ -12,13 +12,17 @@
 // An expert whose key is -inf or NaN (a masked logit) is never chosen; missing
 // choices get id -1 and weight 0.
 //
-// A warp per token.  A lane keeps its E/32 keys as order-preserving integers
-// with the low bits replaced by the inverted expert index, so that a round of
-// the selection is one warp-wide integer maximum (redux) that names the expert,
-// and removing it is one compare per key.  When two neighbouring results (the
-// first rejected key included) agree in every bit that is left of the key, the
-// token's selection runs again on the whole keys.  bf16 logits without a bias
-// lose no bits and never need that.
+// Two kernels.  k_route_few (top_k <= 8): 4 to 32 lanes per token; a lane takes
+// its experts in batches of eight, sorts each batch with a fixed network and
+// merges it into its running eight largest, then the lanes' lists are merged
+// pairwise by shuffles.  k_route_any, a warp per token: every other form
+// (top_k > 8, softmax scores with a bias, group counts that do not divide a
+// lane count).  In both a key is an order-preserving integer whose low bits are
+// replaced by the inverted expert index, so that one integer maximum carries
+// the expert along and ties fall to the lowest index.  Where two neighbouring
+// results (the largest rejected key included) agree in every bit that is left
+// of the key, the token's selection runs again on the whole keys.  bf16 logits
+// without a bias lose no bits and never need that.
 #include <cfloat>
 
 #include "internal.h"
@@ -93,10 +97,12 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *x) {
   }
 }
 
-// ---------------------------------------------------------------- selection --
+// ------------------------------------------------- selection, a warp per token --
+// The k largest by k rounds of one warp-wide integer maximum (redux), which
+// names the expert; removing it is one compare per key.
 // Expert of a lane's value (c, i): c * 32 * VEC + lane * VEC + i.
 template <typename T, int VEC, int NCH>
-__global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk(const RouteTopkParams p) {
+__global__ void __launch_bounds__(kRouterWarps * 32) k_route_any(const RouteTopkParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   constexpr int VPL = VEC * NCH;
@@ -275,6 +281,267 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk(const RouteTop
   }
 }
 
+// ------------------------------------------ selection, up to 8 experts per token --
+// Descending order of keys a, b.
+__device__ __forceinline__ void cex(uint32_t &a, uint32_t &b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+// A 19-comparator sorting network for eight keys (its six layers; every
+// 0/1 input is sorted, which proves it for all).
+__device__ __forceinline__ void sort8(uint32_t (&v)[8]) {
+  cex(v[0], v[2]); cex(v[1], v[3]); cex(v[4], v[6]); cex(v[5], v[7]);
+  cex(v[0], v[4]); cex(v[1], v[5]); cex(v[2], v[6]); cex(v[3], v[7]);
+  cex(v[0], v[1]); cex(v[2], v[3]); cex(v[4], v[5]); cex(v[6], v[7]);
+  cex(v[2], v[4]); cex(v[3], v[5]);
+  cex(v[1], v[4]); cex(v[3], v[6]);
+  cex(v[1], v[2]); cex(v[3], v[4]); cex(v[5], v[6]);
+}
+// run (sorted) <- the eight largest of run and v (sorted): the elementwise
+// maxima of one and the other reversed are them, as a bitonic sequence.
+// kRest: rest <- the largest key that ever lost.
+template <bool kRest>
+__device__ __forceinline__ void merge8(uint32_t (&run)[8], const uint32_t (&v)[8], uint32_t &rest) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = run[i], b = v[7 - i];
+    run[i] = max(a, b);
+    if (kRest) rest = max(rest, min(a, b));
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & o)) cex(run[i], run[i + o]);
+  }
+}
+
+// Eight consecutive logits: two or one 16-byte loads, or (kVec false) the n
+// first of them, -inf behind.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_eight(const T *p, int n, float (&x)[8]) {
+  if constexpr (kVec) {
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += V) load_vec<V>(p + i, x + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? load1(p + i) : -INFINITY;
+  }
+}
+
+// The key and the value that groups are ranked by, of expert e.
+template <bool kScored>
+__device__ __forceinline__ uint32_t route_key(const RouteTopkParams &p, int e, float x, float &gval) {
+  bool in = x > -INFINITY;
+  float key = x, s = x;
+  if (kScored) {
+    s = sigmoid(x);
+    if (p.bias) {
+      s += __ldg(p.bias + e);
+      key = s;
+      in = in && key > -INFINITY;
+    }
+  }
+  gval = in ? s : -INFINITY;         // (kScored without a bias: only where groups are ranked by scores)
+  const uint32_t b = __float_as_uint(key + 0.0f);                       // -0 counts as +0
+  const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return in ? u : 0u;
+}
+
+// The exact selection of one token by a whole warp: k rounds, each the largest
+// (key, lowest index) below the previous round's.  Lane j returns choice j.
+template <typename T, bool kScored>
+__device__ __noinline__ int route_exact(const RouteTopkParams &p, const T *row, uint32_t keep) {
+  const int lane = threadIdx.x & 31;
+  uint32_t last = 0xffffffffu;
+  int last_e = -1, id = -1;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t best = 0u;
+    int best_e = 0;
+    for (int e = lane; e < p.num_experts; e += 32) {
+      if (!((keep >> ((uint32_t)e * p.group_magic >> 22)) & 1u)) continue;
+      float g;
+      const uint32_t u = route_key<kScored>(p, e, load1(row + e), g);
+      if ((u < last || (u == last && e > last_e)) && u > best) {
+        best = u;
+        best_e = e;
+      }
+    }
+    const uint32_t m = redux_max(best);
+    if (m == 0u) break;
+    last = m;
+    last_e = (int)redux_min(best == m ? (uint32_t)best_e : 0xffffffffu);
+    if (lane == j) id = last_e;
+  }
+  return id;
+}
+
+// L lanes per token.  kScored: keys or group values are sigmoid scores; kVec:
+// a lane's eight experts are whole 16-byte vectors.  With groups a lane's
+// experts are a run of E / L inside one group (L / G lanes per group);
+// without, the lanes' batches of eight interleave.
+template <typename T, int L, bool kScored, bool kVec>
+__global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopkParams p) {
+  griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
+  constexpr bool kRest = kScored || sizeof(T) == 4;    // packed keys may lose bits
+  constexpr int kTok = 32 / L;                         // tokens per warp
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const int E = p.num_experts, k = p.top_k;
+  const uint32_t imask = p.index_mask;
+  const bool grouped = p.num_groups > 1;
+  const int first = grouped ? sub * (E / L) : sub * 8;
+  const int end = grouped ? first + E / L : E, step = grouped ? 8 : 8 * L;
+  const int64_t stride = (int64_t)gridDim.x * kRouterWarps * kTok;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5)) * kTok; t0 < p.tokens; t0 += stride) {
+    const int64_t t = t0 + lane / L;
+    const bool live = t < p.tokens;
+    const T *row = reinterpret_cast<const T *>(p.logits) + (live ? t : t0) * p.ld;
+    uint32_t run[8], rest = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) run[i] = 0u;
+    float t1 = -INFINITY, t2 = -INFINITY, row_max = -INFINITY;
+    for (int e0 = first; e0 < end; e0 += step) {
+      float x[8];
+      load_eight<T, kVec>(row + e0, end - e0, x);
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = kVec ? e0 + i : min(e0 + i, E - 1);
+        float g;
+        const uint32_t u = route_key<kScored>(p, e, x[i], g);
+        v[i] = u ? (u & ~imask) | (imask - (uint32_t)e) : 0u;
+        if (grouped) {
+          t2 = fmaxf(t2, fminf(t1, g));
+          t1 = fmaxf(t1, g);
+        }
+        if (!kScored && p.need_row_sum) row_max = fmaxf(row_max, finite_top(x[i]));   // (fmaxf passes over NaN)
+      }
+      sort8(v);
+      merge8<kRest>(run, v, rest);
+    }
+    uint32_t keep = 0xffffffffu;       // groups that stay, bit g
+    if (grouped) {
+      const int G = p.num_groups, per = L / G;       // lanes per group, a power of two
+      for (int o = 1; o < per; o <<= 1) {
+        const float o1 = __shfl_xor_sync(kAll, t1, o), o2 = __shfl_xor_sync(kAll, t2, o);
+        t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+        t1 = fmaxf(t1, o1);
+      }
+      const float score = p.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+      const int g = sub / per;
+      int better = 0;
+      keep = 0u;
+      for (int j = 0; j < G; ++j) {
+        const float sj = __shfl_sync(kAll, score, (lane - sub) + j * per);
+        better += sj > score || (sj == score && j < g);
+      }
+      const uint32_t votes = __ballot_sync(kAll, better < p.topk_groups);
+      for (int j = 0; j < G; ++j) keep |= ((votes >> ((lane - sub) + j * per)) & 1u) << j;
+      if (better >= p.topk_groups) {
+        rest = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) run[i] = 0u;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __shfl_xor_sync(kAll, run[i], o);
+      if (kRest) rest = max(rest, __shfl_xor_sync(kAll, rest, o));
+      merge8<kRest>(run, v, rest);
+    }
+    // this lane's choices: slots sub, sub + L, ... (two for L = 4)
+    constexpr int kSlots = L >= 8 ? 1 : 8 / L;
+    int id[kSlots];
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i == sub + q * L) m = run[i];
+      id[q] = m && sub + q * L < k ? (int)(imask - (m & imask)) : -1;
+    }
+    if constexpr (kRest) {
+      bool close = false;              // two neighbours agree in the bits that are left
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t below = i < 7 ? run[i < 7 ? i + 1 : 7] : rest;
+        close |= i < k && below && ((run[i] ^ below) & ~imask) == 0u;
+      }
+      uint32_t again = __ballot_sync(kAll, close && live && sub == 0);
+      while (again) {
+        const int src = __ffs(again) - 1;            // the token's first lane
+        again &= again - 1;
+        const T *r = reinterpret_cast<const T *>(p.logits) + (t0 + src / L) * p.ld;
+        const int e = route_exact<T, kScored>(p, r, __shfl_sync(kAll, keep, src));
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+          const int v = __shfl_sync(kAll, e, (sub + q * L) & 31);
+          if (lane - sub == src) id[q] = sub + q * L < k ? v : -1;
+        }
+      }
+    }
+    const auto sum_tok = [](float v) {
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+      return v;
+    };
+    const auto max_tok = [](float v) {
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+      return v;
+    };
+    float w[kSlots], total = 0.0f;
+    if (p.softmax) {
+      float xs[kSlots], m = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        xs[q] = id[q] >= 0 ? finite_top(load1(row + id[q])) : -INFINITY;
+        m = fmaxf(m, xs[q]);
+      }
+      if (p.need_row_sum) m = row_max;
+      m = max_tok(m);
+      if (!(m > -INFINITY)) m = 0.0f;
+      if (p.need_row_sum) {            // the scores' denominator: the whole row
+        for (int e0 = first; e0 < end; e0 += step) {
+          float x[8];
+          load_eight<T, kVec>(row + e0, end - e0, x);
+          // (exp2 approximations: the terms that count are within a few of m)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (x[i] > -INFINITY) total += __expf(finite_top(x[i]) - m);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        w[q] = id[q] >= 0 ? expf(xs[q] - m) : 0.0f;
+        if (!p.need_row_sum) total += w[q];
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        w[q] = id[q] >= 0 ? sigmoid(load1(row + id[q])) : 0.0f;
+        total += w[q];
+      }
+    }
+    total = sum_tok(total);
+    const bool divide = p.softmax || p.renormalize;
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      const int slot = sub + q * L;
+      if (divide) w[q] = total > 0.0f ? w[q] / total : 0.0f;
+      if (live && slot < k) {
+        p.expert_ids[t * k + slot] = id[q];
+        p.weights[t * k + slot] = w[q] * p.scale;
+      }
+    }
+  }
+}
+
 // ----------------------------------------------------------------- gradient --
 // With d_j = scale * grad_w_j (0 for an id outside [0, E)) and the choice held fixed:
 //   sigmoid:  ds_j = renormalize ? (d_j - sum_i d_i w_i) / S : d_j,  w_i = s_i / S,  S = sum_i s_i
@@ -282,86 +549,104 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk(const RouteTop
 //   softmax, renormalized: the weights are the softmax over the chosen logits:
 //             dx_j = w_j (d_j - sum_i d_i w_i) on the chosen experts, 0 elsewhere
 //   softmax:  dx_e = p_e (d_e - sum_j d_j p_j) for every expert
-// Each row of grad_logits is written whole: a warp lays its row out in shared
-// memory (zeros, the chosen experts' values on top) and stores it in 16-byte
-// vectors.  HBM-bound on that write (and, in the last form, the logits' read).
-template <typename T, bool kVec, bool kDense>
+// L lanes per token (8, or a warp where top_k > 8).  The row is written whole
+// in 16-byte vectors -- zeros, or p_e times minus the dot product (kDense) --
+// and the chosen experts' elements over it.  HBM-bound: that write and, with
+// kDense, the read of the logits (the second pass over them hits the caches).
+// The exponentials of the dense form are exp2 approximations (__expf): with
+// |x - max| < 64 their relative error stays below 2^-17.
+template <typename T, int L, bool kVec, bool kDense>
 __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const RouteGradParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
-  extern __shared__ __align__(16) uint8_t sh_grad[];
   constexpr int VEC = kVec ? 16 / (int)sizeof(T) : 1;
-  const int lane = threadIdx.x & 31;
+  constexpr int kTok = 32 / L;
+  const int lane = threadIdx.x & 31, sub = lane % L;
   const int E = p.num_experts, k = p.top_k;
-  // kDense: fp32 d_e of every expert; else the finished row in T
-  using B = typename std::conditional<kDense, float, T>::type;
-  B *buf = reinterpret_cast<B *>(sh_grad + (size_t)(threadIdx.x >> 5) * p.row_bytes);
-  for (int e = lane; e < E; e += 32) store1(buf + e, 0.0f);
-  __syncwarp();
-  for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < p.tokens;
-       t += (int64_t)gridDim.x * kRouterWarps) {
-    const T *row = reinterpret_cast<const T *>(p.logits) + t * p.ld;
-    T *out = reinterpret_cast<T *>(p.grad_logits) + t * p.ld_grad;
-    int id = lane < k ? __ldg(p.expert_ids + t * k + lane) : -1;
+  const auto sum_tok = [](float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  };
+  const auto max_tok = [](float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+  };
+  const int64_t stride = (int64_t)gridDim.x * kRouterWarps * kTok;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5)) * kTok; t0 < p.tokens; t0 += stride) {
+    const int64_t t = t0 + lane / L;
+    const bool live = t < p.tokens;
+    const T *row = reinterpret_cast<const T *>(p.logits) + (live ? t : t0) * p.ld;
+    T *out = reinterpret_cast<T *>(p.grad_logits) + (live ? t : t0) * p.ld_grad;
+    int id = live && sub < k ? __ldg(p.expert_ids + t * k + sub) : -1;
     if (id >= E) id = -1;
-    const float d = id >= 0 ? __ldg(p.grad_weights + t * k + lane) * p.scale : 0.0f;
+    const float d = id >= 0 ? __ldg(p.grad_weights + t * k + sub) * p.scale : 0.0f;
     const float xs = id >= 0 ? load1(row + id) : -INFINITY;
+    float g = 0.0f;                    // of the chosen expert
     if constexpr (kDense) {
-      float m = -INFINITY;
-      for (int e = lane * VEC; e < E; e += 32 * VEC) {
-        float x[VEC];
+      // running maximum and sum of the lane's part of the row, then of the token
+      float m = -INFINITY, s = 0.0f;
+      for (int e = sub * VEC; e < E; e += L * VEC) {
+        float x[VEC], top = m;
         load_vec<VEC>(row + e, x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (x[i] > m) m = finite_top(x[i]);
-      }
-      m = warp_max(m);
-      if (!(m > -INFINITY)) m = 0.0f;      // an empty row: every p is 0
-      float s = 0.0f;
-      for (int e = lane * VEC; e < E; e += 32 * VEC) {
-        float x[VEC];
-        load_vec<VEC>(row + e, x);
+        for (int i = 0; i < VEC; ++i) {
+          x[i] = finite_top(x[i]);
+          top = fmaxf(top, x[i]);
+        }
+        if (top > -INFINITY) {
+          s *= __expf(m - top);
+          m = top;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (x[i] > -INFINITY) s += expf(finite_top(x[i]) - m);
-      }
-      s = warp_sum(s);
-      const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-      const float ps = xs > -INFINITY ? expf(finite_top(xs) - m) * inv : 0.0f;
-      const float dot = warp_sum(d * ps);
-      if (id >= 0) buf[id] = d;
-      __syncwarp();
-      for (int e = lane * VEC; e < E; e += 32 * VEC) {
-        float x[VEC];
-        load_vec<VEC>(row + e, x);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          x[i] = x[i] > -INFINITY ? expf(finite_top(x[i]) - m) * inv * (buf[e + i] - dot) : 0.0f;
-        if constexpr (VEC == 8) {
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t *>(&h);
-          }
-          *reinterpret_cast<uint4 *>(out + e) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else if constexpr (VEC == 4) {
-          *reinterpret_cast<float4 *>(out + e) = make_float4(x[0], x[1], x[2], x[3]);
-        } else {
-          store1(out + e, x[0]);
+          for (int i = 0; i < VEC; ++i)
+            if (x[i] > -INFINITY) s += __expf(x[i] - m);
         }
       }
-      __syncwarp();
-      if (id >= 0) buf[id] = 0.0f;
-      __syncwarp();
+      const float top = max_tok(m);
+      const float mt = top > -INFINITY ? top : 0.0f;          // an empty row: every p is 0
+      s = sum_tok(m > -INFINITY ? s * __expf(m - mt) : 0.0f);
+      const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+      const float ps = xs > -INFINITY ? __expf(finite_top(xs) - mt) * inv : 0.0f;
+      const float dot = sum_tok(d * ps);
+      g = ps * (d - dot);
+      if (live) {
+        const float c = -dot * inv;
+        for (int e = sub * VEC; e < E; e += L * VEC) {
+          float x[VEC];
+          load_vec<VEC>(row + e, x);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) x[i] = x[i] > -INFINITY ? __expf(finite_top(x[i]) - mt) * c : 0.0f;
+          if constexpr (VEC == 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+              o[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(out + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          } else if constexpr (VEC == 4) {
+            *reinterpret_cast<float4 *>(out + e) = make_float4(x[0], x[1], x[2], x[3]);
+          } else {
+            store1(out + e, x[0]);
+          }
+        }
+      }
     } else {
-      float g = 0.0f;
+      if (live) {
+        for (int e = sub * VEC; e < E; e += L * VEC) {
+          if constexpr (kVec)
+            *reinterpret_cast<uint4 *>(out + e) = make_uint4(0, 0, 0, 0);
+          else
+            store1(out + e, 0.0f);
+        }
+      }
       if (p.softmax) {                       // renormalized
-        const float m = warp_max(finite_top(xs));
+        const float m = max_tok(finite_top(xs));
         const float e = xs > -INFINITY ? expf(finite_top(xs) - m) : 0.0f;
-        const float s = warp_sum(e);
+        const float s = sum_tok(e);
         const float w = s > 0.0f ? e / s : 0.0f;
-        const float c = warp_sum(d * w);
+        const float c = sum_tok(d * w);
         g = w * (d - c);
       } else {
         // s (1 - s) from exp(-|x|): 1 - s would cancel for large x
@@ -370,25 +655,16 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
         if (p.renormalize) {
           // slope / S <= 1 whatever the size of S: 1 / S alone may overflow
           const float s = id >= 0 ? sigmoid(xs) : 0.0f;
-          const float S = warp_sum(s);
-          const float c = warp_sum(S > 0.0f ? d * (s / S) : 0.0f);
+          const float S = sum_tok(s);
+          const float c = sum_tok(S > 0.0f ? d * (s / S) : 0.0f);
           g = id >= 0 && S > 0.0f ? (d - c) * (slope / S) : 0.0f;
         } else {
           g = id >= 0 ? d * slope : 0.0f;
         }
       }
-      if (id >= 0) store1(buf + id, g);
-      __syncwarp();
-      if constexpr (kVec) {
-        for (int e = lane * VEC; e < E; e += 32 * VEC)
-          *reinterpret_cast<uint4 *>(out + e) = *reinterpret_cast<const uint4 *>(buf + e);
-      } else {
-        for (int e = lane; e < E; e += 32) out[e] = buf[e];
-      }
-      __syncwarp();
-      if (id >= 0) store1(buf + id, 0.0f);
-      __syncwarp();
     }
+    __syncwarp();      // the row's stores come before the chosen experts'
+    if (id >= 0) store1(out + id, g);
   }
 }
 
@@ -396,7 +672,42 @@ template <typename T, int VEC, int NCH>
 cudaError_t launch_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   const size_t smem = p.num_groups > 1 ? (size_t)kRouterWarps * p.num_experts * 4 : 0;   // <= 32 KB
   const int64_t ctas = std::min<int64_t>((p.tokens + kRouterWarps - 1) / kRouterWarps, (int64_t)num_sms * 8);
-  return launch_pdl(k_route_topk<T, VEC, NCH>, dim3((unsigned)ctas), dim3(kRouterWarps * 32), smem, st, p);
+  return launch_pdl(k_route_any<T, VEC, NCH>, dim3((unsigned)ctas), dim3(kRouterWarps * 32), smem, st, p);
+}
+
+// Lanes per token: enough warps for the device (16 per SM) with as few lanes
+// as that takes -- every halving of L saves a merge and its shuffles per token
+// -- but at least eight experts per lane; with groups, whole lanes per group.
+template <typename T, int L, bool kScored>
+cudaError_t launch_few(const RouteTopkParams &p, bool vec, int num_sms, cudaStream_t st) {
+  const int64_t per_cta = (int64_t)kRouterWarps * (32 / L);
+  const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
+  const dim3 grid((unsigned)ctas), block(kRouterWarps * 32);
+  return vec ? launch_pdl(k_route_few<T, L, kScored, true>, grid, block, 0, st, p)
+             : launch_pdl(k_route_few<T, L, kScored, false>, grid, block, 0, st, p);
+}
+template <typename T, bool kScored>
+cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
+  const int E = p.num_experts, G = p.num_groups;
+  int L = 32;
+  while (L > 4 && (L > G || G == 1) && (p.tokens * (L / 2) >= (int64_t)num_sms * 16 * 32 || E < 8 * L)) L /= 2;
+  L = std::max(L, G);
+  const bool vec = E % 8 == 0 && (G == 1 || E / L % 8 == 0) && p.ld * sizeof(T) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
+  switch (L) {
+    case 4: return launch_few<T, 4, kScored>(p, vec, num_sms, st);
+    case 8: return launch_few<T, 8, kScored>(p, vec, num_sms, st);
+    case 16: return launch_few<T, 16, kScored>(p, vec, num_sms, st);
+    default: return launch_few<T, 32, kScored>(p, vec, num_sms, st);
+  }
+}
+// The forms that k_route_few takes: up to 8 choices; keys that need no row
+// statistics; groups that are whole lanes (a power of two of them, E / 32
+// experts or more each, so that a lane count from G to 32 divides E).
+bool takes_few(const RouteTopkParams &p) {
+  if (p.top_k > 8 || (p.softmax && (p.bias || p.rank_by_score))) return false;
+  const int G = p.num_groups;
+  return G == 1 || ((G & (G - 1)) == 0 && p.num_experts % 32 == 0);
 }
 
 // Values per lane by the number of experts; vector loads where the rows allow
@@ -404,6 +715,9 @@ cudaError_t launch_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) 
 template <typename T>
 cudaError_t pick_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   const int E = p.num_experts;
+  if (takes_few(p))
+    return !p.softmax && (p.bias || p.rank_by_score) ? pick_few<T, true>(p, num_sms, st)
+                                                     : pick_few<T, false>(p, num_sms, st);
   const auto vec_ok = [&](int vec) {
     return E % vec == 0 && p.ld % vec == 0 && reinterpret_cast<uintptr_t>(p.logits) % (vec * sizeof(T)) == 0;
   };
@@ -423,23 +737,21 @@ cudaError_t pick_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   return launch_topk<T, 1, 32>(p, num_sms, st);
 }
 
-template <typename T>
-cudaError_t pick_grad(const RouteGradParams &p0, int num_sms, cudaStream_t st) {
-  RouteGradParams p = p0;
+template <typename T, int L>
+cudaError_t pick_grad(const RouteGradParams &p, int num_sms, cudaStream_t st) {
   constexpr int vec = 16 / (int)sizeof(T);
   const bool dense = p.softmax && !p.renormalize;
   const bool v = p.num_experts % vec == 0 && p.ld % vec == 0 && p.ld_grad % vec == 0 &&
                  reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
                  reinterpret_cast<uintptr_t>(p.grad_logits) % 16 == 0;
-  p.row_bytes = (int)(((size_t)p.num_experts * (dense ? 4 : sizeof(T)) + 15) / 16 * 16);
-  const size_t smem = (size_t)kRouterWarps * p.row_bytes;   // <= 32 KB
-  const int64_t ctas = std::min<int64_t>((p.tokens + kRouterWarps - 1) / kRouterWarps, (int64_t)num_sms * 8);
+  const int64_t per_cta = (int64_t)kRouterWarps * (32 / L);
+  const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
   const dim3 grid((unsigned)ctas), block(kRouterWarps * 32);
   if (dense)
-    return v ? launch_pdl(k_route_topk_backward<T, true, true>, grid, block, smem, st, p)
-             : launch_pdl(k_route_topk_backward<T, false, true>, grid, block, smem, st, p);
-  return v ? launch_pdl(k_route_topk_backward<T, true, false>, grid, block, smem, st, p)
-           : launch_pdl(k_route_topk_backward<T, false, false>, grid, block, smem, st, p);
+    return v ? launch_pdl(k_route_topk_backward<T, L, true, true>, grid, block, 0, st, p)
+             : launch_pdl(k_route_topk_backward<T, L, false, true>, grid, block, 0, st, p);
+  return v ? launch_pdl(k_route_topk_backward<T, L, true, false>, grid, block, 0, st, p)
+           : launch_pdl(k_route_topk_backward<T, L, false, false>, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -448,7 +760,9 @@ cudaError_t launch_route_topk(const RouteTopkParams &p, bool bf16, int num_sms, 
   return bf16 ? pick_topk<__nv_bfloat16>(p, num_sms, st) : pick_topk<float>(p, num_sms, st);
 }
 cudaError_t launch_route_topk_backward(const RouteGradParams &p, bool bf16, int num_sms, cudaStream_t st) {
-  return bf16 ? pick_grad<__nv_bfloat16>(p, num_sms, st) : pick_grad<float>(p, num_sms, st);
+  if (p.top_k <= 8)
+    return bf16 ? pick_grad<__nv_bfloat16, 8>(p, num_sms, st) : pick_grad<float, 8>(p, num_sms, st);
+  return bf16 ? pick_grad<__nv_bfloat16, 32>(p, num_sms, st) : pick_grad<float, 32>(p, num_sms, st);
 }
 
 }  // namespace nvfp4
