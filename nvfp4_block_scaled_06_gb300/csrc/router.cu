@@ -55,6 +55,12 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 __device__ __forceinline__ float load1(const float *p) { return __ldg(p); }
@@ -331,6 +337,41 @@ __device__ __forceinline__ void load_eight(const T *p, int n, float (&x)[8]) {
   }
 }
 
+// The packed keys of eight experts from e0 (a multiple of 8) on, keys that are
+// the logits, without a look at infinities and NaNs: positive ones and +inf
+// land at or above 0xFF800000, -inf and the negative ones below 0x00800000,
+// where the caller finds them if they were chosen.
+__device__ __forceinline__ void plain_keys(const float *p, int e0, uint32_t imask, uint32_t (&v)[8], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) load_vec<4>(p + i, x + i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(x[i] + 0.0f);                      // -0 counts as +0
+    const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    v[i] = (u & ~imask) | (imask - (uint32_t)(e0 + i));
+  }
+}
+// bf16: two experts per word until the index comes in below their 16 bits.
+__device__ __forceinline__ void plain_keys(const __nv_bfloat16 *p, int e0, uint32_t imask, uint32_t (&v)[8],
+                                           float (&x)[8]) {
+  const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  const uint32_t index = (imask - (uint32_t)e0) * 0x00010001u - 0x00010000u;   // low half: expert e0, high: e0 + 1
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t b;                                                           // x * 1 + 0: -0 becomes +0
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(b) : "r"(w[j]), "r"(0x3F803F80u), "r"(0u));
+    uint32_t sign;                                                        // each half's sign, 16 times
+    asm("prmt.b32 %0, %1, %2, 0xBB99;" : "=r"(sign) : "r"(b), "r"(0u));
+    const uint32_t u = b ^ (sign | 0x80008000u);
+    const uint32_t at = index - 0x00020002u * j;
+    v[2 * j] = __byte_perm(u, at, 0x1054);
+    v[2 * j + 1] = __byte_perm(u, at, 0x3276);
+    x[2 * j] = bf16lo(w[j]);
+    x[2 * j + 1] = bf16hi(w[j]);
+  }
+}
+
 // The key and the value that groups are ranked by, of expert e.
 template <bool kScored>
 __device__ __forceinline__ uint32_t route_key(const RouteTopkParams &p, int e, float x, float &gval) {
@@ -387,6 +428,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   constexpr bool kRest = kScored || sizeof(T) == 4;    // packed keys may lose bits
+  constexpr bool kPlain = !kScored && kVec;            // keys without a look at infinities and NaNs
   constexpr int kTok = 32 / L;                         // tokens per warp
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int E = p.num_experts, k = p.top_k;
@@ -405,8 +447,27 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
     float t1 = -INFINITY, t2 = -INFINITY, row_max = -INFINITY;
     for (int e0 = first; e0 < end; e0 += step) {
       float x[8];
-      load_eight<T, kVec>(row + e0, end - e0, x);
       uint32_t v[8];
+      if constexpr (kPlain) {
+        plain_keys(row + e0, e0, imask, v, x);
+        if (grouped) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float g = x[i] > -INFINITY ? x[i] : -INFINITY;
+            t2 = fmaxf(t2, fminf(t1, g));
+            t1 = fmaxf(t1, g);
+          }
+        }
+        if (p.need_row_sum) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) row_max = fmaxf(row_max, x[i]);         // (fmaxf passes over NaN)
+          row_max = finite_top(row_max);
+        }
+        sort8(v);
+        merge8<kRest>(run, v, rest);
+        continue;
+      }
+      load_eight<T, kVec>(row + e0, end - e0, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = kVec ? e0 + i : min(e0 + i, E - 1);
@@ -465,12 +526,14 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
         if (i == sub + q * L) m = run[i];
       id[q] = m && sub + q * L < k ? (int)(imask - (m & imask)) : -1;
     }
-    if constexpr (kRest) {
-      bool close = false;              // two neighbours agree in the bits that are left
+    if constexpr (kRest || kPlain) {
+      bool close = kPlain && run[0] >= 0xFF800000u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t below = i < 7 ? run[i < 7 ? i + 1 : 7] : rest;
-        close |= i < k && below && ((run[i] ^ below) & ~imask) == 0u;
+        if (kPlain) close |= i < k && run[i] < 0x00800000u;
+        // two neighbours agree in the bits that are left
+        if (kRest) close |= i < k && below && ((run[i] ^ below) & ~imask) == 0u;
       }
       uint32_t again = __ballot_sync(kAll, close && live && sub == 0);
       while (again) {
@@ -549,12 +612,14 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
 //   softmax, renormalized: the weights are the softmax over the chosen logits:
 //             dx_j = w_j (d_j - sum_i d_i w_i) on the chosen experts, 0 elsewhere
 //   softmax:  dx_e = p_e (d_e - sum_j d_j p_j) for every expert
-// L lanes per token (8, or a warp where top_k > 8).  The row is written whole
-// in 16-byte vectors -- zeros, or p_e times minus the dot product (kDense) --
-// and the chosen experts' elements over it.  HBM-bound: that write and, with
-// kDense, the read of the logits (the second pass over them hits the caches).
-// The exponentials of the dense form are exp2 approximations (__expf): with
-// |x - max| < 64 their relative error stays below 2^-17.
+// L lanes per token (8, or a warp where top_k > 8 or E > 256).  The row is
+// written whole in 16-byte vectors -- zeros, or p_e times minus the dot product
+// (kDense) -- and the chosen experts' elements over it.  HBM-bound: that write
+// and, with kDense, the read of the logits.  This kernel serves the sparse
+// forms, and the dense one for rows that are not whole 16-byte vectors.
+// The exponentials of the dense form are exp2 approximations: with |x - max| <
+// 64 their relative error stays below 2^-17 (most of it the rounding of the
+// exponent's argument, which is why it is small where the term is large).
 template <typename T, int L, bool kVec, bool kDense>
 __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const RouteGradParams p) {
   griddep_launch_dependents();
@@ -668,6 +733,96 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
   }
 }
 
+// The dense softmax form with the row in registers: 32 / VEC vectors per lane
+// (L = 8: up to 256 experts, L = 32: up to 1024), one exponential per element.
+// The first attempt takes every logit for finite; a row for which that shows
+// to be wrong (the maximum infinite, the sum NaN) sends its warp through a
+// second one that masks -inf and NaN and takes +inf for the largest fp32.
+template <typename T, int L>
+__global__ void __launch_bounds__(kRouterWarps * 32) k_route_softmax_backward(const RouteGradParams p) {
+  griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
+  constexpr int VEC = 16 / (int)sizeof(T), NV = 32 / VEC, kTok = 32 / L;
+  constexpr float kLog2e = 1.44269504f;
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const int E = p.num_experts, k = p.top_k;
+  const auto sum_tok = [](float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  };
+  const int64_t stride = (int64_t)gridDim.x * kRouterWarps * kTok;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5)) * kTok; t0 < p.tokens; t0 += stride) {
+    const int64_t t = t0 + lane / L;
+    const bool live = t < p.tokens;
+    const T *row = reinterpret_cast<const T *>(p.logits) + (live ? t : t0) * p.ld;
+    T *out = reinterpret_cast<T *>(p.grad_logits) + (live ? t : t0) * p.ld_grad;
+    int id = live && sub < k ? __ldg(p.expert_ids + t * k + sub) : -1;
+    if (id >= E) id = -1;
+    const float d = id >= 0 ? __ldg(p.grad_weights + t * k + sub) * p.scale : 0.0f;
+    const float xs = id >= 0 ? load1(row + id) : -INFINITY;
+    float x[NV][VEC], m, s, ps;
+    for (int attempt = 0;; ++attempt) {
+      m = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int e = (v * L + sub) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[v][i] = -INFINITY;
+        if (v * L * VEC >= E) continue;
+        if (e < E) load_vec<VEC>(row + e, x[v]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (attempt) x[v][i] = x[v][i] > -INFINITY ? finite_top(x[v][i]) : -INFINITY;
+          m = fmaxf(m, x[v][i]);
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+      if (attempt && !(m > -INFINITY)) m = 0.0f;         // an empty row: every p is 0
+      const float shift = m * kLog2e;
+      s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (v * L * VEC >= E) continue;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          x[v][i] = attempt ? __expf(x[v][i] - m) : exp2_approx(fmaf(x[v][i], kLog2e, -shift));
+          s += x[v][i];
+        }
+      }
+      s = sum_tok(s);
+      ps = attempt ? (xs > -INFINITY ? __expf(finite_top(xs) - m) : 0.0f) : exp2_approx(fmaf(xs, kLog2e, -shift));
+      if (attempt || __all_sync(kAll, m <= FLT_MAX && s <= FLT_MAX)) break;   // (a NaN compares false)
+    }
+    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    ps *= inv;
+    const float dot = sum_tok(d * ps);
+    const float c = -dot * inv;
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int e = (v * L + sub) * VEC;
+        if (e >= E) continue;
+        if constexpr (VEC == 8) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[v][2 * i] * c, x[v][2 * i + 1] * c);
+            o[i] = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          *reinterpret_cast<uint4 *>(out + e) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          *reinterpret_cast<float4 *>(out + e) =
+              make_float4(x[v][0] * c, x[v][1] * c, x[v][2] * c, x[v][3] * c);
+        }
+      }
+    }
+    __syncwarp();      // the row's stores come before the chosen experts'
+    if (id >= 0) store1(out + id, ps * (d - dot));
+  }
+}
+
 template <typename T, int VEC, int NCH>
 cudaError_t launch_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   const size_t smem = p.num_groups > 1 ? (size_t)kRouterWarps * p.num_experts * 4 : 0;   // <= 32 KB
@@ -748,7 +903,7 @@ cudaError_t pick_grad(const RouteGradParams &p, int num_sms, cudaStream_t st) {
   const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
   const dim3 grid((unsigned)ctas), block(kRouterWarps * 32);
   if (dense)
-    return v ? launch_pdl(k_route_topk_backward<T, L, true, true>, grid, block, 0, st, p)
+    return v ? launch_pdl(k_route_softmax_backward<T, L>, grid, block, 0, st, p)
              : launch_pdl(k_route_topk_backward<T, L, false, true>, grid, block, 0, st, p);
   return v ? launch_pdl(k_route_topk_backward<T, L, true, false>, grid, block, 0, st, p)
            : launch_pdl(k_route_topk_backward<T, L, false, false>, grid, block, 0, st, p);
@@ -760,7 +915,7 @@ cudaError_t launch_route_topk(const RouteTopkParams &p, bool bf16, int num_sms, 
   return bf16 ? pick_topk<__nv_bfloat16>(p, num_sms, st) : pick_topk<float>(p, num_sms, st);
 }
 cudaError_t launch_route_topk_backward(const RouteGradParams &p, bool bf16, int num_sms, cudaStream_t st) {
-  if (p.top_k <= 8)
+  if (p.top_k <= 8 && p.num_experts <= 256)
     return bf16 ? pick_grad<__nv_bfloat16, 8>(p, num_sms, st) : pick_grad<float, 8>(p, num_sms, st);
   return bf16 ? pick_grad<__nv_bfloat16, 32>(p, num_sms, st) : pick_grad<float, 32>(p, num_sms, st);
 }
