@@ -483,10 +483,10 @@ nvfp4_status run_gemm(const nvfp4_gemm_args *a, const GemmPlan &pl, int sms, cud
   p.stall_probe = tmo == 0;
   if (pl.skinny) {
     // the activation rows as the MMA's B operand: boxes of 32 rows of the
-    // 128-row padded buffer; the weights keep their 128-row boxes
+    // 128-row padded buffer; the weights' 128-row tiles come in two boxes
     CUtensorMap mx;
     if (!map2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, a->K / 2, a_rows, a->K / 2, 128, 32) ||
-        !map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, 128))
+        !map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, 64))
       return NVFP4_ERR_CUDA;
     p.tiles_n = (int)ceil_div(a->N, 128);
     if (cudaError_t e_ = mark(a->prof_begin, st); e_ != cudaSuccess) return cuda_status(e_);
@@ -612,6 +612,7 @@ struct GroupedProducts {
   void *d;                        // [P][N], bf16 or fp32
   int out_fp32;
   int mx = 0;                     // MXFP4 operands (no global scales, no LoRA)
+  bool few_rows = false;          // MXFP4: the operand-swapped kernel, 32 rows of an expert at a time
   void *prof_begin, *prof_end;
 };
 
@@ -678,7 +679,17 @@ nvfp4_status run_grouped_products(const GroupedProducts &g, int *status, uint64_
   p.timeout_ns = tmo;
   p.stall_probe = tmo == 0;
   if (cudaError_t e_ = mark(g.prof_begin, st); e_ != cudaSuccess) return cuda_status(e_);
-  cudaError_t e = launch_gemm_fp4(p, maps, bn, sms, st);
+  cudaError_t e;
+  if (g.few_rows) {
+    CUtensorMap mx;
+    if (!map2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.aq, g.K / 2, g.prow_max, g.K / 2, 128, 32) ||
+        !map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, g.E * g.N, g.K / 2, 128, 64))
+      return NVFP4_ERR_CUDA;
+    p.tiles_n = (int)(g.N / 128);
+    e = launch_gemm_fp4_skinny(p, mx, maps.b, sms, st);
+  } else {
+    e = launch_gemm_fp4(p, maps, bn, sms, st);
+  }
   if (e == cudaSuccess) e = mark(g.prof_end, st);
   return cuda_status(e);
 }
@@ -1442,7 +1453,7 @@ nvfp4_status run_mx_gemm(const nvfp4_mxfp4_gemm_args *a, const MxGemmPlan &pl, i
   // A quantized in the call spans the padded rows of its buffer: whatever codes
   // they hold, with scale byte 0, stay in accumulator rows that are not stored
   const int64_t a_rows = a->a_bf16 ? pad_up(a->M, 128) : a->M;
-  const int b_box = pl.pair || pl.skinny ? 128 : pl.bn;
+  const int b_box = pl.skinny ? 64 : pl.pair ? 128 : pl.bn;
   GemmMaps maps;
   if (!map2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, a->K / 2, a_rows, a->K / 2, 128, pl.skinny ? 32 : 128) ||
       !map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, b_box))
@@ -1549,6 +1560,11 @@ void plan_mx_grouped(const nvfp4_mxfp4_grouped_args *a, MxGroupedPlan *pl) {
   pl->xsf = c.take<uint8_t>(mx_sf_swizzled_bytes(pl->prow_max, a->K));
   pl->ws = c.off;
 }
+
+// Decode: few rows per expert on average, and no more than 512 on any (an expert
+// gets a token once): the operand-swapped kernel, whose stages hold weights
+// instead of padding rows.
+bool mx_few_rows(int64_t T, int64_t k, int64_t E) { return T <= 512 && T * k <= 16 * E; }
 
 // The sizes that both routed MXFP4 calls take.
 nvfp4_status validate_mx_experts(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
@@ -1668,6 +1684,7 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
   gp.d = a->d;
   gp.out_fp32 = a->out_dtype == NVFP4_OUT_FP32;
   gp.mx = 1;
+  gp.few_rows = mx_few_rows(a->num_tokens, a->top_k, a->num_experts);
   gp.prof_begin = a->prof_begin;
   gp.prof_end = a->prof_end;
   return run_grouped_products(gp, status, g_timeout_ns.load(), sms, st);
@@ -1745,6 +1762,7 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
   gp.w_sf = a->w_sf;
   gp.d = pl.d;
   gp.mx = 1;
+  gp.few_rows = mx_few_rows(a->num_tokens, a->top_k, a->num_experts);
   gp.prof_begin = a->prof_begin;
   gp.prof_end = a->prof_end;
   nvfp4_status s = run_grouped_products(gp, status, g_timeout_ns.load(), sms, st);

@@ -12,22 +12,32 @@
 // of weights -- are in flight per SM instead of the six (96 KB) of the
 // 128 x 128 tile whose A side would be the padded activation rows.
 //
-// A persistent kernel, one CTA per SM, 192 threads:
-//   warp 0      producer (one thread): the stage's weight tile (128 rows x
-//               256 codes) and activation tile (32 rows x 256 codes) by
-//               TMA, their scale atoms by bulk copy.
+// A persistent kernel, one CTA per SM (grouped: two), 384 threads:
+//   warps 0, 10, 11  producers (one thread each): the stage's weight tile (128
+//               rows x 256 codes) in two halves by TMA; the activation tile (32
+//               rows x 256 codes) by TMA and the scale atoms by bulk copy.
+//               (One warp's tile loads arrive at about 24 B/cycle per SM, 40 us
+//               for 214 MB of weights: the stream needs more issuing warps.)
 //   warp 1      MMA issue (one thread): kind::mxf4nvf4 scale_vec::4X, M=128,
 //               N=32, K=64, four per stage.
-//   warps 2..5  scales -> tensor memory for every stage; after a unit's last
-//               stage they drain the 128 x 32 accumulator and store Y (or the
-//               unit's fp32 split-K partial) transposed: lane = feature n,
-//               one store per activation row, coalesced across the warp.
+//   warps 2..5  scales -> tensor memory for every stage.
+//   warps 6..9  drain a unit's 128 x 32 accumulator (two of them, so that the
+//               next unit's MMAs go on) and store Y (or the unit's fp32 split-K
+//               partial) transposed: lane = feature n, one store per
+//               activation row, coalesced across the warp.
 // Work units are (128-feature tile, K range); K ranges are summed in order by
 // the split-K pass.  Every wait is bounded.
 //
 // MX: the same kernel for MXFP4 operands (one E8M0 scale per 32 elements): a
 // stage has two scale atoms per operand instead of four, and the MMA (kind::mxf4
 // scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
+//
+// GROUPED (MXFP4 experts at decode): a unit is a 128-feature tile of one
+// expert's weights against 32 of its routed rows, taken from the m-tile table
+// (four such row groups per 128-row tile, those without rows skipped), so the
+// experts' weights, not the padding of their rows, fill the stages: 32 tokens'
+// top 8 of 32 experts (N 6144, K 2048, 214 MB of weights) against the 128 x 256
+// tiles' 43.5 us.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -35,23 +45,31 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kSkThreads = 192;
-constexpr int kSkStages = 9;
+constexpr int kSkThreads = 384;
+// Dense: nine stages, one CTA per SM (four and two CTAs: one to two units per
+// CTA, o_proj 16.6 instead of 15.8 us).  Grouped: four, so that two CTAs fit an
+// SM (and its tensor memory) and the units of one, about five, hide the other's
+// starts and drains: 38 instead of 42.5 us.
+constexpr int sk_stages(bool grouped) { return grouped ? 4 : 9; }
 constexpr int kSkN = 32;                         // activation rows per MMA (B operand)
 constexpr int kSkABytes = 128 * 128;             // 128 weight rows x 256 codes
 constexpr int kSkBBytes = kSkN * 128;            // 32 activation rows x 256 codes
 constexpr int kSkSfBytes = 4 * 512;              // one 128-row chunk, four 128x4 atoms
 constexpr int kSkStageBytes = kSkABytes + kSkBBytes + 2 * kSkSfBytes;
-constexpr int kSkSmemBytes = kSkStages * kSkStageBytes + 256 + 1024;
-// TMEM: 32 accumulator columns, then per stage 16 columns of weight scales and
+constexpr int sk_smem_bytes(bool grouped) { return sk_stages(grouped) * kSkStageBytes + 512 + 1024; }
+constexpr int kSkAccs = 2;                       // accumulators in flight
+// TMEM: 2 x 32 accumulator columns, then per stage 16 columns of weight scales and
 // 16 of activation scales (4 per K step each: lane i of every quarter holds
 // line i of the atom, rows i, i+32, i+64, i+96 -- the MMA reads row r of an
 // operand from lane r % 32, column r / 32 of its K step)
 constexpr int kSkSfCols = 32;
-constexpr int kSkTmemCols = 512;
+constexpr int sk_tmem_cols(bool grouped) { return grouped ? 256 : 512; }
 constexpr uint64_t kSkDrainNs = 200000000ull;
-static_assert(kSkN + kSkStages * kSkSfCols <= kSkTmemCols, "TMEM budget");
-static_assert(kSkSmemBytes <= 232448, "shared memory budget");
+constexpr int kSkSfBase = kSkAccs * kSkN;         // first scale column
+static_assert(kSkSfBase + sk_stages(false) * kSkSfCols <= sk_tmem_cols(false) &&
+                  kSkSfBase + sk_stages(true) * kSkSfCols <= sk_tmem_cols(true),
+              "TMEM budget");
+static_assert(sk_smem_bytes(false) <= 232448 && 2 * (sk_smem_bytes(true) + 1024) <= 233472, "shared memory budget");
 
 __device__ __forceinline__ void sk_abort(volatile int *abort_flag, int *status) {
   *abort_flag = 1;
@@ -62,12 +80,12 @@ __device__ __forceinline__ void sk_abort(volatile int *abort_flag, int *status) 
 
 // p.M activation rows (<= 32), p.N features, a_* = activations, b_* = weights
 // (as for k_gemm_fp4); tmX: activation codes, box 128 B x 32 rows; tmW: weight
-// codes, box 128 B x 128 rows.
-template <bool MX>
-__global__ void __launch_bounds__(kSkThreads, 1)
+// codes, box 128 B x 64 rows.
+template <bool MX, bool GROUPED>
+__global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
     k_gemm_fp4_skinny(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                       const GemmParams p) {
-  constexpr int S = kSkStages;
+  constexpr int S = sk_stages(GROUPED);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
@@ -77,20 +95,22 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   uint8_t *sSFX = sSFW + S * kSkSfBytes;
   uint64_t *bars = reinterpret_cast<uint64_t *>(sSFX + S * kSkSfBytes);
   uint64_t *full = bars, *empty = bars + S, *sfready = bars + 2 * S;
-  uint64_t *acc_full = bars + 3 * S, *acc_empty = acc_full + 1, *drain = acc_full + 2;
-  uint64_t *never = acc_full + 3;          // test hook: a barrier nothing arrives at
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 4);
+  uint64_t *acc_full = bars + 3 * S, *acc_empty = acc_full + kSkAccs, *drain = acc_empty + kSkAccs;
+  uint64_t *never = drain + 1;             // test hook: a barrier nothing arrives at
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 3);     // the three producers
       mbar_init(&empty[s], 1);
       mbar_init(&sfready[s], 4);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 4);
+    for (int a = 0; a < kSkAccs; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 4);
+    }
     mbar_init(drain, 1);
     mbar_init(never, 1);
     *abort_flag = 0;
@@ -101,7 +121,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
     tma_prefetch_desc(&tmW);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, kSkTmemCols);
+    tmem_alloc(tmem_slot, sk_tmem_cols(GROUPED));
     tmem_relinquish();
   }
   tc_fence_before();
@@ -110,13 +130,57 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
   // Inputs of this kernel come from the previous one in the stream (the
-  // activation packing), which lets this grid start only after every kernel
-  // before it has completed: the producer issues the weight tiles of its
-  // first stages before its wait, every other thread waits here.
-  if (warp != 0) griddep_wait();
+  // activation packing).  NVFP4: that kernel lets this grid start only after
+  // every kernel before it has completed, so the producer issues the weight
+  // tiles of its first stages before its wait.  MXFP4: the packing lets this
+  // grid start at once, before what precedes it is done, so the producer only
+  // asks L2 for its first unit's weights (a hint: a weight written later is
+  // updated there), which then stream from HBM while the packing and the
+  // previous call's last kernel run.  Grouped: the units come from the
+  // previous kernels.  Every other thread waits here.
+  const bool producer = warp == 0 || warp >= 10;
+  if (!producer || GROUPED) griddep_wait();
 
   const int ksplit = p.ksplit > 1 ? p.ksplit : 1;
-  const int num_units = p.tiles_n * ksplit;          // (128-feature tile, K range)
+  // (128-feature tile, K range); grouped: (row group, m-tile, 128-feature tile),
+  // the first row group of every m-tile before the second (which few have), so
+  // that the units with rows spread over all CTAs
+  const int group_units = GROUPED ? p.tiles_n * *p.gnum_mtiles : 0;
+  const int num_units = GROUPED ? 4 * group_units : p.tiles_n * ksplit;
+  struct Unit {
+    int nt, w_row, x_row, out_row, rows, sub;   // rows: activation rows (0: nothing to do)
+  };
+  // The m-tile of unit u, fetched a unit ahead of its use (an L2 latency).
+  const auto tile_of = [&](int u) {
+    GroupTile g = {};
+    if constexpr (GROUPED)
+      if (u < num_units) g = p.gtiles[u % group_units / p.tiles_n];
+    return g;
+  };
+  const auto unit_of = [&](int u, GroupTile g) {
+    Unit t;
+    if constexpr (!GROUPED) {
+      t.nt = u / ksplit;
+      t.w_row = t.nt * 128;
+      t.x_row = t.out_row = t.sub = 0;
+      t.rows = (int)p.M;
+      return t;
+    } else {
+      t.sub = u / group_units;
+      const int v = u - t.sub * group_units;
+      t.nt = v % p.tiles_n;
+      if (!NVFP4_GUARD(g.expert >= 0 && (int64_t)(g.expert + 1) * p.N <= p.b_sf_row_chunks * 128 && g.a_row0 >= 0 &&
+                           g.a_row0 + 128 <= p.M && g.valid_rows >= 0 && g.valid_rows <= 128 && g.out_row0 >= 0 &&
+                           g.out_row0 + g.valid_rows <= p.out_rows,
+                       p.status))
+        g.expert = g.a_row0 = g.valid_rows = g.out_row0 = 0;
+      t.w_row = (int)(g.expert * p.N) + t.nt * 128;
+      t.x_row = g.a_row0 + 32 * t.sub;
+      t.out_row = g.out_row0 + 32 * t.sub;
+      t.rows = min(32, g.valid_rows - 32 * t.sub);
+      return t;
+    }
+  };
   const int kt_per = (p.num_kt + ksplit - 1) / ksplit;
   const int last_nk = p.nk64 - (p.num_kt - 1) * 4;   // K steps of the last 256-wide K tile
   constexpr int kAtoms = MX ? 2 : 4;                 // scale atoms of a full stage
@@ -125,38 +189,58 @@ __global__ void __launch_bounds__(kSkThreads, 1)
     return (uint32_t)((MX ? (nk + 1) / 2 : nk) * 512);
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer --
+  if (producer) {
+    // ----------------------------------------------------------- producers --
+    // Three threads in three warps, one stream each: the weight tile's upper
+    // and lower 64 rows, and the activation tile with both operands' scales.
     if (lane == 0) {
-      const uint32_t w_base = smem_u32(sW), x_base = smem_u32(sX);
+      const int role = warp == 0 ? 0 : warp - 9;
+      const uint32_t w_base = smem_u32(sW) + (role == 1 ? kSkABytes / 2 : 0), x_base = smem_u32(sX);
       const uint32_t sfw_base = smem_u32(sSFW), sfx_base = smem_u32(sSFX);
       const uint32_t full_base = smem_u32(full), empty_base = smem_u32(empty);
+      const int half_row = role == 1 ? 64 : 0;
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_par = 0;
       bool ok = true;
-      // the first unit's first stages (all free at entry): weights before the wait
+      // the first unit's weights, before the wait
       int pre = 0;
-      if ((int)blockIdx.x < num_units) {
+      if (!GROUPED && (int)blockIdx.x < num_units) {
         const int nt = blockIdx.x / ksplit;
         const int kt0 = (blockIdx.x % ksplit) * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
-        pre = min(S, kt1 - kt0);
         const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)nt * p.b_sf_katoms + (int64_t)kt0 * kAtoms);
-        for (int i = 0; i < pre; ++i) {
-          const int kt = kt0 + i;
-          const uint32_t fb = full_base + 8 * i;
-          const uint32_t sfb = sf_bytes(kt);
-          mbar_arrive_expect_tx_u(fb, kSkABytes + kSkBBytes + 2 * sfb);
-          tma_load_2d_u(w_base + i * kSkABytes, &tmW, fb, kt * 128, nt * 128);
-          bulk_load_u(sfw_base + i * kSkSfBytes, sfw_src, sfb, fb);
-          sfw_src += 512 * kAtoms;
+        if (MX) {
+          for (int i = 0; i < kt1 - kt0; ++i) {
+            if (role < 2)
+              tma_prefetch_2d(&tmW, (kt0 + i) * 128, nt * 128 + half_row);
+            else
+              prefetch_l2_bulk(sfw_src + (int64_t)i * 512 * kAtoms, sf_bytes(kt0 + i));
+          }
+        } else {
+          // the first stages, all free at entry
+          pre = min(S, kt1 - kt0);
+          for (int i = 0; i < pre; ++i) {
+            const uint32_t fb = full_base + 8 * i;
+            if (role < 2) {
+              mbar_arrive_expect_tx_u(fb, kSkABytes / 2);
+              tma_load_2d_u(w_base + i * kSkABytes, &tmW, fb, (kt0 + i) * 128, nt * 128 + half_row);
+            } else {
+              const uint32_t sfb = sf_bytes(kt0 + i);
+              mbar_arrive_expect_tx_u(fb, kSkBBytes + 2 * sfb);
+              bulk_load_u(sfw_base + i * kSkSfBytes, sfw_src + (int64_t)i * 512 * kAtoms, sfb, fb);
+            }
+          }
         }
       }
       griddep_wait();
+      GroupTile ahead = tile_of(blockIdx.x);
       for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
-        const int nt = u / ksplit;
+        const Unit t = unit_of(u, ahead);
+        ahead = tile_of(u + gridDim.x);
+        if (t.rows <= 0) continue;
         const int kt0 = (u % ksplit) * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
-        const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)nt * p.b_sf_katoms + (int64_t)kt0 * kAtoms);
-        const uint8_t *sfx_src = p.a_sf + 512 * ((int64_t)kt0 * kAtoms);   // the rows' one 128-row chunk
+        const uint8_t *sfw_src = p.b_sf + 512 * ((int64_t)(t.w_row >> 7) * p.b_sf_katoms + (int64_t)kt0 * kAtoms);
+        // the rows' 128-row chunk
+        const uint8_t *sfx_src = p.a_sf + 512 * ((int64_t)(t.x_row >> 7) * p.a_sf_katoms + (int64_t)kt0 * kAtoms);
         for (int kt = kt0; kt < kt1; ++kt) {
           const bool early = u == (int)blockIdx.x && kt - kt0 < pre;   // weights already in flight
           const bool got = early || (!*abort_flag && mbar_wait_u(empty_base + 8 * stage, phase ^ 1, p.timeout_ns));
@@ -166,16 +250,22 @@ __global__ void __launch_bounds__(kSkThreads, 1)
             break;
           }
           const uint32_t fb = full_base + 8 * stage;
-          const uint32_t sfb = sf_bytes(kt);
-          if (!early) {
-            mbar_arrive_expect_tx_u(fb, kSkABytes + kSkBBytes + 2 * sfb);
-            tma_load_2d_u(w_base + stage * kSkABytes, &tmW, fb, kt * 128, nt * 128);
-            bulk_load_u(sfw_base + stage * kSkSfBytes, sfw_src, sfb, fb);
+          if (role < 2) {
+            if (!early) {
+              mbar_arrive_expect_tx_u(fb, kSkABytes / 2);
+              tma_load_2d_u(w_base + stage * kSkABytes, &tmW, fb, kt * 128, t.w_row + half_row);
+            }
+          } else {
+            const uint32_t sfb = sf_bytes(kt);
+            if (!early) {
+              mbar_arrive_expect_tx_u(fb, kSkBBytes + 2 * sfb);
+              bulk_load_u(sfw_base + stage * kSkSfBytes, sfw_src, sfb, fb);
+            }
+            tma_load_2d_u(x_base + stage * kSkBBytes, &tmX, fb, kt * 128, t.x_row);
+            bulk_load_u(sfx_base + stage * kSkSfBytes, sfx_src, sfb, fb);
+            sfw_src += 512 * kAtoms;
+            sfx_src += 512 * kAtoms;
           }
-          tma_load_2d_u(x_base + stage * kSkBBytes, &tmX, fb, kt * 128, 0);
-          bulk_load_u(sfx_base + stage * kSkSfBytes, sfx_src, sfb, fb);
-          sfw_src += 512 * kAtoms;
-          sfx_src += 512 * kAtoms;
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
@@ -184,9 +274,10 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           }
         }
       }
-      // every fill this thread started lands before the CTA may exit
+      // every fill this thread started lands before the CTA may exit (after an
+      // abort another producer may never complete a stage: one bounded wait)
       for (int s = 0; s < S; ++s)
-        if (armed & (1u << s)) mbar_wait(&full[s], (armed_par >> s) & 1, kSkDrainNs);
+        if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_par >> s) & 1, kSkDrainNs)) break;
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issue --
@@ -196,21 +287,26 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       const uint64_t wdesc0 = sdesc_k_sw128(sW), xdesc0 = sdesc_k_sw128(sX);
       const uint32_t sfr_base = smem_u32(sfready), empty_base = smem_u32(empty);
       const uint32_t accf = smem_u32(acc_full), acce = smem_u32(acc_empty);
-      int stage = 0;
+      int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       if (p.stall_probe && !mbar_wait(never, 0, p.timeout_ns)) {
         sk_abort(abort_flag, p.status);   // expected: the expiry path under test
         ok = false;
       }
+      GroupTile ahead = tile_of(blockIdx.x);
       for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
+        const Unit t = unit_of(u, ahead);
+        ahead = tile_of(u + gridDim.x);
+        if (t.rows <= 0) continue;
         const int kt0 = (u % ksplit) * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
-        if (*abort_flag || !mbar_wait_u(acce, acc_phase ^ 1, p.timeout_ns)) {
+        if (*abort_flag || !mbar_wait_u(acce + 8 * acc, acc_phase ^ 1, p.timeout_ns)) {
           sk_abort(abort_flag, p.status);
           break;
         }
         tc_fence_after();
         uint32_t accumulate = 0;
+        const uint32_t dcol = tmem + acc * kSkN;
         for (int kt = kt0; kt < kt1; ++kt) {
           // the stage's operands have landed and its scales are in tensor memory
           if (*abort_flag || !mbar_wait_u(sfr_base + 8 * stage, phase, p.timeout_ns)) {
@@ -222,15 +318,16 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           const int nk = kt == p.num_kt - 1 ? last_nk : 4;
           const uint64_t wdesc = wdesc0 + (uint64_t)((stage * kSkABytes) >> 4);
           const uint64_t xdesc = xdesc0 + (uint64_t)((stage * kSkBBytes) >> 4);
-          const uint32_t sfw_col = tmem + kSkN + stage * kSkSfCols, sfx_col = sfw_col + 16;
+          // row r of a 128-row chunk has its scales in column r / 32 of its K step
+          const uint32_t sfw_col = tmem + kSkSfBase + stage * kSkSfCols, sfx_col = sfw_col + 16 + (GROUPED ? t.sub : 0);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j < nk) {
               if constexpr (MX)
-                tc_mma_mxfp4(tmem, wdesc + 2 * j, xdesc + 2 * j, j & 1 ? idesc_hi : idesc, sfw_col + 4 * (j >> 1),
+                tc_mma_mxfp4(dcol, wdesc + 2 * j, xdesc + 2 * j, j & 1 ? idesc_hi : idesc, sfw_col + 4 * (j >> 1),
                              sfx_col + 4 * (j >> 1), accumulate);
               else
-                tc_mma_nvfp4(tmem, wdesc + 2 * j, xdesc + 2 * j, idesc, sfw_col + 4 * j, sfx_col + 4 * j, accumulate);
+                tc_mma_nvfp4(dcol, wdesc + 2 * j, xdesc + 2 * j, idesc, sfw_col + 4 * j, sfx_col + 4 * j, accumulate);
               accumulate = 1;
             }
           }
@@ -241,24 +338,29 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           }
         }
         if (!ok) break;
-        tc_commit_u(accf);
-        acc_phase ^= 1;
+        tc_commit_u(accf + 8 * acc);
+        if (++acc == kSkAccs) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
       }
       // all MMAs issued by this thread complete before TMEM is freed
       tc_commit(drain);
       mbar_wait(drain, 0, kSkDrainNs);
     }
-  } else {
-    // ------------------------------- scales -> tensor memory, then epilogue --
+  } else if (warp < 6) {
+    // --------------------------------------------------- scales -> tensor memory --
     const int q = warp & 3;
     const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
-    const float alpha = acc_scale_of(p.g_a ? *p.g_a : 1.0f, p.g_b ? *p.g_b : 1.0f);
     int stage = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    uint32_t phase = 0;
     bool ok = true;
+    GroupTile ahead = tile_of(blockIdx.x);
     for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
-      const int nt = u / ksplit, ks = u % ksplit;
-      const int kt0 = ks * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
+      const Unit t = unit_of(u, ahead);
+      ahead = tile_of(u + gridDim.x);
+      if (t.rows <= 0) continue;
+      const int kt0 = (u % ksplit) * kt_per, kt1 = min(p.num_kt, kt0 + kt_per);
       for (int kt = kt0; kt < kt1; ++kt) {
         if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(&full[stage], phase, p.timeout_ns))) {
           if (lane == 0) sk_abort(abort_flag, p.status);
@@ -273,13 +375,13 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           const uint4 w = fw[32 * (j % kAtoms)];     // atom j, line `lane` (MX: columns 8..15 are not read)
           v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
-        tmem_st_32x32b_x16(tq + kSkN + stage * kSkSfCols, v);
+        tmem_st_32x32b_x16(tq + kSkSfBase + stage * kSkSfCols, v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 w = fx[32 * (j % kAtoms)];
           v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
-        tmem_st_32x32b_x16(tq + kSkN + stage * kSkSfCols + 16, v);
+        tmem_st_32x32b_x16(tq + kSkSfBase + stage * kSkSfCols + 16, v);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -289,36 +391,52 @@ __global__ void __launch_bounds__(kSkThreads, 1)
           phase ^= 1;
         }
       }
-      if (!ok) break;
-      // epilogue: thread = feature n0 + 32q + lane, its 32 columns = the activation rows
-      if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(acc_full, acc_phase, p.timeout_ns))) {
+    }
+  } else if (warp < 10) {
+    // ------------------------------------------------------------ epilogue --
+    // thread = feature n0 + 32q + lane, its 32 columns = the activation rows
+    const int q = warp & 3;
+    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
+    const float alpha = acc_scale_of(p.g_a ? *p.g_a : 1.0f, p.g_b ? *p.g_b : 1.0f);
+    int slot = 0;
+    uint32_t acc_phase = 0;
+    GroupTile ahead = tile_of(blockIdx.x);
+    for (int u = blockIdx.x; u < num_units; u += gridDim.x) {
+      const Unit t = unit_of(u, ahead);
+      ahead = tile_of(u + gridDim.x);
+      if (t.rows <= 0) continue;
+      const int ks = u % ksplit;
+      if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(&acc_full[slot], acc_phase, p.timeout_ns))) {
         if (lane == 0) sk_abort(abort_flag, p.status);
         break;
       }
       tc_fence_after();
       uint32_t acc[32];
       __syncwarp();
-      tmem_ld_32x32b_x32(tq, acc);
+      tmem_ld_32x32b_x32(tq + slot * kSkN, acc);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
-      acc_phase ^= 1;
+      if (lane == 0) mbar_arrive(&acc_empty[slot]);
+      if (++slot == kSkAccs) {
+        slot = 0;
+        acc_phase ^= 1;
+      }
       const int row = q * 32 + lane;
-      const int64_t n = (int64_t)nt * 128 + row;
+      const int64_t n = (int64_t)t.nt * 128 + row;
       float f[kSkN];
 #pragma unroll
       for (int m = 0; m < kSkN; ++m) f[m] = __fmul_rn(__uint_as_float(acc[m]), alpha);
       if (n < p.N) {
 #pragma unroll
         for (int m = 0; m < kSkN; ++m) {
-          if (m < p.M) {
+          if (m < t.rows) {
             if (p.partial)
               p.partial[((int64_t)ks * p.M + m) * p.N + n] = f[m];
             else if (p.out_fp32)
-              reinterpret_cast<float *>(p.d)[m * p.ldd + n] = f[m];
+              reinterpret_cast<float *>(p.d)[(t.out_row + (int64_t)m) * p.ldd + n] = f[m];
             else
-              reinterpret_cast<__nv_bfloat16 *>(p.d)[m * p.ldd + n] = __float2bfloat16_rn(f[m]);
+              reinterpret_cast<__nv_bfloat16 *>(p.d)[(t.out_row + (int64_t)m) * p.ldd + n] = __float2bfloat16_rn(f[m]);
           }
         }
       }
@@ -327,18 +445,23 @@ __global__ void __launch_bounds__(kSkThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kSkTmemCols);
+    tmem_dealloc(tmem, sk_tmem_cols(GROUPED));
   }
 }
 
 cudaError_t launch_gemm_fp4_skinny(const GemmParams &p, const CUtensorMap &x, const CUtensorMap &w, int num_sms,
                                    cudaStream_t st) {
-  const auto kernel = p.mx ? k_gemm_fp4_skinny<true> : k_gemm_fp4_skinny<false>;
-  if (cudaError_t e = ensure_dynamic_smem((const void *)kernel, kSkSmemBytes); e != cudaSuccess) return e;
-  const int64_t units = (int64_t)p.tiles_n * std::max(1, p.ksplit);
-  const int64_t grid = std::min<int64_t>(units, num_sms);
+  const auto kernel = p.gtiles ? k_gemm_fp4_skinny<true, true>
+                      : p.mx  ? k_gemm_fp4_skinny<true, false>
+                              : k_gemm_fp4_skinny<false, false>;
+  const int smem = sk_smem_bytes(p.gtiles != nullptr);
+  if (cudaError_t e = ensure_dynamic_smem((const void *)kernel, smem); e != cudaSuccess) return e;
+  if (p.gtiles && !p.mx) return cudaErrorInvalidValue;   // the grouped form takes MXFP4 experts
+  const int64_t slots = p.gtiles ? 2 * num_sms : num_sms;
+  const int64_t units = p.gtiles ? slots : (int64_t)p.tiles_n * std::max(1, p.ksplit);
+  const int64_t grid = std::min<int64_t>(units, slots);
   if (grid <= 0) return cudaSuccess;
-  return launch_pdl(kernel, dim3((unsigned)grid), dim3(kSkThreads), kSkSmemBytes, st, x, w, p);
+  return launch_pdl(kernel, dim3((unsigned)grid), dim3(kSkThreads), smem, st, x, w, p);
 }
 
 }  // namespace nvfp4

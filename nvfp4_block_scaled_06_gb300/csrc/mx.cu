@@ -85,11 +85,8 @@ constexpr int kMxUnit = 2;   // blocks per lane and step: 128 bytes of loads in 
 // rows and columns is written (0 outside the matrix).
 template <bool kV8>
 __global__ void __launch_bounds__(256) k_mx_quant(const MxQuantParams p) {
-  // The wait comes first: a kernel launched after this one may read what no
-  // earlier kernel writes (the operand-swapped GEMM streams its weights)
-  // before its own wait, which is safe only once every earlier kernel is done.
-  griddep_wait();
   griddep_launch_dependents();
+  griddep_wait();   // inputs may come from the previous kernel in the stream
   const int lane = threadIdx.x & 31;
   const uint32_t warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const uint32_t nwarps = gridDim.x * (blockDim.x >> 5);
