@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
 // to be wrong (the maximum infinite, the sum NaN) sends its warp through a
 // second one that masks -inf and NaN and takes +inf for the largest fp32.
 template <typename T, int L>
-__global__ void __launch_bounds__(kRouterWarps * 32) k_route_softmax_backward(const RouteGradParams p) {
+__global__ void __launch_bounds__(kRouterWarps * 32, 5) k_route_softmax_backward(const RouteGradParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   constexpr int VEC = 16 / (int)sizeof(T), NV = 32 / VEC, kTok = 32 / L;
@@ -836,7 +836,7 @@ cudaError_t launch_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) 
 template <typename T, int L, bool kScored>
 cudaError_t launch_few(const RouteTopkParams &p, bool vec, int num_sms, cudaStream_t st) {
   const int64_t per_cta = (int64_t)kRouterWarps * (32 / L);
-  const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
+  const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 64);
   const dim3 grid((unsigned)ctas), block(kRouterWarps * 32);
   return vec ? launch_pdl(k_route_few<T, L, kScored, true>, grid, block, 0, st, p)
              : launch_pdl(k_route_few<T, L, kScored, false>, grid, block, 0, st, p);
@@ -900,7 +900,7 @@ cudaError_t pick_grad(const RouteGradParams &p, int num_sms, cudaStream_t st) {
                  reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
                  reinterpret_cast<uintptr_t>(p.grad_logits) % 16 == 0;
   const int64_t per_cta = (int64_t)kRouterWarps * (32 / L);
-  const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
+  const int64_t ctas = std::min<int64_t>((p.tokens + per_cta - 1) / per_cta, (int64_t)num_sms * 64);
   const dim3 grid((unsigned)ctas), block(kRouterWarps * 32);
   if (dense)
     return v ? launch_pdl(k_route_softmax_backward<T, L>, grid, block, 0, st, p)
