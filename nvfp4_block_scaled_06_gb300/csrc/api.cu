@@ -1534,6 +1534,9 @@ struct MxGroupedPlan {
   int32_t *hist = nullptr, *counts = nullptr, *offsets = nullptr, *poffsets = nullptr;
   int32_t *row_map = nullptr, *nmt = nullptr;
   GroupTile *gtiles = nullptr;
+  // bf16 rows with expert ids are quantized straight into their top_k grouped
+  // rows; with the caller's routing once per token, then copied
+  int32_t *pair_row = nullptr;
   uint8_t *xq = nullptr, *xsf = nullptr;          // grouped, padded A operand
   uint8_t *xq_tok = nullptr, *xsf_tok = nullptr;  // X quantized once per token (linear scales)
 };
@@ -1552,7 +1555,9 @@ void plan_mx_grouped(const nvfp4_mxfp4_grouped_args *a, MxGroupedPlan *pl) {
   pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
   pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
   pl->nmt = c.take<int32_t>(4);
-  if (!a->x_codes) {
+  if (!a->x_codes && a->expert_ids) {
+    pl->pair_row = c.take<int32_t>((size_t)P * 4);
+  } else if (!a->x_codes) {
     pl->xq_tok = c.take<uint8_t>((size_t)a->num_tokens * a->K / 2);
     pl->xsf_tok = c.take<uint8_t>((size_t)a->num_tokens * (a->K / 32));
   }
@@ -1611,6 +1616,7 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
     r.gtiles = pl.gtiles;
     r.gnum_mtiles = pl.nmt;
     r.offsets_out = a->expert_offsets_out;
+    r.pair_row = pl.pair_row;
     r.status = status;
     if (cudaError_t e_ = launch_route(r, st); e_ != cudaSuccess) return cuda_status(e_);
   } else {
@@ -1631,9 +1637,7 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
         return cuda_status(e_);
   }
   const uint8_t *codes = a->x_codes, *sf = a->x_sf;
-  // few rows: each is quantized where it goes, top_k times over, which saves
-  // the copy's launch; many: once per token, then copied
-  const bool direct = a->x_bf16 && P <= 2048;
+  const bool direct = pl.pair_row != nullptr;
   if (direct) {
     MxQuantParams q{};
     q.src = static_cast<const __nv_bfloat16 *>(a->x_bf16);
@@ -1644,13 +1648,11 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
     q.sf = pl.xsf;
     q.sf_swizzled = 1;
     q.dst_rows = pl.prow_max;
-    q.row_map = pl.row_map;
-    q.num_mtiles = pl.nmt;
+    q.pair_row = pl.pair_row;
+    q.copies = (int)a->top_k;
     q.status = status;
     if (cudaError_t e_ = launch_mx_quant(q, sms, st); e_ != cudaSuccess) return cuda_status(e_);
   } else if (a->x_bf16) {
-    // every token row is quantized once, then its codes and scales are copied
-    // to each of its top_k rows of the grouped operand
     MxQuantParams q{};
     q.src = static_cast<const __nv_bfloat16 *>(a->x_bf16);
     q.rows = q.dst_rows = a->num_tokens;

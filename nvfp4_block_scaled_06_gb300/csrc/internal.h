@@ -77,6 +77,8 @@ struct MxQuantParams {
   int sf_swizzled;
   int64_t dst_rows;                   // rows written
   const int32_t *row_map;             // optional gather: dst row -> src row (< 0: left untouched)
+  const int32_t *pair_row;            // optional scatter [rows][copies]: a source row's dst rows (< 0: none)
+  int copies;
   const int32_t *num_mtiles;          // optional (device, batch 1): only rows < 128 x this are in use
   int *status;
 };
@@ -209,6 +211,7 @@ struct RouteParams {
   int32_t *poffsets;          // [E+1] padded (multiples of 128)
   int32_t *perm;              // [pairs]
   int32_t *row_map;           // [padded_rows_max]
+  int32_t *pair_row;          // optional [pairs]: a pair's padded row (-1: its id was dropped)
   int64_t padded_rows_max;
   GroupTile *gtiles;          // [max m-tiles]
   int32_t *gnum_mtiles;

@@ -200,6 +200,7 @@ __device__ __forceinline__ void scatter_pairs(const RouteParams &p, int64_t i, b
   if (in) {
     e = p.expert_ids[i];
     if (e < 0 || e >= E) e = -1;
+    if (e < 0 && p.pair_row) p.pair_row[i] = -1;
   }
   const unsigned same = __match_any_sync(0xffffffffu, e);
   const unsigned lt = (1u << lane) - 1u;
@@ -214,6 +215,7 @@ __device__ __forceinline__ void scatter_pairs(const RouteParams &p, int64_t i, b
     if (NVFP4_GUARD(pos >= 0 && pos < p.pairs && prow >= 0 && prow < p.padded_rows_max, p.status)) {
       p.perm[pos] = (int32_t)i;
       p.row_map[prow] = (int32_t)(i / p.top_k);
+      if (p.pair_row) p.pair_row[i] = (int32_t)prow;
     }
   }
 }
