@@ -318,8 +318,7 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
           const int nk = kt == p.num_kt - 1 ? last_nk : 4;
           const uint64_t wdesc = wdesc0 + (uint64_t)((stage * kSkABytes) >> 4);
           const uint64_t xdesc = xdesc0 + (uint64_t)((stage * kSkBBytes) >> 4);
-          // row r of a 128-row chunk has its scales in column r / 32 of its K step
-          const uint32_t sfw_col = tmem + kSkSfBase + stage * kSkSfCols, sfx_col = sfw_col + 16 + (GROUPED ? t.sub : 0);
+          const uint32_t sfw_col = tmem + kSkSfBase + stage * kSkSfCols, sfx_col = sfw_col + 16;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j < nk) {
@@ -379,7 +378,10 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 w = fx[32 * (j % kAtoms)];
-          v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
+          // the MMA's 32 activation rows take their scales from the first of
+          // the four columns: the words of this unit's row group go there
+          v[4 * j] = !GROUPED || t.sub == 0 ? w.x : t.sub == 1 ? w.y : t.sub == 2 ? w.z : w.w;
+          v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
         tmem_st_32x32b_x16(tq + kSkSfBase + stage * kSkSfCols + 16, v);
         tmem_st_wait();

@@ -301,6 +301,40 @@ def test_grouped_forms(T, E, k, N, K, out_dtype):
         assert torch.equal(r[0], got)
 
 
+@pytest.mark.parametrize("T,E,k,N,K,heavy", [(93, 64, 2, 2048, 736, 0), (150, 64, 2, 512, 352, 150),
+                                             (500, 40, 1, 256, 1056, 300), (32, 32, 8, 1024, 2048, 0)])
+def test_grouped_few_rows_per_expert(T, E, k, N, K, heavy):
+    """Few rows per expert on average (the operand-swapped kernel), with more
+    units than the GPU's CTAs, K that wraps its stages, and one expert that takes
+    `heavy` of the tokens: several groups of 32 rows and more than one m-tile."""
+    rng, wl, wc_d, wsf_d, ids = expert_case(T, E, k, N, K, seed=21)
+    for t in range(heavy):
+        if 3 not in ids[t]:
+            ids[t, t % k] = 3
+    x = bits(rng, T, K)
+    d, S, perm, offsets = grouped_reference(mo.dequantize(*mo.quantize(x)), ids, wl)
+    ids_d = torch.from_numpy(np.ascontiguousarray(ids)).cuda()
+    call, (got, p, offs) = nv.prepare_mxfp4_grouped(ids_d, dev_bf16(x), wc_d, wsf_d, N, K, E,
+                                                    out_dtype=torch.float32)
+    for _ in range(3):
+        call()
+    assert nv.read_device_status(call.workspace) == 0
+    assert np.array_equal(p.cpu().numpy(), perm) and np.array_equal(offs.cpu().numpy(), offsets)
+    assert_gemm_close(got, d, S)
+    # the down-projection's form: rows already grouped, weighted back to the tokens
+    h = bits(rng, T * k, K)
+    hv = mo.dequantize(*mo.quantize(h))
+    dd, SS = np.zeros((T * k, N)), np.zeros((T * k, N))
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        dd[r], SS[r] = product(hv[r], wl[e])
+    w = rng.random((T, k)).astype(np.float32)
+    y = nv.nvfp4_mxfp4_moe_down_combine(dev_bf16(h), p, offs, torch.from_numpy(w).cuda(), wc_d, wsf_d, N, K, E)
+    want = o.moe_combine(dd, perm, w, k)
+    tol = o.moe_combine(2.0 ** -8 * np.abs(dd) + 2e-5 * SS, perm, np.abs(w), k) + o.bf16_ulp(np.abs(want) + 1e-30)
+    assert np.all(np.abs(y.float().cpu().numpy() - want) <= tol)
+
+
 def test_grouped_drops_missing_choices():
     """ids of -1 (the router's missing choices) take no row."""
     T, E, k, N, K = 40, 6, 4, 256, 96
