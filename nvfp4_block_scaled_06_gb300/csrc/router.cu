@@ -757,20 +757,33 @@ __global__ void __launch_bounds__(kRouterWarps * 32, 5) k_route_softmax_backward
     const bool live = t < p.tokens;
     const T *row = reinterpret_cast<const T *>(p.logits) + (live ? t : t0) * p.ld;
     T *out = reinterpret_cast<T *>(p.grad_logits) + (live ? t : t0) * p.ld_grad;
-    int id = live && sub < k ? __ldg(p.expert_ids + t * k + sub) : -1;
-    if (id >= E) id = -1;
-    const float d = id >= 0 ? __ldg(p.grad_weights + t * k + sub) * p.scale : 0.0f;
-    const float xs = id >= 0 ? load1(row + id) : -INFINITY;
+    // every load is issued before the first use: the ids and their gradients,
+    // the row, then (the one that depends on another) the chosen logits
+    const bool slot = live && sub < k;
+    int id = slot ? __ldg(p.expert_ids + t * k + sub) : -1;
+    float d = slot ? __ldg(p.grad_weights + t * k + sub) * p.scale : 0.0f;
     float x[NV][VEC], m, s, ps;
-    for (int attempt = 0;; ++attempt) {
-      m = -INFINITY;
+    const auto load_row = [&]() {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int e = (v * L + sub) * VEC;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) x[v][i] = -INFINITY;
-        if (v * L * VEC >= E) continue;
         if (e < E) load_vec<VEC>(row + e, x[v]);
+      }
+    };
+    load_row();
+    if (id < 0 || id >= E) {
+      id = -1;
+      d = 0.0f;
+    }
+    const float xs = id >= 0 ? load1(row + id) : -INFINITY;
+    for (int attempt = 0;; ++attempt) {
+      if (attempt) load_row();
+      m = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (v * L * VEC >= E) continue;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           if (attempt) x[v][i] = x[v][i] > -INFINITY ? finite_top(x[v][i]) : -INFINITY;
