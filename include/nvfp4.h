@@ -611,9 +611,11 @@ size_t nvfp4_mxfp4_dgrad_workspace_bytes(const nvfp4_mxfp4_dgrad_args *args);
  * nvfp4_mxfp4_grouped_gemm, nvfp4_mxfp4_moe_down_combine -- the routed
  * experts' products with MXFP4 experts: nvfp4_grouped_gemm and
  * nvfp4_moe_down_combine with MXFP4 in place of NVFP4 (no global scales, no
- * LoRA); the routing forms, the row order, the handling of ids outside
- * [0, num_experts) and the other requirements are theirs.  x_sf is linear
- * [num_tokens][K/32], w_sf [E][swizzled N x K/32].
+ * LoRA); the routing forms, the row order and the other requirements are
+ * theirs.  x_sf is linear [num_tokens][K/32], w_sf [E][swizzled N x K/32].
+ * Ids outside [0, num_experts) (nvfp4_route_topk's -1) take no grouped row: the
+ * rows of d past the last offset are not written, perm_out is -1 there, and the
+ * combine leaves such slots out (a token without any gets a row of zeros).
  * ------------------------------------------------------------------------ */
 typedef struct {
   int64_t num_tokens, top_k, num_experts, N, K;

@@ -238,7 +238,9 @@ __global__ void __launch_bounds__(1024) k_route_scatter(const RouteParams p) {
   }
   __syncthreads();
   const int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x;
-  scatter_pairs(p, i, threadIdx.x < p.chunk && i < p.pairs, sh_base, sh_cnt, p.offsets, p.poffsets);
+  const bool in = threadIdx.x < p.chunk && i < p.pairs;
+  if (in && i >= p.offsets[E]) p.perm[i] = -1;   // dropped pairs leave grouped rows unused at the end
+  scatter_pairs(p, i, in, sh_base, sh_cnt, p.offsets, p.poffsets);
 }
 
 // Up to 1024 pairs (decode): counts, layout and scatter by one block in one
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(1024) k_route_one(const RouteParams p) {
     sh_poff[threadIdx.x] = poff;
   }
   __syncthreads();
+  if (in && (int)threadIdx.x >= p.offsets[E]) p.perm[threadIdx.x] = -1;
   scatter_pairs(p, threadIdx.x, in, sh_off, sh_cnt, sh_off, sh_poff);
 }
 
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restri
       }
     }
     if (inv) {
-      for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) {
+      for (int64_t i = threadIdx.x; i < ctotal; i += blockDim.x) {
         const int32_t q = perm[i];
         if (NVFP4_NOTE(q >= 0 && q < pairs, status)) inv[q] = (int32_t)i;
       }
@@ -421,12 +424,16 @@ cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pa
 // y[t][n] = sum over slots j (in order) of w[t][j] * d[g(t, j)][n], fp32
 // accumulation (one fused multiply-add per slot), rounded once to bf16, where
 // g(t, j) is the grouped row of pair t*top_k + j (the inverse of perm).
-// perm is the caller's device data: entries outside [0, pairs) are skipped,
-// and inv is first filled with -1 so that a pair no entry names reads nothing.
-__global__ void k_invert_perm(const int32_t *__restrict__ perm, int64_t pairs, int32_t *inv, int *status) {
+// perm is the caller's device data: only its first *rows entries name grouped
+// rows (the last offset: dropped pairs have none), entries outside [0, pairs)
+// are skipped, and inv is first filled with -1 so that a pair no entry names
+// reads nothing.
+__global__ void k_invert_perm(const int32_t *__restrict__ perm, int64_t pairs, const int32_t *__restrict__ rows,
+                              int32_t *inv, int *status) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pairs;
+  const int64_t n = min(pairs, (int64_t)*rows);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int32_t q = perm[i];
     if (NVFP4_NOTE(q >= 0 && q < pairs, status)) inv[q] = (int32_t)i;
@@ -525,13 +532,13 @@ __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__rest
 
 cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,
                                int64_t tokens, int top_k, int64_t N, __nv_bfloat16 *y, int num_sms,
-                               cudaStream_t st, int *status, bool inv_ready) {
+                               cudaStream_t st, int *status, bool inv_ready, const int32_t *rows) {
   const int64_t pairs = tokens * top_k;
   if (!inv_ready) {
     const int64_t c1 = std::max<int64_t>(1, std::min<int64_t>((pairs + 255) / 256, (int64_t)num_sms * 4));
     cudaError_t e = launch_pdl(k_fill_i32, dim3((unsigned)c1), dim3(256), 0, st, inv, pairs, (int32_t)-1);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_invert_perm, dim3((unsigned)c1), dim3(256), 0, st, perm, pairs, inv, status);
+    e = launch_pdl(k_invert_perm, dim3((unsigned)c1), dim3(256), 0, st, perm, pairs, rows, inv, status);
     if (e != cudaSuccess) return e;
   }
   // column ranges until every SM has 32 warps

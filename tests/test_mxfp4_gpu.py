@@ -350,6 +350,45 @@ def test_grouped_drops_missing_choices():
     assert_gemm_close(got[:n], d, S)
 
 
+@pytest.mark.parametrize("T,E,k", [(12, 8, 4), (300, 8, 4), (3000, 16, 8)])
+def test_missing_choices_through_router_and_both_products(T, E, k):
+    """Tokens whose masked logits leave fewer than k experts, or none: their
+    slots take no grouped row, the rest is as if they were not there, and a
+    token without experts gets zeros (small and large routing paths)."""
+    N, K = 256, 64
+    rng, wl, wc_d, wsf_d, _ = expert_case(T, E, k, N, K, seed=33)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    logits[::3, 2:] = -np.inf
+    logits[1::7] = -np.inf
+    r = nv.nvfp4_route_topk(torch.from_numpy(logits).cuda(), k, score="softmax")
+    ids = r["expert_ids"].cpu().numpy()
+    assert (ids[1::7] == -1).all() and (ids[0, 2:] == -1).all()
+    x = bits(rng, T, K)
+    d, S, perm, offsets = grouped_reference(mo.dequantize(*mo.quantize(x)), ids, wl)
+    got, p, offs = nv.nvfp4_mxfp4_grouped_gemm(r["expert_ids"], dev_bf16(x), wc_d, wsf_d, N, K, E,
+                                               out_dtype=torch.float32)
+    n = len(perm)
+    assert np.array_equal(offs.cpu().numpy(), offsets) and np.array_equal(p[:n].cpu().numpy(), perm)
+    assert bool((p[n:] == -1).all())
+    assert_gemm_close(got[:n], d, S)
+    h = bits(rng, T * k, K)
+    hv = mo.dequantize(*mo.quantize(h))
+    dd, SS = np.zeros((T * k, N)), np.zeros((T * k, N))
+    for e in range(E):
+        s = slice(offsets[e], offsets[e + 1])
+        dd[s], SS[s] = product(hv[s], wl[e])
+    w = r["weights"].cpu().numpy().astype(np.float64)
+    want, tol = np.zeros((T, N)), np.zeros((T, N))
+    for i in range(n):
+        t, j = divmod(int(perm[i]), k)
+        want[t] += w[t, j] * dd[i]
+        tol[t] += abs(w[t, j]) * (2.0 ** -8 * np.abs(dd[i]) + 2e-5 * SS[i])
+    y = nv.nvfp4_mxfp4_moe_down_combine(dev_bf16(h), p, offs, r["weights"], wc_d, wsf_d, N, K, E)
+    y = y.float().cpu().numpy()
+    assert np.all(np.abs(y - want) <= tol + o.bf16_ulp(np.abs(want) + 1e-30))
+    assert (y[1::7] == 0).all()
+
+
 @pytest.mark.parametrize("T,E,k,N,K", [(1, 4, 2, 256, 64), (32, 32, 8, 512, 352), (200, 40, 4, 256, 256)])
 def test_moe_down(T, E, k, N, K):
     rng, wl, wc_d, wsf_d, ids = expert_case(T, E, k, N, K, seed=9)
