@@ -120,7 +120,9 @@ __device__ __forceinline__ void signal_abort(volatile int *abort_flag, int *stat
 // MX: the operands are MXFP4 (one E8M0 scale per 32 elements).  A 128x4 scale
 // atom then covers 128 elements of K, so a stage has two atoms per 128 rows
 // instead of four, and the MMA (kind::mxf4 scale_vec::2X) of K step j takes
-// half (j & 1) of atom j / 2; everything else is the same.
+// half (j & 1) of atom j / 2; everything else is the same.  4096 tokens' top 8
+// of 256 experts (165 with rows, N 2048, K 6144): 295 us, 1.30 GB read, bound by
+// L2 -> SM copies at experts of many rows and by DRAM at those of few.
 template <int BN, bool MX>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

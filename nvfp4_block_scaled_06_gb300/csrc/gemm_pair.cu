@@ -39,6 +39,7 @@
 // MX: the same kernel for MXFP4 operands (one E8M0 scale per 32 elements): a
 // stage has two scale atoms per 128 rows instead of four, and the MMA
 // (kind::mxf4 scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
+// 8192 x 2048 x 6144: 40-41 us cold = 5.1 PFLOP/s (NVFP4: 47.6-49.4 us).
 // Every wait is bounded; on expiry a CTA records a timeout, drains its own
 // copies (and, in the leader, its MMAs) and leaves its loops; the peer's waits
 // then expire too.  Both CTAs meet at a cluster barrier before freeing TMEM.

@@ -11,6 +11,8 @@
 // the quantizer writes.
 //
 // HBM-bound, one pass: 2 B read + 0.53125 B written per element, and back.
+// 32 x [2048, 6144] (1.02 GB either way): packing 157 us = 6.5 TB/s, unpacking
+// 152 us = 6.7 TB/s (copy: 6.74 TB/s).
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -282,7 +284,8 @@ __global__ void __launch_bounds__(256) k_mx_dequant_t(const uint8_t *__restrict_
 // rows, half a block), 8 bytes of codes of each row in, per column one 16-byte
 // store of its eight rows.  Of a warp's lanes eight take consecutive row groups
 // (a store fills 128 bytes of four output rows) and four consecutive half
-// blocks (a load reads 32 bytes of a row).
+// blocks (a load reads 32 bytes of a row).  [2048, 6144]: 9 us alone with cold
+// caches, one wave's latency; in front of the gradient GEMM 4 to 5 us.
 __global__ void __launch_bounds__(128) k_mx_dequant_t8(const uint8_t *__restrict__ codes,
                                                        const uint8_t *__restrict__ sf, int swz, int64_t rows,
                                                        int64_t cols, int64_t sf_bstride,
