@@ -1395,6 +1395,7 @@ struct MxGemmPlan {
   uint8_t *aq_codes = nullptr, *aq_sf = nullptr;   // in-call quantization of A
   int bn = 256, ksplit = 1;
   bool pair = false, skinny = false;
+  bool fuse = false;                               // a few rows, packed by the operand-swapped kernel
   float *partial = nullptr;                        // split-K partials [ksplit][M][N]
 };
 
@@ -1402,14 +1403,15 @@ struct MxGemmPlan {
 // comes packed or not), then the 1-SM and the pair kernel by the same rules.
 void plan_mx_gemm(const nvfp4_mxfp4_gemm_args *a, MxGemmPlan *pl) {
   Carve c(a->workspace);
-  if (a->a_bf16) {
-    pl->aq_codes = c.take<uint8_t>((size_t)pad_up(a->M, 128) * a->K / 2);
-    pl->aq_sf = c.take<uint8_t>(mx_sf_swizzled_bytes(a->M, a->K));
-  }
   const int sms = plan_sms();
   pl->bn = pick_bn(a->M, a->N, sms);
   pl->skinny = a->M <= 32;
   pl->ksplit = pl->skinny ? pick_skinny_ksplit(a->N, a->K, sms) : pick_ksplit(a->M, a->N, a->K, pl->bn, sms, false);
+  pl->fuse = a->a_bf16 && skinny_fuses(a->M, ceil_div(a->K, 256), pl->ksplit);
+  if (a->a_bf16 && !pl->fuse) {
+    pl->aq_codes = c.take<uint8_t>((size_t)pad_up(a->M, 128) * a->K / 2);
+    pl->aq_sf = c.take<uint8_t>(mx_sf_swizzled_bytes(a->M, a->K));
+  }
   pl->pair = !pl->skinny && use_pair(a->M, pl->ksplit);
   if (pl->ksplit > 1) pl->partial = c.take<float>((size_t)pl->ksplit * a->M * a->N * 4);
   pl->ws = c.off;
@@ -1436,7 +1438,7 @@ nvfp4_status validate_mx_gemm(const nvfp4_mxfp4_gemm_args *a) {
 nvfp4_status run_mx_gemm(const nvfp4_mxfp4_gemm_args *a, const MxGemmPlan &pl, int sms, cudaStream_t st) {
   const uint64_t tmo = g_timeout_ns.load();
   const uint8_t *a_codes = a->a_codes, *a_sf = a->a_sf;
-  if (a->a_bf16) {
+  if (a->a_bf16 && !pl.fuse) {
     MxQuantParams q{};
     q.src = static_cast<const __nv_bfloat16 *>(a->a_bf16);
     q.rows = q.dst_rows = a->M;
@@ -1455,8 +1457,11 @@ nvfp4_status run_mx_gemm(const nvfp4_mxfp4_gemm_args *a, const MxGemmPlan &pl, i
   const int64_t a_rows = a->a_bf16 ? pad_up(a->M, 128) : a->M;
   const int b_box = pl.skinny ? 64 : pl.pair ? 128 : pl.bn;
   GemmMaps maps;
-  if (!map2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, a->K / 2, a_rows, a->K / 2, 128, pl.skinny ? 32 : 128) ||
-      !map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, b_box))
+  if (!map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->b_codes, a->K / 2, a->N, a->K / 2, 128, b_box))
+    return NVFP4_ERR_CUDA;
+  maps.a = maps.b;   // (rows packed by the kernel: not read)
+  if (!pl.fuse && !map2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, a->K / 2, a_rows, a->K / 2, 128,
+                         pl.skinny ? 32 : 128))
     return NVFP4_ERR_CUDA;
   maps.t = maps.a;
   maps.lb = maps.b;
@@ -1467,6 +1472,10 @@ nvfp4_status run_mx_gemm(const nvfp4_mxfp4_gemm_args *a, const MxGemmPlan &pl, i
   p.num_kt = (int)ceil_div(a->K, 256);
   p.nk64 = (int)ceil_div(a->K, 64);
   p.mx = 1;
+  if (pl.fuse) {
+    p.x_bf16 = static_cast<const __nv_bfloat16 *>(a->a_bf16);
+    p.x_ld = a->lda;
+  }
   p.a_sf = a_sf;
   p.b_sf = a->b_sf;
   p.a_sf_katoms = pad_up(a->K / 32, 4) / 4;

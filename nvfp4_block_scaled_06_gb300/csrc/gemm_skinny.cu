@@ -31,6 +31,14 @@
 // stage has two scale atoms per operand instead of four, and the MMA (kind::mxf4
 // scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
 //
+// FUSE (MXFP4, up to eight bf16 rows with at most 768 of their blocks per CTA): no
+// packing kernel in front (6144 x 16384, one row: 16.5 -> 14.3 us per call; eight
+// rows are 1408 blocks there and took 17.6 us against 16.3 with the kernel).
+// Warps 2..9 pack the CTA's K range of the rows before the first stage, into one
+// 8-row group of the swizzled tile (1 KB) per 256-wide K tile; they stay for all
+// of the CTA's units, and the stages carry weights only.  The MMA's rows 8..31
+// read whatever follows: their results are not stored.
+//
 // GROUPED (MXFP4 experts at decode): a unit is a 128-feature tile of one
 // expert's weights against 32 of its routed rows, taken from the m-tile table
 // (four such row groups per 128-row tile, those without rows skipped), so the
@@ -39,6 +47,7 @@
 // where the 128 x 256 tiles took 43.5 us; bound by whole units in rounds (1296
 // of them on 304 CTAs).
 #include "internal.h"
+#include "mxfp4.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -81,7 +90,7 @@ __device__ __forceinline__ void sk_abort(volatile int *abort_flag, int *status) 
 // p.M activation rows (<= 32), p.N features, a_* = activations, b_* = weights
 // (as for k_gemm_fp4); tmX: activation codes, box 128 B x 32 rows; tmW: weight
 // codes, box 128 B x 64 rows.
-template <bool MX, bool GROUPED>
+template <bool MX, bool GROUPED, bool FUSE>
 __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
     k_gemm_fp4_skinny(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                       const GemmParams p) {
@@ -97,7 +106,8 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
   uint64_t *full = bars, *empty = bars + S, *sfready = bars + 2 * S;
   uint64_t *acc_full = bars + 3 * S, *acc_empty = acc_full + kSkAccs, *drain = acc_empty + kSkAccs;
   uint64_t *never = drain + 1;             // test hook: a barrier nothing arrives at
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
+  uint64_t *xready = drain + 2;            // FUSE: the rows are packed
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 3);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -113,6 +123,7 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
     }
     mbar_init(drain, 1);
     mbar_init(never, 1);
+    mbar_init(xready, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -190,6 +201,38 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
     return (uint32_t)((MX ? (nk + 1) / 2 : nk) * 512);
   };
 
+  if (FUSE && warp >= 2 && warp < 10) {
+    // ------------------------------------------------------- pack the rows --
+    // (K ranges: one unit per CTA; one range: the same rows for every unit)
+    if ((int)blockIdx.x < num_units) {
+      const int kt0 = (blockIdx.x % ksplit) * kt_per, nblocks = (min(p.num_kt, kt0 + kt_per) - kt0) * 8;
+      const int64_t nblk = p.K / 32;
+      const uint32_t x_base = smem_u32(sX);
+      constexpr int kPer = kFuseBlocks / 256;        // blocks per thread, every load before the first use
+      uint32_t w[kPer][16];
+#pragma unroll
+      for (int h = 0; h < kPer; ++h) {
+        const int i = threadIdx.x - 64 + 256 * h, r = i / nblocks, b = i - r * nblocks;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[h][k] = 0u;
+        if (r < p.M && (int64_t)kt0 * 8 + b < nblk)
+          load32<false>(p.x_bf16 + r * p.x_ld + ((int64_t)kt0 * 8 + b) * 32, w[h]);
+      }
+#pragma unroll
+      for (int h = 0; h < kPer; ++h) {
+        const int i = threadIdx.x - 64 + 256 * h, r = i / nblocks, b = i - r * nblocks;
+        if (r >= p.M) continue;
+        uint32_t sb;
+        const uint4 c = mx_encode32(w[h], sb);
+        // 128-byte swizzle: 16-byte chunk c of row r sits at c ^ (r & 7)
+        sts128(x_base + (b >> 3) * 1024 + r * 128 + (((b & 7) ^ r) << 4), c.x, c.y, c.z, c.w);
+        sSFX[(b >> 3) * 64 + r * 8 + (b & 7)] = (uint8_t)sb;
+      }
+      fence_proxy_async_shared();      // the tiles are read by the MMA (async proxy)
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (threadIdx.x == 64) mbar_arrive(xready);
+  }
   if (producer) {
     // ----------------------------------------------------------- producers --
     // Three threads in three warps, one stream each: the weight tile's upper
@@ -259,11 +302,13 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
           } else {
             const uint32_t sfb = sf_bytes(kt);
             if (!early) {
-              mbar_arrive_expect_tx_u(fb, kSkBBytes + 2 * sfb);
+              mbar_arrive_expect_tx_u(fb, FUSE ? sfb : kSkBBytes + 2 * sfb);
               bulk_load_u(sfw_base + stage * kSkSfBytes, sfw_src, sfb, fb);
             }
-            tma_load_2d_u(x_base + stage * kSkBBytes, &tmX, fb, kt * 128, t.x_row);
-            bulk_load_u(sfx_base + stage * kSkSfBytes, sfx_src, sfb, fb);
+            if constexpr (!FUSE) {
+              tma_load_2d_u(x_base + stage * kSkBBytes, &tmX, fb, kt * 128, t.x_row);
+              bulk_load_u(sfx_base + stage * kSkSfBytes, sfx_src, sfb, fb);
+            }
             sfw_src += 512 * kAtoms;
             sfx_src += 512 * kAtoms;
           }
@@ -295,6 +340,10 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
         sk_abort(abort_flag, p.status);   // expected: the expiry path under test
         ok = false;
       }
+      if (FUSE && ok && !mbar_wait(xready, 0, p.timeout_ns)) {
+        sk_abort(abort_flag, p.status);
+        ok = false;
+      }
       GroupTile ahead = tile_of(blockIdx.x);
       for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
         const Unit t = unit_of(u, ahead);
@@ -318,7 +367,7 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
           tc_fence_after();
           const int nk = kt == p.num_kt - 1 ? last_nk : 4;
           const uint64_t wdesc = wdesc0 + (uint64_t)((stage * kSkABytes) >> 4);
-          const uint64_t xdesc = xdesc0 + (uint64_t)((stage * kSkBBytes) >> 4);
+          const uint64_t xdesc = xdesc0 + (uint64_t)((FUSE ? (kt - kt0) * 1024 : stage * kSkBBytes) >> 4);
           const uint32_t sfw_col = tmem + kSkSfBase + stage * kSkSfCols, sfx_col = sfw_col + 16;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -376,8 +425,14 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
           v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
         tmem_st_32x32b_x16(tq + kSkSfBase + stage * kSkSfCols, v);
+        if constexpr (FUSE) {
+          // rows 0..7, lanes 0..7: the two words of this K tile
+          const uint2 w = *reinterpret_cast<const uint2 *>(sSFX + (kt - kt0) * 64 + (lane & 7) * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 16; ++j) v[j] = lane < 8 ? (j & 4 ? w.y : w.x) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 4 && !FUSE; ++j) {
           const uint4 w = fx[32 * (j % kAtoms)];
           // the MMA's 32 activation rows take their scales from the first of
           // the four columns: the words of this unit's row group go there
@@ -454,12 +509,15 @@ __global__ void __launch_bounds__(kSkThreads, GROUPED ? 2 : 1)
 
 cudaError_t launch_gemm_fp4_skinny(const GemmParams &p, const CUtensorMap &x, const CUtensorMap &w, int num_sms,
                                    cudaStream_t st) {
-  const auto kernel = p.gtiles ? k_gemm_fp4_skinny<true, true>
-                      : p.mx  ? k_gemm_fp4_skinny<true, false>
-                              : k_gemm_fp4_skinny<false, false>;
+  const auto kernel = p.gtiles   ? k_gemm_fp4_skinny<true, true, false>
+                      : p.x_bf16 ? k_gemm_fp4_skinny<true, false, true>
+                      : p.mx     ? k_gemm_fp4_skinny<true, false, false>
+                                 : k_gemm_fp4_skinny<false, false, false>;
   const int smem = sk_smem_bytes(p.gtiles != nullptr);
   if (cudaError_t e = ensure_dynamic_smem((const void *)kernel, smem); e != cudaSuccess) return e;
-  if (p.gtiles && !p.mx) return cudaErrorInvalidValue;   // the grouped form takes MXFP4 experts
+  // the grouped form and the rows packed by the kernel are MXFP4's
+  if ((p.gtiles || p.x_bf16) && !p.mx) return cudaErrorInvalidValue;
+  if (p.x_bf16 && !skinny_fuses(p.M, p.num_kt, p.ksplit)) return cudaErrorInvalidValue;
   const int64_t slots = p.gtiles ? 2 * num_sms : num_sms;
   const int64_t units = p.gtiles ? slots : (int64_t)p.tiles_n * std::max(1, p.ksplit);
   const int64_t grid = std::min<int64_t>(units, slots);

@@ -123,6 +123,8 @@ struct GemmParams {
   int pair_half_tail;         // pair kernel: a last wave of at most half the pairs runs as 256 x 128 units
   int mx;                     // MXFP4 operands: one E8M0 scale per 32 elements (a 128x4 scale atom is 128
                               // elements long), g_a = g_b = null
+  const __nv_bfloat16 *x_bf16;   // operand-swapped MXFP4 kernel: the activation rows, which the kernel packs
+  int64_t x_ld;                  // itself (where skinny_fuses), or null
 };
 
 struct GemmMaps {
@@ -132,6 +134,15 @@ struct GemmMaps {
   bool has_d = false;
   bool has_half = false;
 };
+
+// Whether the operand-swapped MXFP4 kernel packs M bf16 rows itself: one 8-row
+// group of the swizzled tile per K tile of a unit, in the nine stages' 36 KB of
+// activation tiles (the last one's MMA reads 3 KB on), three blocks per packing thread.
+constexpr int kFuseRows = 8, kFuseTiles = 33, kFuseBlocks = 768;
+inline bool skinny_fuses(int64_t M, int64_t num_kt, int ksplit) {
+  const int64_t tiles = (num_kt + std::max(1, ksplit) - 1) / std::max(1, ksplit);
+  return M <= kFuseRows && tiles <= kFuseTiles && M * tiles * 8 <= kFuseBlocks;
+}
 
 cudaError_t launch_gemm_fp4(const GemmParams &p, const GemmMaps &maps, int bn, int num_sms,
                             cudaStream_t st);

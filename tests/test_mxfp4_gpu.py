@@ -150,6 +150,24 @@ def test_gemm_quantized_in_the_call_and_packed(M, N, K, out_dtype):
         assert_gemm_close(got, y, S, what=f"{M}x{N}x{K}")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 20488, 352), (5, 20480, 544), (8, 19464, 2080), (3, 256, 8448), (8, 128, 3104),
+                                   (2, 392, 14336)])
+def test_gemm_few_rows_packed_by_the_kernel(M, N, K):
+    """Rows that the operand-swapped kernel packs itself: more weight tiles than
+    SMs (the packed rows serve every unit of a CTA), long K ranges, K ranges whose
+    last tile is partly outside K; strided rows."""
+    rng = np.random.default_rng(M + N + K)
+    big = dev_bf16(bits(rng, M, K + 32))
+    x = big[:, 16:16 + K]
+    wc, wb, wc_d, wsf_d = packed(bits(rng, N, K, scale=0.02))
+    y, S = product(mo.dequantize(*mo.quantize(host_bits(x))), mo.dequantize(wc, wb))
+    call, got = nv.prepare_mxfp4_gemm(wc_d, wsf_d, N, K, a_bf16=x, out_dtype=torch.float32)
+    for _ in range(3):
+        call()
+    assert nv.read_device_status(call.workspace) == 0
+    assert_gemm_close(got, y, S)
+
+
 def test_gemm_scales_of_every_size():
     """Scales spread over 2^-40 .. 2^40 between blocks: each block's scale, not
     a neighbour's, multiplies its codes (K steps of both halves of an atom)."""
