@@ -542,7 +542,7 @@ nvfp4_status plan_grouped(const nvfp4_grouped_args *a, GroupedPlan *pl) {
   pl->poffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
   pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
   pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
-  pl->nmt = c.take<int32_t>(4);
+  pl->nmt = c.take<int32_t>(8);   // two counts
   if (!a->x_codes) {
     if (!a->x_global_scale) {
       pl->nparts = amax_parts_for(a->num_tokens);
@@ -687,6 +687,14 @@ nvfp4_status run_grouped_products(const GroupedProducts &g, int *status, uint64_
       return NVFP4_ERR_CUDA;
     p.tiles_n = (int)(g.N / 128);
     e = launch_gemm_fp4_skinny(p, mx, maps.b, sms, st);
+  } else if (g.mx) {
+    if (!map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, g.E * g.N, g.K / 2, 128, 128) ||
+        !map2d(&maps.bh, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, g.E * g.N, g.K / 2, 128, 64))
+      return NVFP4_ERR_CUDA;
+    maps.lb = maps.b;
+    maps.lbh = maps.bh;
+    maps.has_half = 1;
+    e = launch_gemm_fp4_pair(p, maps, sms, st);
   } else {
     e = launch_gemm_fp4(p, maps, bn, sms, st);
   }
@@ -714,6 +722,7 @@ nvfp4_status run_grouped(const nvfp4_grouped_args *a, const GroupedPlan &pl, int
     r.row_map = pl.row_map;
     r.padded_rows_max = pl.prow_max;
     r.gtiles = pl.gtiles;
+    r.tile_rows = 128;
     r.gnum_mtiles = pl.nmt;
     r.offsets_out = a->expert_offsets_out;
     r.status = status;
@@ -722,7 +731,7 @@ nvfp4_status run_grouped(const nvfp4_grouped_args *a, const GroupedPlan &pl, int
     // the caller's grouping: padded layout from its offsets, row_map -> token through its perm
     if (cudaError_t e_ = launch_layout_from_offsets(a->offsets_in, (int)a->num_experts, P, pl.prow_max, pl.goffsets,
                                                     pl.poffsets, pl.gtiles, pl.nmt, pl.row_map, a->perm_in,
-                                                    (int)a->top_k, sms, st, status, nullptr);
+                                                    (int)a->top_k, sms, st, status, nullptr, 128);
         e_ != cudaSuccess)
       return cuda_status(e_);
     if (a->perm_out && a->perm_out != a->perm_in &&
@@ -844,7 +853,7 @@ void plan_moe_down(const nvfp4_moe_down_args *a, MoeDownPlan *pl) {
   pl->poffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
   pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
   pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
-  pl->nmt = c.take<int32_t>(4);
+  pl->nmt = c.take<int32_t>(8);   // two counts
   pl->inv = c.take<int32_t>((size_t)P * 4);
   if (!a->h_global_scale) {
     pl->nparts = amax_parts_for(P);
@@ -884,7 +893,7 @@ nvfp4_status run_moe_down(const nvfp4_moe_down_args *a, const MoeDownPlan &pl, i
   const int64_t P = a->num_tokens * a->top_k;
   if (cudaError_t e_ = launch_layout_from_offsets(a->expert_offsets, (int)a->num_experts, P, pl.prow_max,
                                                   pl.goffsets, pl.poffsets, pl.gtiles, pl.nmt, pl.row_map,
-                                                  a->perm, 0, sms, st, status, pl.inv);
+                                                  a->perm, 0, sms, st, status, pl.inv, 128);
       e_ != cudaSuccess)
     return cuda_status(e_);
   // h is quantized once (one tensor-wide g) straight into the padded layout:
@@ -1536,6 +1545,13 @@ nvfp4_status run_mx_dgrad(const nvfp4_mxfp4_dgrad_args *a, int sms, cudaStream_t
                        static_cast<int *>(a->workspace), a->prof_begin, a->prof_end, sms, st);
 }
 
+// Decode: few rows per expert on average, and no more than 512 on any (an expert
+// gets a token once): the operand-swapped kernel, whose stages hold weights
+// instead of padding rows.
+bool mx_few_rows(int64_t T, int64_t k, int64_t E) { return T <= 512 && T * k <= 16 * E; }
+// The m-tiles' rows: the pair kernel takes every other call.
+int mx_tile_rows(int64_t T, int64_t k, int64_t E) { return mx_few_rows(T, k, E) ? 128 : 256; }
+
 struct MxGroupedPlan {
   size_t ws = 0;
   int nchunks = 0;
@@ -1563,7 +1579,7 @@ void plan_mx_grouped(const nvfp4_mxfp4_grouped_args *a, MxGroupedPlan *pl) {
   pl->poffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
   pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
   pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
-  pl->nmt = c.take<int32_t>(4);
+  pl->nmt = c.take<int32_t>(8);   // two counts
   if (!a->x_codes && a->expert_ids) {
     pl->pair_row = c.take<int32_t>((size_t)P * 4);
   } else if (!a->x_codes) {
@@ -1575,10 +1591,6 @@ void plan_mx_grouped(const nvfp4_mxfp4_grouped_args *a, MxGroupedPlan *pl) {
   pl->ws = c.off;
 }
 
-// Decode: few rows per expert on average, and no more than 512 on any (an expert
-// gets a token once): the operand-swapped kernel, whose stages hold weights
-// instead of padding rows.
-bool mx_few_rows(int64_t T, int64_t k, int64_t E) { return T <= 512 && T * k <= 16 * E; }
 
 // The sizes that both routed MXFP4 calls take.
 nvfp4_status validate_mx_experts(int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
@@ -1623,6 +1635,7 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
     r.row_map = pl.row_map;
     r.padded_rows_max = pl.prow_max;
     r.gtiles = pl.gtiles;
+    r.tile_rows = mx_tile_rows(a->num_tokens, a->top_k, a->num_experts);
     r.gnum_mtiles = pl.nmt;
     r.offsets_out = a->expert_offsets_out;
     r.pair_row = pl.pair_row;
@@ -1632,7 +1645,8 @@ nvfp4_status run_mx_grouped(const nvfp4_mxfp4_grouped_args *a, const MxGroupedPl
     // the caller's grouping: padded layout from its offsets, row_map -> token through its perm
     if (cudaError_t e_ = launch_layout_from_offsets(a->offsets_in, (int)a->num_experts, P, pl.prow_max, pl.offsets,
                                                     pl.poffsets, pl.gtiles, pl.nmt, pl.row_map, a->perm_in,
-                                                    (int)a->top_k, sms, st, status, nullptr);
+                                                    (int)a->top_k, sms, st, status, nullptr,
+                                                    mx_tile_rows(a->num_tokens, a->top_k, a->num_experts));
         e_ != cudaSuccess)
       return cuda_status(e_);
     if (a->perm_out && a->perm_out != a->perm_in)
@@ -1718,7 +1732,7 @@ void plan_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, MxMoeDownPlan *pl) {
   pl->poffsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
   pl->row_map = c.take<int32_t>((size_t)pl->prow_max * 4);
   pl->gtiles = c.take<GroupTile>((size_t)(pl->prow_max / 128) * sizeof(GroupTile));
-  pl->nmt = c.take<int32_t>(4);
+  pl->nmt = c.take<int32_t>(8);   // two counts
   pl->inv = c.take<int32_t>((size_t)P * 4);
   pl->hq = c.take<uint8_t>((size_t)pl->prow_max * a->K / 2);
   pl->hsf = c.take<uint8_t>(mx_sf_swizzled_bytes(pl->prow_max, a->K));
@@ -1741,7 +1755,7 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
   const int64_t P = a->num_tokens * a->top_k;
   if (cudaError_t e_ = launch_layout_from_offsets(a->expert_offsets, (int)a->num_experts, P, pl.prow_max,
                                                   pl.goffsets, pl.poffsets, pl.gtiles, pl.nmt, pl.row_map,
-                                                  a->perm, 0, sms, st, status, pl.inv);
+                                                  a->perm, 0, sms, st, status, pl.inv, mx_tile_rows(a->num_tokens, a->top_k, a->num_experts));
       e_ != cudaSuccess)
     return cuda_status(e_);
   // h is quantized straight into the padded layout: padded row r takes grouped row row_map[r]

@@ -80,6 +80,8 @@ static_assert(kPSmemBytes <= 232448, "shared memory budget");
 
 struct PairTile {
   int64_t m0, n0;      // first row of the unit's A (256 rows) and B (256 or 128 rows)
+  int64_t out_row0, col0;   // first row and column of D
+  int valid;           // rows of D from out_row0 on
   bool half;           // a 256 x 128 unit: one half of a tail tile
 };
 
@@ -96,9 +98,10 @@ struct PairSchedule {
   int num_units;
 };
 
+template <bool GROUPED>
 __device__ __forceinline__ PairSchedule pair_schedule(const GemmParams &p, int npairs) {
   PairSchedule s;
-  s.tiles_m2 = (int)((p.M + 255) / 256);
+  s.tiles_m2 = GROUPED ? p.gnum_mtiles[1] : (int)((p.M + 255) / 256);
   const int tiles = s.tiles_m2 * p.tiles_n;
   const int tail = tiles % npairs;
   const bool split = p.pair_half_tail && tail > 0 && 2 * tail <= npairs;
@@ -107,7 +110,10 @@ __device__ __forceinline__ PairSchedule pair_schedule(const GemmParams &p, int n
   return s;
 }
 
-__device__ __forceinline__ PairTile pair_tile(const PairSchedule &s, int u) {
+// Grouped: m-tile major (an m-tile's n-tiles run together: its A rows and the
+// expert's weights stay in L2).
+template <bool GROUPED>
+__device__ __forceinline__ PairTile pair_tile(const GemmParams &p, const PairSchedule &s, int u) {
   PairTile t;
   int v = u, sub = 0;
   t.half = u >= s.split_from;
@@ -115,8 +121,25 @@ __device__ __forceinline__ PairTile pair_tile(const PairSchedule &s, int u) {
     v = s.split_from + ((u - s.split_from) >> 1);
     sub = (u - s.split_from) & 1;
   }
+  if constexpr (GROUPED) {
+    GroupTile g = p.gtiles[v / p.tiles_n];
+    if (!NVFP4_GUARD(g.expert >= 0 && (int64_t)(g.expert + 1) * p.N <= p.b_sf_row_chunks * 128 && g.a_row0 >= 0 &&
+                         g.a_row0 + 128 <= p.M && g.valid_rows >= 0 && g.valid_rows <= 256 && g.out_row0 >= 0 &&
+                         g.out_row0 + g.valid_rows <= p.out_rows,
+                     p.status))
+      g.expert = g.a_row0 = g.valid_rows = g.out_row0 = 0;
+    t.col0 = (int64_t)(v % p.tiles_n) * 256 + 128 * sub;
+    t.n0 = g.expert * p.N + t.col0;
+    t.m0 = g.a_row0;
+    t.out_row0 = g.out_row0;
+    t.valid = g.valid_rows;
+    return t;
+  }
   t.n0 = (int64_t)(v / s.tiles_m2) * 256 + 128 * sub;
   t.m0 = (int64_t)(v % s.tiles_m2) * 256;
+  t.out_row0 = t.m0;
+  t.col0 = t.n0;
+  t.valid = (int)(p.M - t.m0 < 256 ? p.M - t.m0 : 256);
   return t;
 }
 
@@ -143,7 +166,7 @@ __device__ __forceinline__ void pair_abort(volatile int *abort_flag, int *status
 
 }  // namespace
 
-template <bool MX>
+template <bool MX, bool GROUPED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_gemm_fp4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmLB,
@@ -217,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   griddep_wait();      // inputs of this kernel come from the previous one in the stream
 
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const PairSchedule sched = pair_schedule(p, npairs);
+  const PairSchedule sched = pair_schedule<GROUPED>(p, npairs);
   const int num_units = sched.num_units;
   const int a_sf_chunks = (int)((p.M + 127) / 128);
   // the leader's barriers as cluster addresses (for the peer: its remote copy)
@@ -239,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint32_t phase = 0, armed = 0, armed_par = 0;
     bool ok = true;
     for (int u = pair; ok && u < num_units; u += npairs) {
-      const PairTile t = pair_tile(sched, u);
+      const PairTile t = pair_tile<GROUPED>(p, sched, u);
       // a half unit's B is 128 rows: 64 in each CTA
       const int a_row = (int)(t.m0 + 128 * rank), b_row = (int)(t.n0 + (t.half ? 64 : 128) * rank);
       const uint32_t b_bytes = t.half ? kPBBytes / 2 : kPBBytes;
@@ -517,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint32_t acc_phase = 0;
     const float alpha = acc_scale_of(p.g_a ? *p.g_a : 1.0f, p.g_b ? *p.g_b : 1.0f);
     for (int u = pair; u < num_units; u += npairs) {
-      const PairTile t = pair_tile(sched, u);
+      const PairTile t = pair_tile<GROUPED>(p, sched, u);
       const int halves = t.half ? 1 : 2;
       // warp-uniform outcome: tcgen05.ld below is a warp-collective instruction
       PSTAT_T0();
@@ -529,8 +552,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         break;
       }
       tc_fence_after();
-      const int64_t orow = t.m0 + 128 * rank + r;
-      const bool row_ok = orow < p.M;
+      const int64_t orow = t.out_row0 + 128 * rank + r;
+      const bool row_ok = 128 * (int)rank + r < t.valid;
 #pragma unroll 1
       for (int half = 0; half < halves; ++half) {
         uint32_t v[4][32];
@@ -556,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const uint32_t box0 = smem_u32(stg) + (uint32_t)(q * 4 * 2048);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (t.n0 + (half * 4 + c) * 32 < p.N) {
+            if (t.col0 + (half * 4 + c) * 32 < p.N) {
               uint32_t w[16];
 #pragma unroll
               for (int i2 = 0; i2 < 16; ++i2) {
@@ -575,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lane == 0) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int64_t n = t.n0 + (half * 4 + c) * 32;
+              const int64_t n = t.col0 + (half * 4 + c) * 32;
               if (n < p.N) tma_store_2d(&tmD, box0 + (uint32_t)(c * 2048), (int32_t)n, (int32_t)(t.m0 + 128 * rank + 32 * q));
             }
             bulk_commit_group();
@@ -585,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!row_ok) continue;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int64_t n = t.n0 + (half * 4 + c) * 32;
+          const int64_t n = t.col0 + (half * 4 + c) * 32;
           if (n >= p.N) break;
           float f[32];
 #pragma unroll
@@ -654,13 +677,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // How many CTA pairs of this kernel the device holds at once (clusters of two
 // need two SMs of one GPC), queried once per device and instance, after its
 // shared-memory limit was raised.
-static int resident_pairs(const void *kernel, bool mx, int num_sms) {
+static int resident_pairs(const void *kernel, int instance, int num_sms) {
   static std::mutex mu;
-  static int cached_for[2][64] = {};
+  static int cached_for[3][64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 2;
   std::lock_guard<std::mutex> lk(mu);
-  int *cached = cached_for[mx ? 1 : 0];
+  int *cached = cached_for[instance];
   if (!cached[dev]) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
@@ -677,12 +700,15 @@ static int resident_pairs(const void *kernel, bool mx, int num_sms) {
 }
 
 cudaError_t launch_gemm_fp4_pair(const GemmParams &p, const GemmMaps &m, int num_sms, cudaStream_t st) {
-  const auto kernel = p.mx ? k_gemm_fp4_pair<true> : k_gemm_fp4_pair<false>;
+  if (p.gtiles && (!p.mx || p.lora_steps)) return cudaErrorInvalidValue;   // the grouped form takes MXFP4 experts
+  const auto kernel = p.gtiles ? k_gemm_fp4_pair<true, true>
+                      : p.mx  ? k_gemm_fp4_pair<true, false>
+                              : k_gemm_fp4_pair<false, false>;
   if (cudaError_t e = ensure_dynamic_smem((const void *)kernel, kPSmemBytes); e != cudaSuccess) return e;
-  const int64_t tiles = ((p.M + 255) / 256) * (int64_t)p.tiles_n;
-  const int64_t resident = resident_pairs((const void *)kernel, p.mx != 0, num_sms);
+  const int64_t resident = resident_pairs((const void *)kernel, p.gtiles ? 2 : p.mx ? 1 : 0, num_sms);
+  const int64_t tiles = p.gtiles ? resident : ((p.M + 255) / 256) * (int64_t)p.tiles_n;
   GemmParams q = p;
-  q.store_tma = p.store_tma && m.has_d;
+  q.store_tma = p.store_tma && m.has_d && !p.gtiles;
   // half units need the 64-row B maps, and every half of the last n-tile
   // must hold a column of D (so that its B scale chunk exists)
   q.pair_half_tail = m.has_half && p.N - (int64_t)(p.tiles_n - 1) * 256 > 128;

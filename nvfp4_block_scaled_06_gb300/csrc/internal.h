@@ -89,8 +89,9 @@ cudaError_t launch_mx_dequant(const uint8_t *codes, const uint8_t *sf, int sf_sw
                               int64_t out_bstride, int num_sms, cudaStream_t st);
 
 // --------------------------------------------------------------------- GEMM --
-// One grouped m-tile: expert, first A row (padded grouped order), valid rows,
-// first output row (unpadded grouped order).
+// One grouped m-tile: expert, first A row (padded grouped order), valid rows
+// (up to 128, or 256 for the pair kernel), first output row (unpadded grouped
+// order).
 struct GroupTile {
   int32_t expert, a_row0, valid_rows, out_row0;
 };
@@ -112,7 +113,7 @@ struct GemmParams {
   int lora_steps;             // 64-wide bf16 K steps of the LoRA up-projection
   int tiles_m, tiles_n;
   const GroupTile *gtiles;    // grouped mode: m-tile table
-  const int32_t *gnum_mtiles; // grouped mode: number of m-tiles (device)
+  const int32_t *gnum_mtiles; // grouped mode: number of m-tiles (device; [1]: of the pair kernel's)
   int64_t out_rows;           // grouped mode: rows of D (index checks)
   int ksplit;                 // >1: K split into ranges, fp32 partials [ksplit][M][N]
   float *partial;
@@ -149,7 +150,9 @@ cudaError_t launch_gemm_fp4(const GemmParams &p, const GemmMaps &maps, int bn, i
 // The dense product on CTA pairs (256 x 256 tiles, tcgen05 cta_group::2):
 // p.tiles_n = ceil(N / 256); maps.b and maps.lb with 128-row boxes (each CTA
 // loads its half of the B tile), maps.bh and maps.lbh (has_half) the same
-// with 64-row boxes; no grouped tiles, split-K or accumulation.
+// with 64-row boxes; no split-K or accumulation.  With p.gtiles (MXFP4 only;
+// 256-row entries): the grouped product, maps.a over the padded grouped rows,
+// maps.b over the stacked experts.
 cudaError_t launch_gemm_fp4_pair(const GemmParams &p, const GemmMaps &maps, int num_sms, cudaStream_t st);
 // The product for M <= 32 activation rows with the operands swapped (weights
 // as the MMA's 128-row A side): x = activation codes in 32-row boxes of a
@@ -225,7 +228,8 @@ struct RouteParams {
   int32_t *pair_row;          // optional [pairs]: a pair's padded row (-1: its id was dropped)
   int64_t padded_rows_max;
   GroupTile *gtiles;          // [max m-tiles]
-  int32_t *gnum_mtiles;
+  int tile_rows;              // rows per entry of gtiles: 128 or 256
+  int32_t *gnum_mtiles;       // [2]: 128-row tiles of the padded layout, entries of gtiles
   int32_t *offsets_out;       // optional copy of offsets for the caller
   int *status;                // device status word (index checks)
 };
@@ -239,7 +243,7 @@ bool layout_makes_inverse(int64_t padded_rows_max);
 cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pairs, int64_t padded_rows_max,
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,
-                                       int num_sms, cudaStream_t st, int *status, int32_t *inv);
+                                       int num_sms, cudaStream_t st, int *status, int32_t *inv, int tile_rows);
 // y[t] = sum_j w[t][j] d[inverse perm (t*top_k + j)] (bf16 rows, fp32 sums);
 // inv holds the inverse already, or is made here from perm's first *rows entries.
 cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,

@@ -98,7 +98,7 @@ __device__ __forceinline__ void write_layout(const RouteParams &p, int32_t count
   const int e = threadIdx.x;
   const bool act = e < p.num_experts;
   const int32_t padded = (count + 127) & ~127;
-  const int32_t mt = padded / 128;
+  const int32_t mt = (count + p.tile_rows - 1) / p.tile_rows;
   int32_t total, ptotal, mtotal;
   off = block_exclusive_scan(count, scratch, total);
   poff = block_exclusive_scan(padded, scratch, ptotal);
@@ -121,13 +121,13 @@ __device__ __forceinline__ void write_layout(const RouteParams &p, int32_t count
     const int lane = threadIdx.x & 31;
     for (int x = threadIdx.x >> 5; x < p.num_experts; x += blockDim.x >> 5) {
       const int32_t cnt = s_cnt[x], of = s_off[x], pf = s_poff[x], mo = s_moff[x];
-      const int32_t pad = (cnt + 127) & ~127;
-      for (int j = lane; j < pad / 128; j += 32) {
+      const int32_t pad = (cnt + 127) & ~127, tr = p.tile_rows;
+      for (int j = lane; j * tr < cnt; j += 32) {
         GroupTile g;
         g.expert = x;
-        g.a_row0 = pf + 128 * j;
-        g.valid_rows = min(128, cnt - 128 * j);
-        g.out_row0 = of + 128 * j;
+        g.a_row0 = pf + tr * j;
+        g.valid_rows = min(tr, cnt - tr * j);
+        g.out_row0 = of + tr * j;
         if (NVFP4_GUARD(mo + j < p.padded_rows_max / 128, p.status)) p.gtiles[mo + j] = g;
       }
       for (int32_t i = cnt + lane; i < pad; i += 32)
@@ -138,7 +138,8 @@ __device__ __forceinline__ void write_layout(const RouteParams &p, int32_t count
     p.offsets[p.num_experts] = total;
     p.poffsets[p.num_experts] = ptotal;
     if (p.offsets_out) p.offsets_out[p.num_experts] = total;
-    *p.gnum_mtiles = mtotal;
+    p.gnum_mtiles[0] = ptotal / 128;
+    p.gnum_mtiles[1] = mtotal;
   }
   // rows past ptotal (= 128 x the m-tile count) are never read: every user of
   // the layout is bounded by the m-tile count
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restri
                                                          int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                                          int32_t *gnum_mtiles, int64_t max_tiles, int *status,
                                                          int32_t *row_map, const int32_t *__restrict__ perm,
-                                                         int top_k, int32_t *inv) {
+                                                         int top_k, int32_t *inv, int tile_rows) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   __shared__ int32_t scratch[64];
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restri
   (void)NVFP4_NOTE(!act || (int64_t)count == diff, status);   // the caller's offsets were clamped
   if (threadIdx.x == 0) (void)NVFP4_NOTE(offsets[0] == 0, status);
   const int32_t padded = (count + 127) & ~127;
-  const int32_t mt = padded / 128;
+  const int32_t mt = (count + tile_rows - 1) / tile_rows;
   int32_t ctotal, ptotal, mtotal;
   const int32_t off = block_exclusive_scan(count, scratch, ctotal);
   const int32_t poff = block_exclusive_scan(padded, scratch, ptotal);
@@ -326,16 +327,17 @@ __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restri
     for (int j = 0; j < mt; ++j) {
       GroupTile g;
       g.expert = e;
-      g.a_row0 = poff + 128 * j;
-      g.valid_rows = min(128, count - 128 * j);
-      g.out_row0 = off + 128 * j;
+      g.a_row0 = poff + tile_rows * j;
+      g.valid_rows = min(tile_rows, count - tile_rows * j);
+      g.out_row0 = off + tile_rows * j;
       if (NVFP4_GUARD(moff + j < max_tiles, status)) gtiles[moff + j] = g;
     }
   }
   if (threadIdx.x == 0) {
     goffsets[E] = ctotal;
     poffsets[E] = ptotal;
-    *gnum_mtiles = mtotal;
+    gnum_mtiles[0] = ptotal / 128;
+    gnum_mtiles[1] = mtotal;
   }
   if (row_map) {
     // few rows: the row map (and the inverse of perm) by the same block, a
@@ -409,11 +411,11 @@ bool layout_makes_inverse(int64_t padded_rows_max) { return padded_rows_max <= k
 cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pairs, int64_t padded_rows_max,
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,
-                                       int num_sms, cudaStream_t st, int *status, int32_t *inv) {
+                                       int num_sms, cudaStream_t st, int *status, int32_t *inv, int tile_rows) {
   const bool one = layout_makes_inverse(padded_rows_max);
   cudaError_t e = launch_pdl(k_offsets_layout, dim3(1), dim3(1024), 0, st, offsets, E, pairs, goffsets, poffsets,
                              gtiles, gnum_mtiles, padded_rows_max / 128, status, one ? row_map : (int32_t *)nullptr,
-                             perm, top_k, one ? inv : (int32_t *)nullptr);
+                             perm, top_k, one ? inv : (int32_t *)nullptr, tile_rows);
   if (e != cudaSuccess || one) return e;
   const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>((padded_rows_max + 255) / 256, (int64_t)num_sms * 4));
   return launch_pdl(k_rowmap_from_offsets, dim3((unsigned)ctas), dim3(256), 0, st, (const int32_t *)goffsets,

@@ -353,6 +353,45 @@ def test_grouped_few_rows_per_expert(T, E, k, N, K, heavy):
     assert np.all(np.abs(y.float().cpu().numpy() - want) <= tol)
 
 
+@pytest.mark.parametrize("T,E,k,N,K,heavy,empty", [(300, 4, 2, 256, 96, 0, 1), (513, 5, 2, 512, 1312, 513, 0),
+                                                   (1100, 9, 4, 2048, 160, 0, 8), (700, 40, 3, 768, 416, 690, 5)])
+def test_grouped_many_rows_per_expert(T, E, k, N, K, heavy, empty):
+    """Tiles of 256 rows: experts that end in a tile's first half, in its second or
+    on its edge, one row past it, an expert without rows (its choices dropped),
+    and more units than CTA pairs, the last ones as halves."""
+    rng, wl, wc_d, wsf_d, ids = expert_case(T, E, k, N, K, seed=33)
+    for t in range(heavy):
+        if 3 not in ids[t]:
+            ids[t, t % k] = 3
+    ids[ids == empty] = -1
+    x = bits(rng, T, K)
+    d, S, perm, offsets = grouped_reference(mo.dequantize(*mo.quantize(x)), ids, wl)
+    n = len(perm)
+    ids_d = torch.from_numpy(np.ascontiguousarray(ids)).cuda()
+    for out_dtype in (torch.float32, torch.bfloat16):
+        call, (got, p, offs) = nv.prepare_mxfp4_grouped(ids_d, dev_bf16(x), wc_d, wsf_d, N, K, E, out_dtype=out_dtype)
+        got.fill_(-7.0)
+        call()
+        assert nv.read_device_status(call.workspace) == 0
+        assert np.array_equal(p[:n].cpu().numpy(), perm) and np.array_equal(offs.cpu().numpy(), offsets)
+        assert_gemm_close(got[:n], d, S)
+        assert torch.all(got[n:] == -7.0)
+    h = bits(rng, T * k, K)
+    hv = mo.dequantize(*mo.quantize(h))
+    dd, SS = np.zeros((T * k, N)), np.zeros((T * k, N))
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        dd[r], SS[r] = product(hv[r], wl[e])
+    w = rng.random((T, k)).astype(np.float32)
+    y = nv.nvfp4_mxfp4_moe_down_combine(dev_bf16(h), p, offs, torch.from_numpy(w).cuda(), wc_d, wsf_d, N, K, E)
+    want, tol = np.zeros((T, N)), np.zeros((T, N))
+    for i, pair in enumerate(perm):
+        want[pair // k] += w[pair // k, pair % k] * dd[i]
+        tol[pair // k] += w[pair // k, pair % k] * (2.0 ** -8 * np.abs(dd[i]) + 2e-5 * SS[i])
+    tol += o.bf16_ulp(np.abs(want) + 1e-30)
+    assert np.all(np.abs(y.float().cpu().numpy() - want) <= tol)
+
+
 def test_grouped_drops_missing_choices():
     """ids of -1 (the router's missing choices) take no row."""
     T, E, k, N, K = 40, 6, 4, 256, 96
