@@ -689,9 +689,10 @@ nvfp4_status run_grouped_products(const GroupedProducts &g, int *status, uint64_
     e = launch_gemm_fp4_skinny(p, mx, maps.b, sms, st);
   } else if (g.mx) {
     if (!map2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, g.E * g.N, g.K / 2, 128, 128) ||
-        !map2d(&maps.bh, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, g.E * g.N, g.K / 2, 128, 64))
+        !map2d(&maps.bh, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, g.E * g.N, g.K / 2, 128, 64) ||
+        !map2d(&maps.t, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.aq, g.K / 2, g.prow_max, g.K / 2, 128, 64) ||
+        !map2d(&maps.lb, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.aq, g.K / 2, g.prow_max, g.K / 2, 128, 32))
       return NVFP4_ERR_CUDA;
-    maps.lb = maps.b;
     maps.lbh = maps.bh;
     maps.has_half = 1;
     e = launch_gemm_fp4_pair(p, maps, sms, st);

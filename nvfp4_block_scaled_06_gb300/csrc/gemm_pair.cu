@@ -159,6 +159,15 @@ __device__ __forceinline__ PairTile pair_tile(const GemmParams &p, const PairSch
 #define PSTAT_ADD(p, rank, i) (void)0
 #endif
 
+// Grouped: the rows of A that a CTA loads for a tile (0, 32, 64 or 128: the
+// least box that holds its valid rows; the others keep what a former stage
+// left, and no row of D is theirs).  Most experts have few rows, and their
+// tiles are bound by the copies from L2.
+__device__ __forceinline__ int pair_a_rows(int valid, int rank) {
+  const int n = valid - 128 * rank;
+  return n <= 0 && rank ? 0 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+}
+
 __device__ __forceinline__ void pair_abort(volatile int *abort_flag, int *status) {
   *abort_flag = 1;
   record_timeout(status);
@@ -266,7 +275,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // a half unit's B is 128 rows: 64 in each CTA
       const int a_row = (int)(t.m0 + 128 * rank), b_row = (int)(t.n0 + (t.half ? 64 : 128) * rank);
       const uint32_t b_bytes = t.half ? kPBBytes / 2 : kPBBytes;
-      const bool sfa_ok = (a_row >> 7) < a_sf_chunks;           // rows past the padded scales: codes are 0
+      const int a_rows = GROUPED ? pair_a_rows(t.valid, (int)rank) : 128;
+      const uint32_t a_bytes =                                  // of both CTAs
+          GROUPED ? (uint32_t)(pair_a_rows(t.valid, 0) + pair_a_rows(t.valid, 1)) * 128 : 2 * kPABytes;
+      // rows past the padded scales: codes are 0
+      const bool sfa_ok = (a_row >> 7) < a_sf_chunks && a_rows > 0;
       const int64_t chunk0 = t.n0 >> 7;
       const int chunks = !t.half && chunk0 + 1 < p.b_sf_row_chunks ? 2 : 1;  // B scale chunks read
       const uint8_t *sfa_src = p.a_sf + 512 * ((int64_t)(a_row >> 7) * p.a_sf_katoms);
@@ -285,16 +298,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t fb = full_base + 8 * stage, sfbar = sff_base + 8 * stage;
         if (role < 2) {
           // the leader expects both CTAs' tiles; the peer's land on the leader's barrier
-          const CUtensorMap *tm = role == 0 ? (i < p.num_kt ? &tmA : &tmT)
+          const CUtensorMap *tm = role == 0 ? (GROUPED ? (a_rows == 128 ? &tmA : a_rows == 64 ? &tmT : &tmLB)
+                                               : i < p.num_kt ? &tmA : &tmT)
                                             : t.half ? (i < p.num_kt ? &tmBh : &tmLBh)
                                                      : (i < p.num_kt ? &tmB : &tmLB);
           const uint32_t dst = role == 0 ? a_base + stage * kPABytes : b_base + stage * kPBBytes;
           const int c0 = i < p.num_kt ? i * 128 : (i - p.num_kt) * 64;
           const int c1 = role == 0 ? a_row : b_row;
           if (rank == 0) {
-            mbar_arrive_expect_tx_u(fb, 2 * (role == 0 ? (uint32_t)kPABytes : b_bytes));
-            tma_load_2d_u(dst, tm, fb, c0, c1);
-          } else {
+            mbar_arrive_expect_tx_u(fb, role == 0 ? a_bytes : 2 * b_bytes);
+            tma_load_2d_u(dst, tm, fb, c0, c1);      // (rank 0 of a grouped tile has rows)
+          } else if (role || a_rows) {
             tma_load_2d_pair_u(dst, tm, full_l + 8 * stage, c0, c1);
           }
         } else if (i < p.num_kt) {

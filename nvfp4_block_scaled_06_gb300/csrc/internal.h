@@ -152,7 +152,8 @@ cudaError_t launch_gemm_fp4(const GemmParams &p, const GemmMaps &maps, int bn, i
 // loads its half of the B tile), maps.bh and maps.lbh (has_half) the same
 // with 64-row boxes; no split-K or accumulation.  With p.gtiles (MXFP4 only;
 // 256-row entries): the grouped product, maps.a over the padded grouped rows,
-// maps.b over the stacked experts.
+// maps.b over the stacked experts, maps.t and maps.lb as maps.a with 64- and
+// 32-row boxes.
 cudaError_t launch_gemm_fp4_pair(const GemmParams &p, const GemmMaps &maps, int num_sms, cudaStream_t st);
 // The product for M <= 32 activation rows with the operands swapped (weights
 // as the MMA's 128-row A side): x = activation codes in 32-row boxes of a
