@@ -568,6 +568,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       const int64_t orow = t.out_row0 + 128 * rank + r;
       const bool row_ok = 128 * (int)rank + r < t.valid;
+      // a grouped tile's boxes must not reach past the expert's rows
+      const bool boxes = p.store_tma && (!GROUPED || 128 * (int)rank + 32 * q + 32 <= t.valid);
 #pragma unroll 1
       for (int half = 0; half < halves; ++half) {
         uint32_t v[4][32];
@@ -581,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(acc_empty_l);
         }
-        if (p.store_tma) {
+        if (boxes) {
           // bf16 through shared memory: this warp's four 32 x 32 boxes take
           // the half's four column chunks (row `lane` of each, its 16-byte
           // pieces at their 64-byte-swizzle positions: conflict-free), then
@@ -613,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int64_t n = t.col0 + (half * 4 + c) * 32;
-              if (n < p.N) tma_store_2d(&tmD, box0 + (uint32_t)(c * 2048), (int32_t)n, (int32_t)(t.m0 + 128 * rank + 32 * q));
+              if (n < p.N) tma_store_2d(&tmD, box0 + (uint32_t)(c * 2048), (int32_t)n, (int32_t)(t.out_row0 + 128 * rank + 32 * q));
             }
             bulk_commit_group();
           }
@@ -722,7 +724,7 @@ cudaError_t launch_gemm_fp4_pair(const GemmParams &p, const GemmMaps &m, int num
   const int64_t resident = resident_pairs((const void *)kernel, p.gtiles ? 2 : p.mx ? 1 : 0, num_sms);
   const int64_t tiles = p.gtiles ? resident : ((p.M + 255) / 256) * (int64_t)p.tiles_n;
   GemmParams q = p;
-  q.store_tma = p.store_tma && m.has_d && !p.gtiles;
+  q.store_tma = p.store_tma && m.has_d;
   // half units need the 64-row B maps, and every half of the last n-tile
   // must hold a column of D (so that its B scale chunk exists)
   q.pair_half_tail = m.has_half && p.N - (int64_t)(p.tiles_n - 1) * 256 > 128;
