@@ -35,7 +35,7 @@
 //               leader's stage barrier (remote arrive for the peer).
 //   warps 6..9  epilogue: drain own 128 x 256 accumulator, arrive on the
 //               leader's "accumulator free" barrier, scale, convert, store
-//               (bf16 through shared-memory boxes and tensor stores).
+//               (through shared-memory boxes and tensor stores).
 // MX: the same kernel for MXFP4 operands (one E8M0 scale per 32 elements): a
 // stage has two scale atoms per 128 rows instead of four, and the MMA
 // (kind::mxf4 scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
@@ -60,8 +60,8 @@ constexpr int kPSfaBytes = 4 * 512;            // 128 A rows x 16 scales (four 1
 constexpr int kPSfbBytes = 2 * 4 * 512;        // 256 B rows x 16 scales (two 128-row chunks)
 constexpr int kPStageBytes = kPABytes + kPBBytes + kPSfaBytes + kPSfbBytes;
 constexpr int kPBarBytes = 256;
-// epilogue staging for the bf16 output's tensor stores: per epilogue warp four
-// 32 x 32 bf16 boxes (2 KB each), 1024-aligned
+// epilogue staging for the output's tensor stores: per epilogue warp four
+// 32 x 32 bf16 boxes (2 KB each) or two fp32 ones, 1024-aligned
 constexpr int kPStgBytes = 4 * 4 * 2048;
 constexpr int kPSmemBytes = kPairStages * kPStageBytes + kPBarBytes + 1024 + kPStgBytes + 1024;
 // TMEM columns of one stage's scales: 4 per K step for A, then 8 per K step
@@ -582,6 +582,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(acc_empty_l);
+        }
+        if (boxes && p.out_fp32) {
+          // fp32 the same way, one column chunk at a time in two boxes in turn
+          // (row `lane`, its 16-byte pieces at their 128-byte-swizzle positions);
+          // every chunk commits a group, empty past N, so that all but the last
+          // group having been read frees the box.  An MXFP4 call of 8191 x
+          // 8192 x 512 takes 63.1 us (76.8 with rows stored by their threads).
+          const uint32_t box0 = smem_u32(stg) + (uint32_t)(q * 2 * 4096);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int64_t n = t.col0 + (half * 4 + c) * 32;
+            const uint32_t box = box0 + (uint32_t)((c & 1) * 4096);
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+            if (n < p.N) {
+              const uint32_t row = box + (uint32_t)(lane * 128);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2)
+                  w[i2] = __float_as_uint(__fmul_rn(__uint_as_float(v[c][4 * k + i2]), alpha));
+                sts128(row + ((k ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+              }
+              fence_proxy_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0) {
+              if (n < p.N) tma_store_2d(&tmD, box, (int32_t)n, (int32_t)(t.out_row0 + 128 * rank + 32 * q));
+              bulk_commit_group();
+            }
+          }
+          continue;
         }
         if (boxes) {
           // bf16 through shared memory: this warp's four 32 x 32 boxes take

@@ -120,7 +120,7 @@ struct GemmParams {
   int *status;
   uint64_t timeout_ns;
   int stall_probe;            // test hook: first wait on a barrier nothing arrives at
-  int store_tma;              // pair kernel, bf16 output: D leaves through GemmMaps::d
+  int store_tma;              // pair kernel: D leaves through GemmMaps::d
   int pair_half_tail;         // pair kernel: a last wave of at most half the pairs runs as 256 x 128 units
   int mx;                     // MXFP4 operands: one E8M0 scale per 32 elements (a 128x4 scale atom is 128
                               // elements long), g_a = g_b = null
@@ -130,7 +130,7 @@ struct GemmParams {
 
 struct GemmMaps {
   CUtensorMap a, b, t, lb;
-  CUtensorMap d;   // pair kernel, bf16 output: D [M][ldd] in 32 x 32 boxes, 64-byte swizzle
+  CUtensorMap d;   // pair kernel: D [M][ldd] in 32 x 32 boxes, 64-byte swizzle (fp32: 128-byte)
   CUtensorMap bh, lbh;   // pair kernel: b and lb with 64-row boxes (the 256 x 128 units)
   bool has_d = false;
   bool has_half = false;
