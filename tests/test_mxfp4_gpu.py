@@ -212,6 +212,30 @@ def test_gemm_non_finite_rows_stay_in_their_rows(M):
     assert np.all(np.abs(got[rest] - y) <= 2e-5 * S)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,pad,shift", [(256, 1000, 24, 0), (300, 1004, 4, 0), (511, 1002, 14, 0), (300, 416, 8, 8),
+                                           (700, 2088, 3, 0), (257, 512, 8, 1), (290, 33, 7, 0)])
+def test_gemm_writes_its_columns_and_rows_only(M, N, pad, shift, out_dtype):
+    """Outputs inside a larger buffer, rows that end off a 16-byte or 32-column
+    boundary: nothing outside [M, N] is written.  A pitch or base that is no
+    multiple of 16 bytes is refused."""
+    rng = np.random.default_rng(M + N)
+    K = 160
+    xb = bits(rng, M, K)
+    wc, wb, wc_d, wsf_d = packed(bits(rng, N, K))
+    buf = torch.full((M + 40, N + pad + shift), 5.0, device="cuda", dtype=out_dtype)
+    if (buf.stride(0) * buf.element_size()) % 16 or (shift * buf.element_size()) % 16:
+        with pytest.raises(nv.NVFP4Error):
+            nv.nvfp4_mxfp4_gemm(wc_d, wsf_d, N, K, a_bf16=dev_bf16(xb), out=buf[:M, shift:shift + N])
+        assert bool((buf == 5.0).all())
+        return
+    nv.nvfp4_mxfp4_gemm(wc_d, wsf_d, N, K, a_bf16=dev_bf16(xb), out=buf[:M, shift:shift + N])
+    y, S = product(mo.dequantize(*mo.quantize(xb)), mo.dequantize(wc, wb))
+    assert_gemm_close(buf[:M, shift:shift + N], y, S)
+    buf[:M, shift:shift + N] = 5.0
+    assert bool((buf == 5.0).all())
+
+
 def test_gemm_strided_x_padded_out_and_full_size_sampled():
     rng = np.random.default_rng(4)
     M, N, K = 200, 136, 512
