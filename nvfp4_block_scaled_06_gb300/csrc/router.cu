@@ -16,13 +16,14 @@
 // its experts in batches of eight, sorts each batch with a fixed network and
 // merges it into its running eight largest, then the lanes' lists are merged
 // pairwise by shuffles.  k_route_any, a warp per token: every other form
-// (top_k > 8, softmax scores with a bias, group counts that do not divide a
-// lane count).  In both a key is an order-preserving integer whose low bits are
+// (top_k > 8, softmax scores with a bias, group counts that are no power of
+// two).  In both a key is an order-preserving integer whose low bits are
 // replaced by the inverted expert index, so that one integer maximum carries
 // the expert along and ties fall to the lowest index.  Where two neighbouring
 // results (the largest rejected key included) agree in every bit that is left
-// of the key, the token's selection runs again on the whole keys.  bf16 logits
-// without a bias lose no bits and never need that.
+// of the key, the token's selection runs again on the whole keys (bf16 logits
+// without a bias lose no bits), as it does where a chosen key turns out to be an
+// infinity or a NaN that k_route_few did not look for.
 #include <cfloat>
 
 #include "internal.h"
@@ -392,14 +393,15 @@ __device__ __forceinline__ uint32_t route_key(const RouteTopkParams &p, int e, f
   return in ? u : 0u;
 }
 
-// The exact selection of one token by a whole warp: k rounds, each the largest
-// (key, lowest index) below the previous round's.  Lane j returns choice j.
+// The exact selection of one token by a whole warp, from choice `from` on: each
+// round the largest (key, lowest index) below the previous one's, last and
+// last_e (~0 and -1: none).  Lane j >= from returns choice j.
 template <typename T, bool kScored>
-__device__ __noinline__ int route_exact(const RouteTopkParams &p, const T *row, uint32_t keep) {
+__device__ __noinline__ int route_exact(const RouteTopkParams &p, const T *row, uint32_t keep, int from, uint32_t last,
+                                        int last_e) {
   const int lane = threadIdx.x & 31;
-  uint32_t last = 0xffffffffu;
-  int last_e = -1, id = -1;
-  for (int j = 0; j < p.top_k; ++j) {
+  int id = -1;
+  for (int j = from; j < p.top_k; ++j) {
     uint32_t best = 0u;
     int best_e = 0;
     for (int e = lane; e < p.num_experts; e += 32) {
@@ -425,9 +427,9 @@ __device__ __noinline__ int route_exact(const RouteTopkParams &p, const T *row, 
 // kernel (ALU pipe 70-85% busy): 65521 tokens, 256 experts, bf16, top 8 in 18.3 us
 // (37.7 MB, 2.1 TB/s); the one-warp-per-token kernel above took 69 us.
 // L lanes per token.  kScored: keys or group values are sigmoid scores; kVec:
-// a lane's eight experts are whole 16-byte vectors.  With groups a lane's
-// experts are a run of E / L inside one group (L / G lanes per group);
-// without, the lanes' batches of eight interleave.
+// a lane's eight experts are whole 16-byte vectors.  With groups L / G lanes
+// share a group and take a run of its experts each (the last ones a shorter one
+// or none); without, the lanes' batches of eight interleave.
 template <typename T, int L, bool kScored, bool kVec>
 __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopkParams p) {
   griddep_launch_dependents();
@@ -439,8 +441,15 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
   const int E = p.num_experts, k = p.top_k;
   const uint32_t imask = p.index_mask;
   const bool grouped = p.num_groups > 1;
-  const int first = grouped ? sub * (E / L) : sub * 8;
-  const int end = grouped ? first + E / L : E, step = grouped ? 8 : 8 * L;
+  int first = sub * 8, end = E;
+  const int step = grouped ? 8 : 8 * L;
+  if (grouped) {
+    const int shift = __ffs(L) - __ffs(p.num_groups), lanes = 1 << shift, g = sub >> shift;
+    const int run = (p.group_size + lanes - 1) >> shift;
+    end = (g + 1) * p.group_size;
+    first = min(g * p.group_size + (sub & (lanes - 1)) * run, end);
+    end = min(first + run, end);
+  }
   const int64_t stride = (int64_t)gridDim.x * kRouterWarps * kTok;
   for (int64_t t0 = ((int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5)) * kTok; t0 < p.tokens; t0 += stride) {
     const int64_t t = t0 + lane / L;
@@ -490,14 +499,14 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
     }
     uint32_t keep = 0xffffffffu;       // groups that stay, bit g
     if (grouped) {
-      const int G = p.num_groups, per = L / G;       // lanes per group, a power of two
+      const int G = p.num_groups, per = 1 << (__ffs(L) - __ffs(G));       // lanes per group
       for (int o = 1; o < per; o <<= 1) {
         const float o1 = __shfl_xor_sync(kAll, t1, o), o2 = __shfl_xor_sync(kAll, t2, o);
         t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
         t1 = fmaxf(t1, o1);
       }
       const float score = p.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
-      const int g = sub / per;
+      const int g = sub >> (__ffs(L) - __ffs(G));
       int better = 0;
       keep = 0u;
       for (int j = 0; j < G; ++j) {
@@ -532,24 +541,81 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
       id[q] = m && sub + q * L < k ? (int)(imask - (m & imask)) : -1;
     }
     if constexpr (kRest || kPlain) {
-      bool close = kPlain && run[0] >= 0xFF800000u;
+      bool close = false, redo = kPlain && run[0] >= 0xFF800000u;
+      int sure = k;                    // choices that no key outside the list can take
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t below = i < 7 ? run[i < 7 ? i + 1 : 7] : rest;
-        if (kPlain) close |= i < k && run[i] < 0x00800000u;
-        // two neighbours agree in the bits that are left
-        if (kRest) close |= i < k && below && ((run[i] ^ below) & ~imask) == 0u;
+      for (int i = 7; i >= 0; --i) {
+        if (kPlain) redo |= i < k && run[i] < 0x00800000u;
+        // neighbours that agree in the bits that are left
+        if (kRest) {
+          if (i < k && rest && ((run[i] ^ rest) & ~imask) == 0u) sure = i;
+          if (i < 7) close |= i < k && run[i < 7 ? i + 1 : 7] && ((run[i] ^ run[i < 7 ? i + 1 : 7]) & ~imask) == 0u;
+        }
       }
-      uint32_t again = __ballot_sync(kAll, close && live && sub == 0);
+      uint32_t whole[kSlots];          // of this lane's slots, once they are known
+      if (kRest && __any_sync(kAll, close || sure < k)) {
+        // the list in the order of its whole keys
+        int e[kSlots], rank[kSlots];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i == sub + q * L) m = run[i];
+          float g;
+          e[q] = m ? (int)(imask - (m & imask)) : E;
+          whole[q] = m ? route_key<kScored>(p, e[q], load1(row + e[q]), g) : 0u;
+          rank[q] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t wj = __shfl_sync(kAll, whole[j / L], lane - sub + j % L);
+          const int ej = __shfl_sync(kAll, e[j / L], lane - sub + j % L);
+#pragma unroll
+          for (int q = 0; q < kSlots; ++q)
+            rank[q] += wj > whole[q] || (wj == whole[q] && (ej < e[q] || (ej == e[q] && j < sub + q * L)));
+        }
+        uint32_t sorted[kSlots];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t wj = __shfl_sync(kAll, whole[j / L], lane - sub + j % L);
+          const int ej = __shfl_sync(kAll, e[j / L], lane - sub + j % L);
+          const int rj = __shfl_sync(kAll, rank[j / L], lane - sub + j % L);
+#pragma unroll
+          for (int q = 0; q < kSlots; ++q) {
+            if (rj == sub + q * L) {
+              sorted[q] = wj;
+              id[q] = wj && rj < k ? ej : -1;
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) whole[q] = sorted[q];
+      }
+      uint32_t again = __ballot_sync(kAll, (redo || sure < k) && live && sub == 0);
       while (again) {
         const int src = __ffs(again) - 1;            // the token's first lane
         again &= again - 1;
         const T *r = reinterpret_cast<const T *>(p.logits) + (t0 + src / L) * p.ld;
-        const int e = route_exact<T, kScored>(p, r, __shfl_sync(kAll, keep, src));
+        const int from = __shfl_sync(kAll, redo ? 0 : sure, src);
+        uint32_t last = 0xffffffffu;
+        int last_e = -1;
+        if (kRest && from > 0) {
+#pragma unroll
+          for (int q = 0; q < kSlots; ++q) {
+            const uint32_t lw = __shfl_sync(kAll, whole[q], src + (from - 1) % L);
+            const int le = __shfl_sync(kAll, id[q], src + (from - 1) % L);
+            if ((from - 1) / L == q) {
+              last = lw;
+              last_e = le;
+            }
+          }
+        }
+        const int e = route_exact<T, kScored>(p, r, __shfl_sync(kAll, keep, src), from, last, last_e);
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
           const int v = __shfl_sync(kAll, e, (sub + q * L) & 31);
-          if (lane - sub == src) id[q] = sub + q * L < k ? v : -1;
+          if (lane - sub == src && sub + q * L >= from) id[q] = sub + q * L < k ? v : -1;
         }
       }
     }
@@ -868,7 +934,7 @@ cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   int L = 32;
   while (L > 4 && (L > G || G == 1) && (p.tokens * (L / 2) >= (int64_t)num_sms * 16 * 32 || E < 8 * L)) L /= 2;
   L = std::max(L, G);
-  const bool vec = E % 8 == 0 && (G == 1 || E / L % 8 == 0) && p.ld * sizeof(T) % 16 == 0 &&
+  const bool vec = E % 8 == 0 && (G == 1 || E % (8 * L) == 0) && p.ld * sizeof(T) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
   switch (L) {
     case 4: return launch_few<T, 4, kScored>(p, vec, num_sms, st);
@@ -878,12 +944,11 @@ cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   }
 }
 // The forms that k_route_few takes: up to 8 choices; keys that need no row
-// statistics; groups that are whole lanes (a power of two of them, E / 32
-// experts or more each, so that a lane count from G to 32 divides E).
+// statistics; a power of two of groups, up to 32 (whole lanes for each).
 bool takes_few(const RouteTopkParams &p) {
   if (p.top_k > 8 || (p.softmax && (p.bias || p.rank_by_score))) return false;
   const int G = p.num_groups;
-  return G == 1 || ((G & (G - 1)) == 0 && p.num_experts % 32 == 0);
+  return G <= 32 && (G & (G - 1)) == 0;
 }
 
 // Values per lane by the number of experts; vector loads where the rows allow

@@ -82,6 +82,19 @@ def test_route_groups(E, G, kg, k, score, group_top):
                         group_top=group_top)
 
 
+@pytest.mark.parametrize("score,group_top", [("sigmoid", 2), ("softmax", 1)])
+@pytest.mark.parametrize("T,E,G,kg,k", [(67, 22, 2, 1, 6), (67, 44, 4, 3, 8), (33, 72, 8, 5, 7), (9, 508, 4, 2, 8),
+                                        (40, 264, 8, 4, 8), (25, 16, 16, 3, 3), (5, 32 * 31, 32, 2, 8), (7, 6, 2, 1, 3),
+                                        (20011, 66, 2, 1, 8), (10007, 264, 8, 4, 8)])
+def test_route_groups_of_any_size(T, E, G, kg, k, score, group_top):
+    """Groups whose experts do not divide among their lanes."""
+    rng = np.random.default_rng(E + T)
+    for dtype in (torch.bfloat16, torch.float32):
+        for bias in (None, rng.standard_normal(E) * 0.1):
+            check_route(make_logits(T, E, dtype, 3 * E + k), k, bias=bias, score=score, num_groups=G, topk_groups=kg,
+                        group_top=group_top, renormalize=bias is None)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_route_ties_go_to_the_lowest_index(dtype):
     for E, k in [(256, 8), (64, 8), (100, 6), (512, 10)]:
