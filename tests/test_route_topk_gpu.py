@@ -82,6 +82,40 @@ def test_route_groups(E, G, kg, k, score, group_top):
                         group_top=group_top)
 
 
+@pytest.mark.parametrize("T", [3, 700, 12011])
+@pytest.mark.parametrize("E,G,kg", [(256, 1, 1), (100, 1, 1), (264, 8, 4), (128, 4, 2)])
+def test_route_close_keys_in_every_list_length(T, E, G, kg):
+    """Keys that differ in their last bits only, more of them than a list holds,
+    and equal ones: lists of 8 and of 16 choose as the whole keys do."""
+    rng = np.random.default_rng(E + T)
+    low = 1.0 + rng.integers(0, 4 * E, (T, E)) * 2.0 ** -23
+    x = torch.from_numpy(np.where(rng.random((T, E)) < 0.02, -low, low).astype(np.float32)).cuda()
+    bias = rng.integers(0, 8, E) * 2.0 ** -24
+    for k in (1, 5, 8, 9, 12, 16):
+        check_route(x, k, score="sigmoid", renormalize=True, num_groups=G, topk_groups=kg, group_top=1)
+        form = dict(bias=torch.from_numpy(bias.astype(np.float32)).cuda(), score="sigmoid", num_groups=G,
+                    topk_groups=kg, group_top=2)
+        ids = nv.nvfp4_route_topk(x, k, **form)["expert_ids"]
+        # the same choices as the first ones of a longer list, which another kernel makes
+        longer = nv.nvfp4_route_topk(x, 20, **form)["expert_ids"]
+        assert torch.equal(ids, longer[:, :k])
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,E,k", [(5, 16, 16), (70, 40, 10), (300, 256, 9), (11003, 64, 12), (10501, 250, 16)])
+def test_route_nine_to_sixteen(T, E, k, dtype, score):
+    rng = np.random.default_rng(k + E)
+    for bias in (None, rng.standard_normal(E) * 0.2):
+        check_route(make_logits(T, E, dtype, T + k), k, bias=bias, score=score, renormalize=bias is not None)
+    # fewer usable experts than choices
+    x = make_logits(T, E, dtype, T)
+    x[:, 3:] = float("-inf")
+    x[::2, 1] = float("nan")
+    ids, w = check_route(x, k, score=score)
+    assert np.all((ids >= 0).sum(1) == np.where(np.arange(T) % 2 == 0, 2, 3)) and np.all(w[ids < 0] == 0)
+
+
 @pytest.mark.parametrize("score,group_top", [("sigmoid", 2), ("softmax", 1)])
 @pytest.mark.parametrize("T,E,G,kg,k", [(67, 22, 2, 1, 6), (67, 44, 4, 3, 8), (33, 72, 8, 5, 7), (9, 508, 4, 2, 8),
                                         (40, 264, 8, 4, 8), (25, 16, 16, 3, 3), (5, 32 * 31, 32, 2, 8), (7, 6, 2, 1, 3),
