@@ -40,6 +40,11 @@
 // stage has two scale atoms per 128 rows instead of four, and the MMA
 // (kind::mxf4 scale_vec::2X) of K step j takes half (j & 1) of atom j / 2.
 // 8192 x 2048 x 6144: 40-41 us cold = 5.1 PFLOP/s (NVFP4: 47.6-49.4 us).
+// GROUPED: the products of routed MXFP4 experts, a table of tiles of up to 256
+// rows of one expert.  A CTA loads as many rows of A as its half of the tile
+// has (32, 64 or 128) and boxes of D that are not full are stored directly.
+// 4096 tokens x 8 of 256 experts, 2048 x 6144: 291 us of 1.25 GB read; 512 rows
+// on each of 128 experts, 2048 x 512: 70% of the 128 x 256 tiles' call.
 // Every wait is bounded; on expiry a CTA records a timeout, drains its own
 // copies (and, in the leader, its MMAs) and leaves its loops; the peer's waits
 // then expire too.  Both CTAs meet at a cluster barrier before freeing TMEM.
