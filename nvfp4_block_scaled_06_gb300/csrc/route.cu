@@ -26,7 +26,8 @@ __global__ void __launch_bounds__(1024) k_route_hist(const RouteParams p) {
   const int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x;
   if (threadIdx.x < p.chunk && i < p.pairs) {
     const int e = p.expert_ids[i];
-    if (NVFP4_NOTE(e >= 0 && e < p.num_experts, p.status)) atomicAdd(&sh_hist[e], 1);   // others are dropped
+    // -1 (a missing choice) is dropped, like any other id outside the experts
+    if (NVFP4_NOTE(e >= -1 && e < p.num_experts, p.status) && e >= 0) atomicAdd(&sh_hist[e], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.num_experts; e += blockDim.x)
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(1024) k_route_one(const RouteParams p) {
   const bool in = threadIdx.x < p.pairs;
   if (in) {
     const int e = p.expert_ids[threadIdx.x];
-    if (NVFP4_NOTE(e >= 0 && e < E, p.status)) atomicAdd(&sh_one[e], 1);   // others are dropped
+    if (NVFP4_NOTE(e >= -1 && e < E, p.status) && e >= 0) atomicAdd(&sh_one[e], 1);   // as above
   }
   __syncthreads();
   int32_t off, poff;
