@@ -616,6 +616,8 @@ size_t nvfp4_mxfp4_dgrad_workspace_bytes(const nvfp4_mxfp4_dgrad_args *args);
  * Ids outside [0, num_experts) (nvfp4_route_topk's -1) take no grouped row: the
  * rows of d past the last offset are not written, perm_out is -1 there, and the
  * combine leaves such slots out (a token without any gets a row of zeros).
+ * The expert outputs are held in fp32 up to the weighted sum, which is rounded
+ * to bf16 once (nvfp4_moe_down_combine rounds each of them as well).
  * ------------------------------------------------------------------------ */
 typedef struct {
   int64_t num_tokens, top_k, num_experts, N, K;

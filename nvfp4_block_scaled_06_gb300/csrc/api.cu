@@ -953,7 +953,7 @@ nvfp4_status run_moe_down(const nvfp4_moe_down_args *a, const MoeDownPlan &pl, i
   gp.prof_end = a->prof_end;
   nvfp4_status s = run_grouped_products(gp, status, tmo, sms, st);
   if (s != NVFP4_OK) return s;
-  return cuda_status(launch_moe_combine(pl.d, a->perm, pl.inv, a->route_weights, a->num_tokens,
+  return cuda_status(launch_moe_combine(pl.d, false, a->perm, pl.inv, a->route_weights, a->num_tokens,
                                         (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
                                         status, layout_makes_inverse(pl.prow_max), pl.goffsets + a->num_experts));
 }
@@ -1729,7 +1729,7 @@ struct MxMoeDownPlan {
   int32_t *goffsets = nullptr, *poffsets = nullptr, *row_map = nullptr, *nmt = nullptr, *inv = nullptr;
   GroupTile *gtiles = nullptr;
   uint8_t *hq = nullptr, *hsf = nullptr;
-  __nv_bfloat16 *d = nullptr;
+  float *d = nullptr;   // the experts' outputs: rounded after the weighted sum, not before it
 };
 
 void plan_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, MxMoeDownPlan *pl) {
@@ -1744,7 +1744,7 @@ void plan_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, MxMoeDownPlan *pl) {
   pl->inv = c.take<int32_t>((size_t)P * 4);
   pl->hq = c.take<uint8_t>((size_t)pl->prow_max * a->K / 2);
   pl->hsf = c.take<uint8_t>(mx_sf_swizzled_bytes(pl->prow_max, a->K));
-  pl->d = c.take<__nv_bfloat16>((size_t)P * a->N * 2);
+  pl->d = c.take<float>((size_t)P * a->N * 4);
   pl->ws = c.off;
 }
 
@@ -1794,13 +1794,14 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
   gp.w_codes = a->w_codes;
   gp.w_sf = a->w_sf;
   gp.d = pl.d;
+  gp.out_fp32 = 1;
   gp.mx = 1;
   gp.few_rows = mx_few_rows(a->num_tokens, a->top_k, a->num_experts);
   gp.prof_begin = a->prof_begin;
   gp.prof_end = a->prof_end;
   nvfp4_status s = run_grouped_products(gp, status, g_timeout_ns.load(), sms, st);
   if (s != NVFP4_OK) return s;
-  return cuda_status(launch_moe_combine(pl.d, a->perm, pl.inv, a->route_weights, a->num_tokens,
+  return cuda_status(launch_moe_combine(pl.d, true, a->perm, pl.inv, a->route_weights, a->num_tokens,
                                         (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
                                         status, layout_makes_inverse(pl.prow_max), pl.goffsets + a->num_experts));
 }

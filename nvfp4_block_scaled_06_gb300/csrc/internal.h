@@ -245,9 +245,9 @@ cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pa
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,
                                        int num_sms, cudaStream_t st, int *status, int32_t *inv, int tile_rows);
-// y[t] = sum_j w[t][j] d[inverse perm (t*top_k + j)] (bf16 rows, fp32 sums);
+// y[t] = sum_j w[t][j] d[inverse perm (t*top_k + j)] (bf16 or fp32 rows, fp32 sums);
 // inv holds the inverse already, or is made here from perm's first *rows entries.
-cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,
+cudaError_t launch_moe_combine(const void *d, bool d_fp32, const int32_t *perm, int32_t *inv, const float *w,
                                int64_t tokens, int top_k, int64_t N, __nv_bfloat16 *y, int num_sms,
                                cudaStream_t st, int *status, bool inv_ready, const int32_t *rows);
 

@@ -450,23 +450,52 @@ __global__ void k_fill_i32(int32_t *p, int64_t n, int32_t v) {
     p[i] = v;
 }
 
+// Sixteen bytes of D as floats.
+__device__ __forceinline__ void unpack16(uint4 q, float (&f)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack16(uint4 q, float (&f)[4]) {
+  f[0] = __uint_as_float(q.x);
+  f[1] = __uint_as_float(q.y);
+  f[2] = __uint_as_float(q.z);
+  f[3] = __uint_as_float(q.w);
+}
+// The sums' one rounding to bf16.
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void store_sums(__nv_bfloat16 *y, const float (&f)[8]) {
+  *reinterpret_cast<uint4 *>(y) = make_uint4(round_pair(f[0], f[1]), round_pair(f[2], f[3]), round_pair(f[4], f[5]),
+                                             round_pair(f[6], f[7]));
+}
+__device__ __forceinline__ void store_sums(__nv_bfloat16 *y, const float (&f)[4]) {
+  *reinterpret_cast<uint2 *>(y) = make_uint2(round_pair(f[0], f[1]), round_pair(f[2], f[3]));
+}
+
 // A warp takes a token, or with few tokens one of `parts` interleaved column
 // ranges of it (32 tokens of 6144 columns, top 8: 4.5 us, with a warp each 22): its
 // slots' row indices and weights are read once, and for top_k <= 8 the 16-byte
 // loads of all slots are in flight together before the sums (which keep the
-// slot order).
-__global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__restrict__ d,
-                                                     const int32_t *__restrict__ inv,
+// slot order).  TD: bf16, or float (the MXFP4 experts' outputs, which are not
+// rounded before the sum).
+template <typename TD>
+__global__ void __launch_bounds__(256) k_moe_combine(const TD *__restrict__ d, const int32_t *__restrict__ inv,
                                                      const float *__restrict__ w, int64_t tokens, int top_k,
                                                      int64_t N, __nv_bfloat16 *__restrict__ y, int parts,
                                                      int *status) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
-  constexpr int kMaxK = 8;
+  constexpr int kMaxK = 8, V = 16 / (int)sizeof(TD);
   const int lane = threadIdx.x & 31;
   const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  const int64_t vecs = N / 8;                       // 16-byte vectors of a row
+  const int64_t vecs = N / V;                       // 16-byte vectors of a row
   for (int64_t item = warp; item < tokens * parts; item += nwarps) {
     const int64_t t = item / parts;
     const int64_t v0 = (item - t * parts) * 32 + lane, vstep = 32 * (int64_t)parts;
@@ -484,57 +513,40 @@ __global__ void __launch_bounds__(256) k_moe_combine(const __nv_bfloat16 *__rest
         uint4 q[kMaxK];
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j) q[j] = rows[j] ? __ldg(rows[j] + v) : make_uint4(0, 0, 0, 0);
-        float acc[8];
+        float acc[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j) {
           if (j >= top_k) break;
-          const uint32_t qw[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+          float f[V];
+          unpack16(q[j], f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[2 * i] = __fmaf_rn(wj[j], __uint_as_float(qw[i] << 16), acc[2 * i]);
-            acc[2 * i + 1] = __fmaf_rn(wj[j], __uint_as_float(qw[i] & 0xFFFF0000u), acc[2 * i + 1]);
-          }
+          for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(wj[j], f[i], acc[i]);
         }
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
-          o[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        reinterpret_cast<uint4 *>(y + t * N)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+        store_sums(y + t * N + v * V, acc);
       }
       continue;
     }
     for (int64_t v = v0; v < vecs; v += vstep) {
-      float acc[8];
+      float acc[V];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < V; ++i) acc[i] = 0.0f;
       for (int j = 0; j < top_k; ++j) {
         const int64_t g = inv[t * top_k + j];
         if (g < 0 || !NVFP4_GUARD(g < tokens * top_k, status)) continue;
         const float wv = w[t * top_k + j];
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(d + g * N) + v);
-        const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+        float f[V];
+        unpack16(__ldg(reinterpret_cast<const uint4 *>(d + g * N) + v), f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[2 * i] = __fmaf_rn(wv, __uint_as_float(qw[i] << 16), acc[2 * i]);
-          acc[2 * i + 1] = __fmaf_rn(wv, __uint_as_float(qw[i] & 0xFFFF0000u), acc[2 * i + 1]);
-        }
+        for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(wv, f[i], acc[i]);
       }
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
-        o[i] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-      reinterpret_cast<uint4 *>(y + t * N)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+      store_sums(y + t * N + v * V, acc);
     }
   }
 }
 
-cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int32_t *inv, const float *w,
+cudaError_t launch_moe_combine(const void *d, bool d_fp32, const int32_t *perm, int32_t *inv, const float *w,
                                int64_t tokens, int top_k, int64_t N, __nv_bfloat16 *y, int num_sms,
                                cudaStream_t st, int *status, bool inv_ready, const int32_t *rows) {
   const int64_t pairs = tokens * top_k;
@@ -546,10 +558,15 @@ cudaError_t launch_moe_combine(const __nv_bfloat16 *d, const int32_t *perm, int3
     if (e != cudaSuccess) return e;
   }
   // column ranges until every SM has 32 warps
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((N / 8 + 31) / 32, (int64_t)num_sms * 32 / tokens));
+  const int64_t vecs = N / (d_fp32 ? 4 : 8);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((vecs + 31) / 32, (int64_t)num_sms * 32 / tokens));
   const int64_t c2 = std::max<int64_t>(1, std::min<int64_t>((tokens * parts + 7) / 8, (int64_t)num_sms * 8));
-  return launch_pdl(k_moe_combine, dim3((unsigned)c2), dim3(256), 0, st, d, (const int32_t *)inv, w, tokens, top_k,
-                    N, y, (int)parts, status);
+  if (d_fp32)
+    return launch_pdl(k_moe_combine<float>, dim3((unsigned)c2), dim3(256), 0, st, static_cast<const float *>(d),
+                      (const int32_t *)inv, w, tokens, top_k, N, y, (int)parts, status);
+  return launch_pdl(k_moe_combine<__nv_bfloat16>, dim3((unsigned)c2), dim3(256), 0, st,
+                    static_cast<const __nv_bfloat16 *>(d), (const int32_t *)inv, w, tokens, top_k, N, y, (int)parts,
+                    status);
 }
 
 }  // namespace nvfp4

@@ -564,3 +564,30 @@ def test_refusals():
     with pytest.raises(ValueError):
         nv.nvfp4_mxfp4_moe_down_combine(x, ids.reshape(-1), ids.reshape(-1)[:2],
                                         torch.ones(16, 2, device="cuda"), c, sf, 256, 64, 1)
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(5, 8, 4, 256, 96), (32, 32, 8, 512, 352), (300, 8, 8, 256, 544),
+                                       (700, 24, 12, 512, 160)])
+def test_moe_down_rounds_once(T, E, k, N, K):
+    """The expert outputs reach the weighted sum in fp32 and the sum is rounded
+    to bf16 once, also where slots of opposite weights cancel: 2e-5 of the
+    absolute terms per product as everywhere, k + 1 roundings of the sum in fp32
+    (2^-24 of its absolute terms each), half a bf16 ulp of the result."""
+    rng, wl, wc_d, wsf_d, ids = expert_case(T, E, k, N, K, seed=51)
+    h = bits(rng, T * k, K)
+    flat = ids.reshape(-1)
+    perm = np.argsort(flat, kind="stable")
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=E))])
+    hv = mo.dequantize(*mo.quantize(h))
+    d, S = np.zeros((T * k, N)), np.zeros((T * k, N))
+    for e in range(E):
+        r = slice(offsets[e], offsets[e + 1])
+        d[r], S[r] = product(hv[r], wl[e])
+    w = rng.uniform(-1, 1, (T, k)).astype(np.float32)
+    y = nv.nvfp4_mxfp4_moe_down_combine(dev_bf16(h), torch.from_numpy(perm.astype(np.int32)).cuda(),
+                                        torch.from_numpy(offsets.astype(np.int32)).cuda(),
+                                        torch.from_numpy(w).cuda(), wc_d, wsf_d, N, K, E)
+    want, term = o.moe_combine(d, perm, w, k), o.moe_combine(np.abs(d), perm, np.abs(w), k)
+    before = 2e-5 * o.moe_combine(S, perm, np.abs(w), k) + (k + 1) * 2.0 ** -24 * term
+    err = np.abs(y.float().cpu().numpy() - want)
+    assert np.all(err <= before + 0.5 * o.bf16_ulp(np.abs(want) + before)), float(np.max(err / np.abs(want).max()))
