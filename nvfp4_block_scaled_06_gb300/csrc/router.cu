@@ -814,9 +814,13 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
 // 65521 tokens, 160 experts, bf16: 10.0 us of 45.1 MB = 4.5 TB/s (18 us when the
 // row was read twice, 13.7 us with the chosen logits' loads, which wait for the
 // ids, issued before the row's); bound by load latency.
-// The first attempt takes every logit for finite; a row for which that shows
-// to be wrong (the maximum infinite, the sum NaN) sends its warp through a
-// second one that masks -inf and NaN and takes +inf for the largest fp32.
+// The first attempt takes every logit for finite and the maximum for small
+// enough that its product with log2(e) keeps its fraction: rounding that product
+// scales every term of the row by the same 2^r.  Up to 1024 terms, the largest
+// of them 2^r, sum to between 2^r and 2^(r + 10), so a sum in [1/2, 2048] bounds r
+// by 11.  A row with any other sum (a maximum that is infinite or beyond about
+// 1e8, a NaN) sends its warp through a second attempt, which takes x - m before
+// the product, masks -inf and NaN and takes +inf for the largest fp32.
 template <typename T, int L>
 __global__ void __launch_bounds__(kRouterWarps * 32, 5) k_route_softmax_backward(const RouteGradParams p) {
   griddep_launch_dependents();
@@ -885,7 +889,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, 5) k_route_softmax_backward
       }
       s = sum_tok(s);
       ps = attempt ? (xs > -INFINITY ? __expf(finite_top(xs) - m) : 0.0f) : exp2_approx(fmaf(xs, kLog2e, -shift));
-      if (attempt || __all_sync(kAll, m <= FLT_MAX && s <= FLT_MAX)) break;   // (a NaN compares false)
+      if (attempt || __all_sync(kAll, s >= 0.5f && s <= 2048.0f)) break;   // (a NaN compares false)
     }
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
     ps *= inv;

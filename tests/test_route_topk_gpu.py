@@ -343,3 +343,44 @@ def test_route_refusals():
     ids = torch.zeros(4, 4, dtype=torch.int64, device="cuda")
     with pytest.raises(TypeError):
         nv.nvfp4_route_topk_backward(x, ids, torch.zeros(4, 4, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,k", [(64, 6), (63, 6), (256, 8), (250, 8), (1024, 20), (1001, 20)])
+def test_route_backward_softmax_at_any_offset(E, k, dtype):
+    """The dense softmax gradient of rows far from zero: all logits equal, two
+    equal largest ones over the others, and a spread of ordinary size around
+    the offset, for rows in whole vectors and not.  The differences of a row's
+    logits are exact in fp32 or so large that their exponential is 0, so the
+    tolerance of test_route_backward holds unchanged."""
+    top = float(torch.finfo(dtype).max)
+    offsets = [0.0] + [s * v for v in (100.0, 3e4, 1e6, 3e10, 1.0007e12, 1e15, 1e30, 2.5e38, top) for s in (1, -1)]
+    rng = np.random.default_rng(E)
+    rows = []
+    for v in offsets:
+        rows.append(np.full(E, v))
+        tied = np.full(E, v / 2 if v > 0 else max(2 * v, -top))
+        tied[[3, E - 2]] = v
+        rows.append(tied)
+        rows.append(np.clip(v + rng.standard_normal(E) * 2.0, -top, top))
+    x = torch.from_numpy(np.array(rows)).to(dtype).cuda()
+    T = x.shape[0]
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    ids[::2, 0], ids[::2, 1] = 3, E - 2
+    for t in range(T):                       # one of each (a duplicate of the two above counts as missing)
+        seen = set()
+        for j in range(k):
+            if ids[t, j] in seen:
+                ids[t, j] = -1
+            seen.add(ids[t, j])
+    g = rng.standard_normal((T, k)).astype(np.float32)
+    got = host(nv.nvfp4_route_topk_backward(x, torch.from_numpy(ids.astype(np.int32)).cuda(),
+                                            torch.from_numpy(g).cuda(), score="softmax", renormalize=False, scale=2.5))
+    xh = host(x)
+    want = mo.route_topk_backward(xh, ids, g.astype(np.float64), "softmax", False, 2.5)
+    tol = 2.0 ** -17 * backward_scale(xh, ids, g.astype(np.float64), "softmax", False, 2.5) + 1e-30
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * np.abs(want)
+    bad = np.argwhere(~(np.abs(got - want) <= tol))
+    assert bad.size == 0, (len(bad), sorted({offsets[r // 3] for r in bad[:, 0]}), got[tuple(bad[0])],
+                           want[tuple(bad[0])])
