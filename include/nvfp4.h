@@ -655,7 +655,8 @@ nvfp4_status nvfp4_mxfp4_moe_down_combine(const nvfp4_mxfp4_moe_down_args *args,
 size_t nvfp4_mxfp4_moe_down_workspace_bytes(const nvfp4_mxfp4_moe_down_args *args);
 
 /* ------------------------------------------------------------------------ *
- * Size queries and status.
+ * Size queries and status.  (The *_workspace_bytes queries above answer 0 for
+ * NULL and for sizes below 1, which their calls refuse.)
  * ------------------------------------------------------------------------ */
 /* Bytes of packed codes of a [rows][cols] matrix: rows * cols / 2. */
 size_t nvfp4_codes_bytes(int64_t rows, int64_t cols);

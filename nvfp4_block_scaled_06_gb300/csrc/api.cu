@@ -10,6 +10,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -347,6 +348,14 @@ nvfp4_status validate_gemm(const nvfp4_gemm_args *a) {
   if ((a->a_bf16 || a->lora_x) && a->lda % 8 != 0) return NVFP4_ERR_ALIGNMENT;
   if (a->a_bf16 && !aligned(a->a_bf16, 16)) return NVFP4_ERR_ALIGNMENT;
   return NVFP4_OK;
+}
+
+// The workspace queries come before a call's checks: a size below 1, which the
+// call refuses, needs no workspace (and no plan, whose divisions assume sizes).
+bool any_empty(std::initializer_list<int64_t> sizes) {
+  for (int64_t n : sizes)
+    if (n < 1) return true;
+  return false;
 }
 
 nvfp4_status check_workspace(void *ws, size_t have, size_t need) {
@@ -1929,7 +1938,7 @@ nvfp4_status nvfp4_read_device_status(void *workspace, nvfp4_stream stream) {
 }
 
 size_t nvfp4_quantize_workspace_bytes(const nvfp4_quant_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->batch, a->rows, a->cols})) return 0;
   nvfp4_quant_args c = *a;
   c.workspace = nullptr;
   QuantPlan pl;
@@ -1949,7 +1958,7 @@ nvfp4_status nvfp4_quantize(const nvfp4_quant_args *a, nvfp4_stream stream) {
 }
 
 size_t nvfp4_gemm_workspace_bytes(const nvfp4_gemm_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->M, a->N, a->K})) return 0;
   nvfp4_gemm_args c = *a;
   c.workspace = nullptr;
   GemmPlan pl;
@@ -1969,7 +1978,7 @@ nvfp4_status nvfp4_gemm(const nvfp4_gemm_args *a, nvfp4_stream stream) {
 }
 
 size_t nvfp4_grouped_workspace_bytes(const nvfp4_grouped_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->num_tokens, a->top_k, a->num_experts, a->N, a->K})) return 0;
   nvfp4_grouped_args c = *a;
   c.workspace = nullptr;
   GroupedPlan pl;
@@ -1989,7 +1998,7 @@ nvfp4_status nvfp4_grouped_gemm(const nvfp4_grouped_args *a, nvfp4_stream stream
 }
 
 size_t nvfp4_lora_workspace_bytes(const nvfp4_lora_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->M, a->N, a->K})) return 0;
   nvfp4_lora_args c = *a;
   c.workspace = nullptr;
   LoraPlan pl;
@@ -2020,7 +2029,7 @@ nvfp4_status nvfp4_dequantize(const nvfp4_dequant_args *a, nvfp4_stream stream) 
 }
 
 size_t nvfp4_dgrad_workspace_bytes(const nvfp4_dgrad_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->M, a->N, a->K})) return 0;
   return dgrad_workspace(a);
 }
 
@@ -2034,7 +2043,7 @@ nvfp4_status nvfp4_dgrad(const nvfp4_dgrad_args *a, nvfp4_stream stream) {
 }
 
 size_t nvfp4_wgrad_workspace_bytes(const nvfp4_wgrad_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->M, a->N, a->K})) return 0;
   nvfp4_wgrad_args c = *a;
   c.workspace = nullptr;
   WgradPlan pl;
@@ -2054,7 +2063,7 @@ nvfp4_status nvfp4_wgrad(const nvfp4_wgrad_args *a, nvfp4_stream stream) {
 }
 
 size_t nvfp4_moe_down_workspace_bytes(const nvfp4_moe_down_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->num_tokens, a->top_k, a->num_experts, a->N, a->K})) return 0;
   nvfp4_moe_down_args c = *a;
   c.workspace = nullptr;
   MoeDownPlan pl;
@@ -2127,7 +2136,7 @@ nvfp4_status nvfp4_mxfp4_dequantize(const nvfp4_mxfp4_dequant_args *a, nvfp4_str
 }
 
 size_t nvfp4_mxfp4_gemm_workspace_bytes(const nvfp4_mxfp4_gemm_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->M, a->N, a->K})) return 0;
   nvfp4_mxfp4_gemm_args c = *a;
   c.workspace = nullptr;
   MxGemmPlan pl;
@@ -2147,7 +2156,7 @@ nvfp4_status nvfp4_mxfp4_gemm(const nvfp4_mxfp4_gemm_args *a, nvfp4_stream strea
 }
 
 size_t nvfp4_mxfp4_dgrad_workspace_bytes(const nvfp4_mxfp4_dgrad_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->M, a->N, a->K})) return 0;
   __nv_bfloat16 *wt;
   return plan_mx_dgrad(a, nullptr, &wt);
 }
@@ -2163,7 +2172,7 @@ nvfp4_status nvfp4_mxfp4_dgrad(const nvfp4_mxfp4_dgrad_args *a, nvfp4_stream str
 }
 
 size_t nvfp4_mxfp4_grouped_workspace_bytes(const nvfp4_mxfp4_grouped_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->num_tokens, a->top_k, a->num_experts, a->N, a->K})) return 0;
   nvfp4_mxfp4_grouped_args c = *a;
   c.workspace = nullptr;
   MxGroupedPlan pl;
@@ -2183,7 +2192,7 @@ nvfp4_status nvfp4_mxfp4_grouped_gemm(const nvfp4_mxfp4_grouped_args *a, nvfp4_s
 }
 
 size_t nvfp4_mxfp4_moe_down_workspace_bytes(const nvfp4_mxfp4_moe_down_args *a) {
-  if (!a) return 0;
+  if (!a || any_empty({a->num_tokens, a->top_k, a->num_experts, a->N, a->K})) return 0;
   nvfp4_mxfp4_moe_down_args c = *a;
   c.workspace = nullptr;
   MxMoeDownPlan pl;

@@ -591,3 +591,17 @@ def test_moe_down_rounds_once(T, E, k, N, K):
     before = 2e-5 * o.moe_combine(S, perm, np.abs(w), k) + (k + 1) * 2.0 ** -24 * term
     err = np.abs(y.float().cpu().numpy() - want)
     assert np.all(err <= before + 0.5 * o.bf16_ulp(np.abs(want) + before)), float(np.max(err / np.abs(want).max()))
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 64, 64), (8, 0, 64), (8, 64, 0), (300, 0, 64), (0, 0, 0), (8, -64, 64)])
+def test_empty_sizes_are_refused(M, N, K):
+    """As an error of the call, from every entry point that asks for its workspace first."""
+    x = torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+    codes, sf = (torch.zeros(1 << 15, device="cuda", dtype=torch.uint8) for _ in range(2))
+    with pytest.raises((nv.NVFP4Error, RuntimeError)):
+        nv.nvfp4_mxfp4_gemm(codes, sf, N, K, a_bf16=x)
+    with pytest.raises((nv.NVFP4Error, RuntimeError)):
+        nv.nvfp4_mxfp4_dgrad(torch.zeros(M, max(N, 0), device="cuda", dtype=torch.bfloat16), codes, sf, max(N, 0), K)
+    ids = torch.zeros(M, 1, device="cuda", dtype=torch.int32)
+    with pytest.raises((nv.NVFP4Error, RuntimeError)):
+        nv.nvfp4_mxfp4_grouped_gemm(ids, x, codes, sf, N, K, 1)

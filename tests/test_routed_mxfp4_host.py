@@ -3,6 +3,7 @@ mirror the header, bad arguments are refused before any device work, size
 queries; and the CPU reference against independent derivations."""
 import ctypes as C
 import math
+import multiprocessing
 
 import numpy as np
 import pytest
@@ -140,6 +141,52 @@ def test_size_queries(clib):
     assert clib.nvfp4_mxfp4_gemm_workspace_bytes(C.byref(a)) >= 8192 * 6144 // 2 + 8192 * 192
     d = B.MxDgradArgs(M=64, N=77, K=64, dy=P, lddy=80, w_codes=P, w_sf=P, dx=P, lddx=64)
     assert clib.nvfp4_mxfp4_dgrad_workspace_bytes(C.byref(d)) >= 64 * 80 * 2
+
+
+QUERIES = {
+    "nvfp4_quantize": (B.QuantArgs, ("batch", "rows", "cols"), ("src",)),
+    "nvfp4_gemm": (B.GemmArgs, ("M", "N", "K"), ("a_bf16",)),
+    "nvfp4_grouped": (B.GroupedArgs, ("num_tokens", "top_k", "num_experts", "N", "K"), ("expert_ids", "x_bf16")),
+    "nvfp4_lora": (B.LoraArgs, ("M", "N", "K"), ("x",)),
+    "nvfp4_dgrad": (B.DgradArgs, ("M", "N", "K"), ("dy",)),
+    "nvfp4_wgrad": (B.WgradArgs, ("M", "N", "K"), ("dy", "x")),
+    "nvfp4_moe_down": (B.MoeDownArgs, ("num_tokens", "top_k", "num_experts", "N", "K"), ("h",)),
+    "nvfp4_mxfp4_gemm": (B.MxGemmArgs, ("M", "N", "K"), ("a_bf16",)),
+    "nvfp4_mxfp4_dgrad": (B.MxDgradArgs, ("M", "N", "K"), ("dy",)),
+    "nvfp4_mxfp4_grouped": (B.MxGroupedArgs, ("num_tokens", "top_k", "num_experts", "N", "K"),
+                            ("expert_ids", "x_bf16")),
+    "nvfp4_mxfp4_moe_down": (B.MxMoeDownArgs, ("num_tokens", "top_k", "num_experts", "N", "K"), ("h",)),
+}
+
+
+def ask_every_query(out):
+    """Sends (query, field, value, answer) of every answer that is wrong."""
+    lib, bad = B.load(), []
+    for name, (cls, sizes, pointers) in QUERIES.items():
+        query = getattr(lib, f"{name}_workspace_bytes")
+        for given in (pointers, ()):
+            base = dict({f: 64 if f == "K" else 8 for f in sizes}, **{f: P for f in given})
+            if name in ("nvfp4_lora", "nvfp4_gemm"):
+                base["rank"] = 32
+            for field in sizes:
+                for value in (0, -1, -200, base[field]):
+                    n = query(C.byref(cls(**dict(base, **{field: value}))))
+                    if (n != 0 if value < 1 else n >= 1 << 32):
+                        bad.append((name, field, value, n))
+    out.send(bad)
+
+
+def test_workspace_queries_of_empty_and_negative_sizes(clib):
+    """A size query is made before the call refuses an empty operand: it answers 0.
+    (Asked in a process of its own, which a division by zero would end.)"""
+    assert {f"{n}_workspace_bytes" for n in QUERIES} == {n for n in B.EXPORTS if n.endswith("_workspace_bytes")}
+    ctx = multiprocessing.get_context("spawn")
+    here, there = ctx.Pipe(duplex=False)
+    child = ctx.Process(target=ask_every_query, args=(there,))
+    child.start()
+    child.join(120)
+    assert child.exitcode == 0
+    assert here.recv() == []
 
 
 # --------------------------------------------------------- reference pinned --
