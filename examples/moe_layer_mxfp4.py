@@ -1,11 +1,16 @@
-"""A routed expert layer on MXFP4 experts, forward and the router's gradient.
+"""A routed expert layer on MXFP4 experts, with the gradients of its router and of
+its shared linear.
 
     x [T, K] -> router logits -> nvfp4_route_topk -> nvfp4_mxfp4_grouped_gemm
       (gate | up projections of the chosen experts) -> SiLU(gate) * up
       -> nvfp4_mxfp4_moe_down_combine -> y [T, K]
 
-plus a shared MXFP4 linear beside the experts with its input gradient.  Run it
-on a GB300 after building the library:  python examples/moe_layer_mxfp4.py
+plus a shared MXFP4 linear beside the experts with its input gradient.  The
+routed products have no gradient: neither the one of x through the experts nor
+the one of the routing weights through the weighted sum, so the routed output
+is a constant to autograd and belongs into no loss that should train the router
+or what makes x.  Run it on a GB300 after building the library:
+python examples/moe_layer_mxfp4.py
 """
 import os
 import sys
@@ -71,18 +76,31 @@ class MoELayer:
     def route(self, x):
         return RouteTopk.apply(x.float() @ self.router.t(), self.top_k, self.form)
 
+    @torch.no_grad()
     def experts(self, x, ids, weights):
-        """The routed experts' output; no gradient flows into the frozen experts."""
+        """The routed experts' output, without a gradient (see above)."""
         d, perm, offsets = nv.nvfp4_mxfp4_grouped_gemm(ids, x, self.up["codes"], self.up["sf"], 2 * self.H, self.K,
                                                        self.E)
         gate, up = d[:, :self.H].float(), d[:, self.H:].float()
         h = (torch.nn.functional.silu(gate) * up).to(torch.bfloat16)
-        return nv.nvfp4_mxfp4_moe_down_combine(h, perm, offsets, weights.detach().contiguous(), self.down["codes"],
+        return nv.nvfp4_mxfp4_moe_down_combine(h, perm, offsets, weights.contiguous(), self.down["codes"],
                                                self.down["sf"], self.K, self.H, self.E)
 
+    def shared_linear(self, x):
+        return MXLinear.apply(x, self.shared["codes"], self.shared["sf"])
+
     def __call__(self, x):
+        """(y, routing weights).  The gradient of y is the shared linear's alone;
+        the weights carry the router's."""
         ids, weights = self.route(x)
-        return self.experts(x, ids, weights) + MXLinear.apply(x, self.shared["codes"], self.shared["sf"]), weights
+        return self.experts(x, ids, weights) + self.shared_linear(x), weights
+
+
+def training_loss(layer, x):
+    """A loss of the parts whose gradients are whole: the shared linear's output
+    and the routing weights."""
+    _, weights = layer.route(x)
+    return layer.shared_linear(x).float().square().mean() + weights.square().sum(1).mean()
 
 
 def main():
@@ -90,11 +108,10 @@ def main():
     layer = MoELayer(K=1024, H=512, E=32, top_k=4, groups=4, topk_groups=2)
     for tokens in (1, 8, 500):                   # one decoded token, a small batch, a prompt
         x = torch.randn(tokens, layer.K, device="cuda").to(torch.bfloat16).requires_grad_(True)
-        y, weights = layer(x)
-        # a loss through the shared linear and the routing weights
-        loss = y.float().square().mean() + (weights.square().sum(1)).mean()
+        with torch.no_grad():
+            y, _ = layer(x)
         layer.router.grad = None
-        loss.backward()
+        training_loss(layer, x).backward()
         print(f"{tokens:4d} tokens: y {tuple(y.shape)} rms {y.float().square().mean().sqrt():.4f}, "
               f"|dx| {x.grad.float().norm():.3e}, |d router| {layer.router.grad.norm():.3e}")
 

@@ -71,3 +71,30 @@ def test_layer_against_torch(tokens):
 def test_example_runs():
     import moe_layer_mxfp4
     moe_layer_mxfp4.main()
+
+
+@pytest.mark.parametrize("tokens", [1, 9, 150])
+def test_training_loss_has_its_whole_gradient(tokens):
+    """Everything that the example's loss depends on reaches x and the router: its
+    gradients against autograd in 64 bits on the decoded weights, the choice held
+    fixed.  The shared linear sees x rounded to MXFP4 with the rounding passed
+    straight through; left are bf16 roundings of its output and of its gradient."""
+    from moe_layer_mxfp4 import MoELayer, training_loss
+    K, E, k = 256, 16, 4
+    layer = MoELayer(K, 256, E, k, groups=4, topk_groups=2, seed=tokens + 1)
+    gen = torch.Generator("cuda").manual_seed(tokens)
+    x = torch.randn(tokens, K, generator=gen, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    y, weights = layer(x)
+    assert not layer.experts(x, *layer.route(x)).requires_grad
+    training_loss(layer, x).backward()
+    ids = layer.route(x.detach())[0].long()
+
+    shared = nv.nvfp4_mxfp4_dequantize(layer.shared["codes"], layer.shared["sf"]).double()
+    xr = x.detach().double().requires_grad_(True)
+    router = layer.router.detach().double().requires_grad_(True)
+    s = torch.sigmoid(xr @ router.t()).gather(1, ids)
+    w = layer.form["scale"] * s / s.sum(1, keepdim=True)
+    seen = xr + (decoded(x.detach()) - xr).detach()
+    ((seen @ shared.t()).square().mean() + w.square().sum(1).mean()).backward()
+    assert float((x.grad.double() - xr.grad).norm() / xr.grad.norm()) < 1e-2
+    assert float((layer.router.grad.double() - router.grad).norm() / router.grad.norm()) < 1e-2
