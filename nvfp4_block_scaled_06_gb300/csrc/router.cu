@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_any(const RouteTopk
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const int v = c * VEC + i, e = c * 32 * VEC + lane * VEC + i;
-        float key = x[v];
+        float key = finite_top(x[v]);
         const bool in = e < E && x[v] > -INFINITY;
         if (p.bias || p.rank_by_score) {
           float s = 0.0f;
@@ -378,14 +378,14 @@ __device__ __forceinline__ void plain_keys(const __nv_bfloat16 *p, int e0, uint3
 template <bool kScored>
 __device__ __forceinline__ uint32_t route_key(const float *bias, int e, float x, float &gval) {
   bool in = x > -INFINITY;
-  float key = x, s = x;
-  if (kScored) {
-    s = sigmoid(x);
-    if (bias) {
-      s += __ldg(bias + e);
-      key = s;
-      in = in && key > -INFINITY;
-    }
+  float key, s = x;
+  if (kScored) s = sigmoid(x);
+  if (kScored && bias) {
+    s += __ldg(bias + e);
+    key = s;
+    in = in && key > -INFINITY;
+  } else {
+    key = fminf(x, FLT_MAX);         // +inf counts as the largest finite value (a NaN is not in)
   }
   gval = in ? s : -INFINITY;         // (kScored without a bias: only where groups are ranked by scores)
   const uint32_t b = __float_as_uint(key + 0.0f);                       // -0 counts as +0
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
         t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
         t1 = fmaxf(t1, o1);
       }
-      const float score = p.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+      // (logits rank groups by their largest alone: a sum of two is of scores)
+      const float score = !kScored ? finite_top(t1) : p.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
       const int g = sub >> (__ffs(L) - __ffs(G));
       int better = 0;
       keep = 0u;

@@ -384,3 +384,35 @@ def test_route_backward_softmax_at_any_offset(E, k, dtype):
     bad = np.argwhere(~(np.abs(got - want) <= tol))
     assert bad.size == 0, (len(bad), sorted({offsets[r // 3] for r in bad[:, 0]}), got[tuple(bad[0])],
                            want[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("E,k", [(64, 8), (63, 5), (96, 12), (95, 16), (256, 20)])
+def test_route_infinity_ties_with_the_largest_finite_logit(E, k):
+    """+inf counts as the largest finite fp32: beside logits of that value it takes
+    its place by index, among experts and among groups."""
+    top, inf = float(np.finfo(np.float32).max), float("inf")
+    x = make_logits(9, E, torch.float32, 17)
+    x[0, [0, 5]] = torch.tensor([top, inf], device="cuda")
+    x[1, [0, 5]] = torch.tensor([inf, top], device="cuda")
+    x[2, ::3], x[2, 1::3] = top, inf
+    x[3, E - 1], x[3, 2] = inf, top
+    x[4], x[4, 7] = top, inf
+    x[5], x[5, 7] = inf, top
+    x[6, 1], x[6, 0], x[6, 3] = float("nan"), top, inf
+    x[7] = -inf
+    x[7, [2, 30]] = torch.tensor([top, inf], device="cuda")
+    forms = [dict()]
+    for G in (2, 3, 4, 8):
+        if E % G == 0:
+            for kg in (1, 2):
+                forms += [dict(num_groups=G, topk_groups=kg, group_top=t) for t in (1, 2) if k <= kg * (E // G)]
+    for score in ("sigmoid", "softmax"):
+        for form in forms:
+            want, want_w, margin = mo.route_topk(host(x), k, score=score, **form)
+            got = nv.nvfp4_route_topk(x, k, score=score, **form)
+            sure = margin > KEY_TOL
+            if form.get("group_top") == 2:       # equal sums of two scores go to the lowest group in both
+                sure |= margin == 0
+            ids = got["expert_ids"].cpu().numpy()
+            assert np.array_equal(ids[sure], want[sure]), (score, form, np.argwhere(ids != want)[:4])
+            assert np.allclose(got["weights"].cpu().numpy()[sure], want_w[sure], rtol=W_TOL, atol=1e-30)
