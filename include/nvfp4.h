@@ -228,7 +228,8 @@ size_t nvfp4_gemm_workspace_bytes(const nvfp4_gemm_args *args);
  *   order; perm_out[i] = the pair index of grouped row i (required with
  *   expert_ids, optional with perm_in); expert_offsets_out (optional) [E+1].
  * Requirements: N % 256 == 0, K % 32 == 0, E <= 1024, as nvfp4_gemm otherwise;
- *   x_codes, x_sf, offsets_in, perm_in 16-byte aligned.
+ *   x_codes, x_sf, offsets_in, perm_in 16-byte aligned, other pointers to their
+ *   element.
  * Workspace: nvfp4_grouped_workspace_bytes(&args).
  * ------------------------------------------------------------------------ */
 typedef struct {

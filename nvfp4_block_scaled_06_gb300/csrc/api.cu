@@ -571,6 +571,13 @@ nvfp4_status plan_grouped(const nvfp4_grouped_args *a, GroupedPlan *pl) {
   return NVFP4_OK;
 }
 
+// Pointers to 32-bit elements (those that are not null).
+bool all_words_aligned(std::initializer_list<const void *> ptrs) {
+  for (const void *q : ptrs)
+    if (q && !aligned(q, 4)) return false;
+  return true;
+}
+
 nvfp4_status validate_grouped(const nvfp4_grouped_args *a) {
   if (!a || !a->w_codes || !a->w_sf || !a->w_global_scale || !a->d) return NVFP4_ERR_INVALID_ARG;
   // routing: expert ids (grouped here, perm_out required) or offsets + perm given
@@ -599,6 +606,7 @@ nvfp4_status validate_grouped(const nvfp4_grouped_args *a) {
   const void *ptrs[] = {a->x_bf16, a->w_codes, a->w_sf, a->d, a->x_codes, a->x_sf, a->offsets_in, a->perm_in};
   for (const void *q : ptrs)
     if (q && !aligned(q, 16)) return NVFP4_ERR_ALIGNMENT;
+  if (!all_words_aligned({a->expert_ids, a->perm_out, a->expert_offsets_out})) return NVFP4_ERR_ALIGNMENT;
   return NVFP4_OK;
 }
 
@@ -898,6 +906,7 @@ nvfp4_status validate_moe_down(const nvfp4_moe_down_args *a) {
   }
   if (!aligned(a->h, 16) || !aligned(a->w_codes, 16) || !aligned(a->w_sf, 16) || !aligned(a->y, 16))
     return NVFP4_ERR_ALIGNMENT;
+  if (!all_words_aligned({a->perm, a->expert_offsets, a->route_weights})) return NVFP4_ERR_ALIGNMENT;
   return NVFP4_OK;
 }
 
@@ -1630,6 +1639,7 @@ nvfp4_status validate_mx_grouped(const nvfp4_mxfp4_grouped_args *a) {
   const void *ptrs[] = {a->x_bf16, a->w_codes, a->w_sf, a->d, a->x_codes, a->x_sf, a->offsets_in, a->perm_in};
   for (const void *q : ptrs)
     if (q && !aligned(q, 16)) return NVFP4_ERR_ALIGNMENT;
+  if (!all_words_aligned({a->expert_ids, a->perm_out, a->expert_offsets_out})) return NVFP4_ERR_ALIGNMENT;
   return NVFP4_OK;
 }
 
@@ -1764,6 +1774,7 @@ nvfp4_status validate_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a) {
     return s;
   if (!aligned(a->h, 16) || !aligned(a->w_codes, 16) || !aligned(a->w_sf, 16) || !aligned(a->y, 16))
     return NVFP4_ERR_ALIGNMENT;
+  if (!all_words_aligned({a->perm, a->expert_offsets, a->route_weights})) return NVFP4_ERR_ALIGNMENT;
   return NVFP4_OK;
 }
 

@@ -143,6 +143,25 @@ def test_size_queries(clib):
     assert clib.nvfp4_mxfp4_dgrad_workspace_bytes(C.byref(d)) >= 64 * 80 * 2
 
 
+@pytest.mark.parametrize("name,field", [
+    (n, f) for n in ("nvfp4_grouped_gemm", "nvfp4_mxfp4_grouped_gemm")
+    for f in ("expert_ids", "perm_out", "expert_offsets_out")] + [
+    (n, f) for n in ("nvfp4_moe_down_combine", "nvfp4_mxfp4_moe_down_combine")
+    for f in ("perm", "expert_offsets", "route_weights")])
+def test_misaligned_routing_pointers_are_refused(clib, name, field):
+    """Pointers to 32-bit elements off a word, which a kernel would fault on."""
+    cls, base = BASES.get(name) or {
+        "nvfp4_grouped_gemm": (B.GroupedArgs, dict(num_tokens=4, top_k=2, num_experts=8, N=256, K=64, expert_ids=P,
+                                                   x_bf16=P, w_codes=P, w_sf=P, w_global_scale=P, d=P, perm_out=P)),
+        "nvfp4_moe_down_combine": (B.MoeDownArgs, dict(num_tokens=4, top_k=2, num_experts=8, N=256, K=64, h=P, perm=P,
+                                                       expert_offsets=P, route_weights=P, w_codes=P, w_sf=P,
+                                                       w_global_scale=P, y=P)),
+    }[name]
+    for offset, refused in ((4, False), (2, True), (1, True)):
+        args = cls(**dict(base, **{field: P + offset}))
+        assert (getattr(clib, name)(C.byref(args), None) == B.ERR_ALIGNMENT) == refused, offset
+
+
 QUERIES = {
     "nvfp4_quantize": (B.QuantArgs, ("batch", "rows", "cols"), ("src",)),
     "nvfp4_gemm": (B.GemmArgs, ("M", "N", "K"), ("a_bf16",)),
