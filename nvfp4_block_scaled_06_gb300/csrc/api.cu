@@ -973,7 +973,7 @@ nvfp4_status run_moe_down(const nvfp4_moe_down_args *a, const MoeDownPlan &pl, i
   if (s != NVFP4_OK) return s;
   return cuda_status(launch_moe_combine(pl.d, false, a->perm, pl.inv, a->route_weights, a->num_tokens,
                                         (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
-                                        status, layout_makes_inverse(pl.prow_max), pl.goffsets + a->num_experts));
+                                        status, layout_makes_inverse(P, pl.prow_max), pl.goffsets + a->num_experts));
 }
 
 // --------------------------------------------------------------------- LoRA --
@@ -1823,7 +1823,7 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
   if (s != NVFP4_OK) return s;
   return cuda_status(launch_moe_combine(pl.d, true, a->perm, pl.inv, a->route_weights, a->num_tokens,
                                         (int)a->top_k, a->N, static_cast<__nv_bfloat16 *>(a->y), sms, st,
-                                        status, layout_makes_inverse(pl.prow_max), pl.goffsets + a->num_experts));
+                                        status, layout_makes_inverse(P, pl.prow_max), pl.goffsets + a->num_experts));
 }
 
 }  // namespace

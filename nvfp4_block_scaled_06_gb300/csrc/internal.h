@@ -239,8 +239,8 @@ cudaError_t launch_route(const RouteParams &p, cudaStream_t st);
 // m-tiles, row_map -> grouped row, or -> token through perm / top_k) of rows
 // that arrive already grouped with the given expert offsets (perm with top_k 0:
 // row_map holds grouped rows).  inv (optional): receives the inverse of perm
-// where layout_makes_inverse(padded_rows_max).
-bool layout_makes_inverse(int64_t padded_rows_max);
+// where layout_makes_inverse(pairs, padded_rows_max).
+bool layout_makes_inverse(int64_t pairs, int64_t padded_rows_max);
 cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pairs, int64_t padded_rows_max,
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,

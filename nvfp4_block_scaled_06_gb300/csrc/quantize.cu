@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(256) k_gather_packed(const uint8_t *__restrict
   const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int64_t vec_per_row = K / 32;               // 16-byte vectors of codes
-  const int64_t nblk = K / block, sfc_pad = (nblk + 3) & ~int64_t(3), ngrp = sfc_pad >> 2;
+  const int64_t nblk = block == 32 ? K / 32 : K / 16, sfc_pad = (nblk + 3) & ~int64_t(3), ngrp = sfc_pad >> 2;
   // only the rows of the routed layout (128 x its m-tile count) are read later
   if (num_mtiles) rows = min(rows, (int64_t)128 * (int64_t)*num_mtiles);
   const int64_t quads = ((rows + 127) >> 7) * 32;

@@ -91,6 +91,11 @@ __device__ __forceinline__ int32_t block_exclusive_scan_capped(int32_t v, int32_
   return min(in_warp, cap - before) + before;
 }
 
+// m-tiles of `rows` rows; tile_rows is 128 or 256.
+__device__ __forceinline__ int32_t tiles_of(int32_t rows, int tile_rows) {
+  return (rows + tile_rows - 1) >> (tile_rows == 256 ? 8 : 7);
+}
+
 // Offsets, 128-padded offsets, the m-tile table and the padding rows of row_map
 // from one expert count per thread of a 1024-thread block; returns the
 // thread's expert's first grouped row and first padded row.
@@ -99,7 +104,7 @@ __device__ __forceinline__ void write_layout(const RouteParams &p, int32_t count
   const int e = threadIdx.x;
   const bool act = e < p.num_experts;
   const int32_t padded = (count + 127) & ~127;
-  const int32_t mt = (count + p.tile_rows - 1) / p.tile_rows;
+  const int32_t mt = tiles_of(count, p.tile_rows);
   int32_t total, ptotal, mtotal;
   off = block_exclusive_scan(count, scratch, total);
   poff = block_exclusive_scan(padded, scratch, ptotal);
@@ -241,8 +246,9 @@ __global__ void __launch_bounds__(1024) k_route_scatter(const RouteParams p) {
   __syncthreads();
   const int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x;
   const bool in = threadIdx.x < p.chunk && i < p.pairs;
-  if (in && i >= p.offsets[E]) p.perm[i] = -1;   // dropped pairs leave grouped rows unused at the end
+  const int32_t total = p.offsets[E];    // (on its way while the pairs are placed)
   scatter_pairs(p, i, in, sh_base, sh_cnt, p.offsets, p.poffsets);
+  if (in && i >= total) p.perm[i] = -1;   // dropped pairs leave grouped rows unused at the end
 }
 
 // Up to 1024 pairs (decode): counts, layout and scatter by one block in one
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(1024) k_offsets_layout(const int32_t *__restri
   (void)NVFP4_NOTE(!act || (int64_t)count == diff, status);   // the caller's offsets were clamped
   if (threadIdx.x == 0) (void)NVFP4_NOTE(offsets[0] == 0, status);
   const int32_t padded = (count + 127) & ~127;
-  const int32_t mt = (count + tile_rows - 1) / tile_rows;
+  const int32_t mt = tiles_of(count, tile_rows);
   int32_t ctotal, ptotal, mtotal;
   const int32_t off = block_exclusive_scan(count, scratch, ctotal);
   const int32_t poff = block_exclusive_scan(padded, scratch, ptotal);
@@ -402,18 +408,22 @@ __global__ void k_rowmap_from_offsets(const int32_t *__restrict__ goffsets,
   }
 }
 
-// Up to this many padded rows the one-block kernel writes the row map and the
-// inverse as well (4352 rows and 256 pairs: 5.6 us in one launch, alone, instead
-// of 12 us in four).
-constexpr int64_t kOneBlockRows = 16384;
+// Up to this many pairs and padded rows the one-block kernel writes the row map
+// and the inverse as well: one launch instead of four.  NVFP4 down-projection
+// against four launches: 4000 pairs on 32 experts (8064 rows) 57.5 instead of
+// 59.7 us, on 8 experts 63.9 instead of 65.7; 6000 pairs on 8 experts 87.2 instead
+// of 85.7, 8000 on 32 (12064 rows) 75.9 instead of 74.4.
+constexpr int64_t kOneBlockPairs = 4096, kOneBlockRows = 8192;
 
-bool layout_makes_inverse(int64_t padded_rows_max) { return padded_rows_max <= kOneBlockRows; }
+bool layout_makes_inverse(int64_t pairs, int64_t padded_rows_max) {
+  return pairs <= kOneBlockPairs && padded_rows_max <= kOneBlockRows;
+}
 
 cudaError_t launch_layout_from_offsets(const int32_t *offsets, int E, int64_t pairs, int64_t padded_rows_max,
                                        int32_t *goffsets, int32_t *poffsets, GroupTile *gtiles,
                                        int32_t *gnum_mtiles, int32_t *row_map, const int32_t *perm, int top_k,
                                        int num_sms, cudaStream_t st, int *status, int32_t *inv, int tile_rows) {
-  const bool one = layout_makes_inverse(padded_rows_max);
+  const bool one = layout_makes_inverse(pairs, padded_rows_max);
   cudaError_t e = launch_pdl(k_offsets_layout, dim3(1), dim3(1024), 0, st, offsets, E, pairs, goffsets, poffsets,
                              gtiles, gnum_mtiles, padded_rows_max / 128, status, one ? row_map : (int32_t *)nullptr,
                              perm, top_k, one ? inv : (int32_t *)nullptr, tile_rows);
@@ -436,11 +446,11 @@ __global__ void k_invert_perm(const int32_t *__restrict__ perm, int64_t pairs, c
                               int32_t *inv, int *status) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
-  const int64_t n = min(pairs, (int64_t)*rows);
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+  const int32_t n = *rows;     // (read beside the entries, not before them)
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pairs;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int32_t q = perm[i];
-    if (NVFP4_NOTE(q >= 0 && q < pairs, status)) inv[q] = (int32_t)i;
+    if (i < n && NVFP4_NOTE(q >= 0 && q < pairs, status)) inv[q] = (int32_t)i;
   }
 }
 __global__ void k_fill_i32(int32_t *p, int64_t n, int32_t v) {
@@ -478,13 +488,13 @@ __device__ __forceinline__ void store_sums(__nv_bfloat16 *y, const float (&f)[4]
   *reinterpret_cast<uint2 *>(y) = make_uint2(round_pair(f[0], f[1]), round_pair(f[2], f[3]));
 }
 
-// A warp takes a token, or with few tokens one of `parts` interleaved column
-// ranges of it (32 tokens of 6144 columns, top 8: 4.5 us, with a warp each 22): its
+// A warp takes a token, or with few tokens (kSplit) one of `parts` interleaved
+// column ranges of it (32 tokens of 6144 columns, top 8: 4.5 us, with a warp each 22): its
 // slots' row indices and weights are read once, and for top_k <= 8 the 16-byte
 // loads of all slots are in flight together before the sums (which keep the
 // slot order).  TD: bf16, or float (the MXFP4 experts' outputs, which are not
 // rounded before the sum).
-template <typename TD>
+template <typename TD, bool kSplit>
 __global__ void __launch_bounds__(256) k_moe_combine(const TD *__restrict__ d, const int32_t *__restrict__ inv,
                                                      const float *__restrict__ w, int64_t tokens, int top_k,
                                                      int64_t N, __nv_bfloat16 *__restrict__ y, int parts,
@@ -496,9 +506,9 @@ __global__ void __launch_bounds__(256) k_moe_combine(const TD *__restrict__ d, c
   const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int64_t vecs = N / V;                       // 16-byte vectors of a row
-  for (int64_t item = warp; item < tokens * parts; item += nwarps) {
-    const int64_t t = item / parts;
-    const int64_t v0 = (item - t * parts) * 32 + lane, vstep = 32 * (int64_t)parts;
+  for (int64_t item = warp; item < (kSplit ? tokens * parts : tokens); item += nwarps) {
+    const int64_t t = kSplit ? item / parts : item;
+    const int64_t v0 = kSplit ? (item - t * parts) * 32 + lane : lane, vstep = kSplit ? 32 * (int64_t)parts : 32;
     if (top_k <= kMaxK) {
       const uint4 *rows[kMaxK];
       float wj[kMaxK];
@@ -561,12 +571,16 @@ cudaError_t launch_moe_combine(const void *d, bool d_fp32, const int32_t *perm, 
   const int64_t vecs = N / (d_fp32 ? 4 : 8);
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((vecs + 31) / 32, (int64_t)num_sms * 32 / tokens));
   const int64_t c2 = std::max<int64_t>(1, std::min<int64_t>((tokens * parts + 7) / 8, (int64_t)num_sms * 8));
-  if (d_fp32)
-    return launch_pdl(k_moe_combine<float>, dim3((unsigned)c2), dim3(256), 0, st, static_cast<const float *>(d),
-                      (const int32_t *)inv, w, tokens, top_k, N, y, (int)parts, status);
-  return launch_pdl(k_moe_combine<__nv_bfloat16>, dim3((unsigned)c2), dim3(256), 0, st,
-                    static_cast<const __nv_bfloat16 *>(d), (const int32_t *)inv, w, tokens, top_k, N, y, (int)parts,
-                    status);
+  const auto go = [&](auto kernel, auto rows_of_d) {
+    return launch_pdl(kernel, dim3((unsigned)c2), dim3(256), 0, st, rows_of_d, (const int32_t *)inv, w, tokens, top_k,
+                      N, y, (int)parts, status);
+  };
+  if (d_fp32) {
+    const float *df = static_cast<const float *>(d);
+    return parts > 1 ? go(k_moe_combine<float, true>, df) : go(k_moe_combine<float, false>, df);
+  }
+  const __nv_bfloat16 *db = static_cast<const __nv_bfloat16 *>(d);
+  return parts > 1 ? go(k_moe_combine<__nv_bfloat16, true>, db) : go(k_moe_combine<__nv_bfloat16, false>, db);
 }
 
 }  // namespace nvfp4
