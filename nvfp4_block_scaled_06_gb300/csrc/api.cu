@@ -545,7 +545,7 @@ nvfp4_status plan_grouped(const nvfp4_grouped_args *a, GroupedPlan *pl) {
   pl->nchunks = (int)ceil_div(P, 1024);
   pl->prow_max = pad_up(P + a->num_experts * 127, 128);
   if (a->expert_ids) {
-    pl->hist = c.take<int32_t>((size_t)pl->nchunks * a->num_experts * 4);
+    if (P > kRouteOnePairs) pl->hist = c.take<int32_t>((size_t)pl->nchunks * a->num_experts * 4);
     pl->counts = c.take<int32_t>((size_t)a->num_experts * 4);
     pl->offsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);
   } else {
@@ -1598,7 +1598,7 @@ void plan_mx_grouped(const nvfp4_mxfp4_grouped_args *a, MxGroupedPlan *pl) {
   pl->nchunks = (int)ceil_div(P, 1024);
   pl->prow_max = pad_up(P + a->num_experts * 127, 128);
   if (a->expert_ids) {
-    pl->hist = c.take<int32_t>((size_t)pl->nchunks * a->num_experts * 4);
+    if (P > kRouteOnePairs) pl->hist = c.take<int32_t>((size_t)pl->nchunks * a->num_experts * 4);
     pl->counts = c.take<int32_t>((size_t)a->num_experts * 4);
   }
   pl->offsets = c.take<int32_t>((size_t)(a->num_experts + 1) * 4);

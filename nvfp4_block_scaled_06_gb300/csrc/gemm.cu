@@ -60,13 +60,14 @@ struct TileInfo {
 // Dense: n-tile major (concurrent CTAs share B tiles; all of A stays in L2).
 // Grouped: m-tile major (the 8 n-tiles of one expert's m-tile run together, so
 // its gathered A tile is read from L2 and each expert's weights stream once).
-template <int BN>
+template <int BN, bool kGrouped>
 __device__ __forceinline__ TileInfo decode_tile(const GemmParams &p, int t, int nmt) {
   TileInfo ti;
-  const int nt = p.gtiles ? t % p.tiles_n : t / nmt;
-  const int j = p.gtiles ? t / p.tiles_n : t % nmt;
+  const bool grouped = kGrouped && p.gtiles;
+  const int nt = grouped ? t % p.tiles_n : t / nmt;
+  const int j = grouped ? t / p.tiles_n : t % nmt;
   ti.n0 = (int64_t)nt * BN;
-  if (p.gtiles) {
+  if (grouped) {
     GroupTile g = p.gtiles[j];
     if (!NVFP4_GUARD(g.expert >= 0 && (int64_t)(g.expert + 1) * p.N <= p.b_sf_row_chunks * 128 && g.a_row0 >= 0 &&
                          g.a_row0 + kBM <= p.M && g.valid_rows >= 0 && g.valid_rows <= kBM && g.out_row0 >= 0 &&
@@ -120,9 +121,8 @@ __device__ __forceinline__ void signal_abort(volatile int *abort_flag, int *stat
 // MX: the operands are MXFP4 (one E8M0 scale per 32 elements).  A 128x4 scale
 // atom then covers 128 elements of K, so a stage has two atoms per 128 rows
 // instead of four, and the MMA (kind::mxf4 scale_vec::2X) of K step j takes
-// half (j & 1) of atom j / 2; everything else is the same.  4096 tokens' top 8
-// of 256 experts (165 with rows, N 2048, K 6144): 295 us, 1.30 GB read, bound by
-// L2 -> SM copies at experts of many rows and by DRAM at those of few.
+// half (j & 1) of atom j / 2; everything else is the same.  Dense only: routed
+// MXFP4 products run on the pair and the operand-swapped kernel.
 template <int BN, bool MX>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   griddep_launch_dependents();
   griddep_wait();   // inputs of this kernel come from the previous one in the stream
 
-  const int nmt = p.gtiles ? *p.gnum_mtiles : p.tiles_m;
+  const int nmt = !MX && p.gtiles ? *p.gnum_mtiles : p.tiles_m;
   const int ksplit = p.ksplit > 1 ? p.ksplit : 1;
   const int num_tiles = nmt * p.tiles_n * ksplit;     // work units: (tile, K range)
   const int kt_per = (p.num_kt + ksplit - 1) / ksplit;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t armed = 0, armed_par = 0;   // bit s: stage s has an outstanding fill
       bool ok = true;
       for (int u = blockIdx.x; ok && u < num_tiles; u += gridDim.x) {
-        const TileInfo ti = decode_tile<BN>(p, u / ksplit, nmt);
+        const TileInfo ti = decode_tile<BN, !MX>(p, u / ksplit, nmt);
         const int kt0 = (u % ksplit) * kt_per;
         const int kt1 = min(p.num_kt, kt0 + kt_per);
         const int64_t chunk0 = ti.b_row0 >> 7;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         ok = false;
       }
       for (int u = blockIdx.x; ok && u < num_tiles; u += gridDim.x) {
-        const TileInfo ti = decode_tile<BN>(p, u / ksplit, nmt);
+        const TileInfo ti = decode_tile<BN, !MX>(p, u / ksplit, nmt);
         const int kt0 = (u % ksplit) * kt_per;
         const int kt1 = min(p.num_kt, kt0 + kt_per);
         WSTAT_T0();
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t acc_phase = 0;
     float sq = 0.0f;
     for (int u = blockIdx.x; u < num_tiles; u += gridDim.x) {
-      const TileInfo ti = decode_tile<BN>(p, u / ksplit, nmt);
+      const TileInfo ti = decode_tile<BN, !MX>(p, u / ksplit, nmt);
       const int ks = u % ksplit;
       WSTAT_T0();
       // warp-uniform outcome: tcgen05.ld below is a warp-collective instruction
@@ -964,6 +964,7 @@ cudaError_t launch_splitk_reduce(const GemmParams &p, int num_sms, cudaStream_t 
 template <int BN, bool MX>
 static cudaError_t launch_bn(const GemmParams &p, const GemmMaps &m, int num_sms, cudaStream_t st) {
   using C = GemmCfg<BN>;
+  if (MX && (p.gtiles || p.lora_steps)) return cudaErrorInvalidValue;
   if (cudaError_t e = ensure_dynamic_smem((const void *)k_gemm_fp4<BN, MX>, C::kSmemBytes); e != cudaSuccess) return e;
   int64_t tiles = (int64_t)p.tiles_n * (p.gtiles ? 0 : p.tiles_m) * std::max(1, p.ksplit);
   int grid = num_sms;

@@ -234,6 +234,8 @@ struct RouteParams {
   int32_t *offsets_out;       // optional copy of offsets for the caller
   int *status;                // device status word (index checks)
 };
+// Up to this many pairs are routed by one block in one launch, without hist.
+constexpr int64_t kRouteOnePairs = 1024;
 cudaError_t launch_route(const RouteParams &p, cudaStream_t st);
 // Padded grouped layout (goffsets = the clamped offsets rebuilt, poffsets,
 // m-tiles, row_map -> grouped row, or -> token through perm / top_k) of rows

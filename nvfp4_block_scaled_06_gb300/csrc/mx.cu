@@ -247,7 +247,6 @@ __global__ void __launch_bounds__(128) k_mx_dequant_t8(const uint8_t *__restrict
     if (g >= groups || blk >= nblk) continue;
     uint2 c[8];
     uint32_t s[8];
-#pragma unroll
     const uint8_t *cr = codes + g * 8 * (cols / 2) + half * 8;
     const uint8_t *sr = mx_scale_at(sf, swz, g * 8, blk, nblk);
     const int64_t sstep = swz ? 16 : nblk;                 // (eight rows from a multiple of 8: one run of an atom)

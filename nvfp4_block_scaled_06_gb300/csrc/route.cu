@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(1024) k_route_scatter(const RouteParams p) {
   if (in && i >= total) p.perm[i] = -1;   // dropped pairs leave grouped rows unused at the end
 }
 
-// Up to 1024 pairs (decode): counts, layout and scatter by one block in one
+// Up to kRouteOnePairs pairs (decode): counts, layout and scatter by one block in one
 // launch (the general path's three take 3 + 8 + 5.5 us, each alone).
 __global__ void __launch_bounds__(1024) k_route_one(const RouteParams p) {
   griddep_launch_dependents();
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(1024) k_route_one(const RouteParams p) {
 }
 
 cudaError_t launch_route(const RouteParams &p, cudaStream_t st) {
-  if (p.pairs <= 1024) {
+  if (p.pairs <= kRouteOnePairs) {
     const size_t one = (size_t)p.num_experts * (3 * sizeof(int32_t) + 32 * sizeof(uint16_t));
     if (cudaError_t e = ensure_dynamic_smem((const void *)k_route_one, one); e != cudaSuccess) return e;
     return launch_pdl(k_route_one, dim3(1), dim3(1024), one, st, p);

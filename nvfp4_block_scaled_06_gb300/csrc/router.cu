@@ -16,8 +16,9 @@
 // its experts in batches of eight, sorts each batch with a fixed network and
 // merges it into its running 8 or 16 largest, then the lanes' lists are merged
 // pairwise by shuffles.  k_route_any, a warp per token: every other form
-// (top_k > 16, softmax scores with a bias, group counts that are no power of
-// two).  In both a key is an order-preserving integer whose low bits are
+// (top_k > 16; softmax scores with a bias or groups ranked by two scores; group
+// counts that are no power of two; 9 to 16 choices by score for few tokens).  In
+// both a key is an order-preserving integer whose low bits are
 // replaced by the inverted expert index, so that one integer maximum carries
 // the expert along and ties fall to the lowest index.  Where two neighbouring
 // results (the largest rejected key included) agree in every bit that is left
@@ -690,10 +691,11 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
 //             dx_j = w_j (d_j - sum_i d_i w_i) on the chosen experts, 0 elsewhere
 //   softmax:  dx_e = p_e (d_e - sum_j d_j p_j) for every expert
 // L lanes per token (8, or a warp where top_k > 8 or E > 256).  The row is
-// written whole in 16-byte vectors -- zeros, or p_e times minus the dot product
-// (kDense) -- and the chosen experts' elements over it.  HBM-bound: that write
-// and, with kDense, the read of the logits.  This kernel serves the sparse
-// forms, and the dense one for rows that are not whole 16-byte vectors.
+// written whole -- zeros, in 16-byte vectors where it allows them (kVec), or p_e
+// times minus the dot product (kDense) -- and the chosen experts' elements over
+// it.  HBM-bound: that write and, with kDense, the read of the logits.  This
+// kernel serves the sparse forms, and the dense one for rows that are not whole
+// 16-byte vectors, an element at a time.
 // The exponentials of the dense form are exp2 approximations: with |x - max| <
 // 64 their relative error stays below 2^-17 (most of it the rounding of the
 // exponent's argument, which is why it is small where the term is large).
@@ -728,21 +730,15 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
     float g = 0.0f;                    // of the chosen expert
     if constexpr (kDense) {
       // running maximum and sum of the lane's part of the row, then of the token
+      static_assert(!kVec, "rows of whole vectors take k_route_softmax_backward");
       float m = -INFINITY, s = 0.0f;
-      for (int e = sub * VEC; e < E; e += L * VEC) {
-        float x[VEC], top = m;
-        load_vec<VEC>(row + e, x);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          x[i] = finite_top(x[i]);
-          top = fmaxf(top, x[i]);
-        }
+      for (int e = sub; e < E; e += L) {
+        const float x = finite_top(load1(row + e));
+        const float top = fmaxf(m, x);                        // (fmaxf passes over NaN)
         if (top > -INFINITY) {
           s *= __expf(m - top);
           m = top;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (x[i] > -INFINITY) s += __expf(x[i] - m);
+          if (x > -INFINITY) s += __expf(x - m);
         }
       }
       const float top = max_tok(m);
@@ -754,24 +750,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
       g = ps * (d - dot);
       if (live) {
         const float c = -dot * inv;
-        for (int e = sub * VEC; e < E; e += L * VEC) {
-          float x[VEC];
-          load_vec<VEC>(row + e, x);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) x[i] = x[i] > -INFINITY ? __expf(finite_top(x[i]) - mt) * c : 0.0f;
-          if constexpr (VEC == 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-              o[i] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            *reinterpret_cast<uint4 *>(out + e) = make_uint4(o[0], o[1], o[2], o[3]);
-          } else if constexpr (VEC == 4) {
-            *reinterpret_cast<float4 *>(out + e) = make_float4(x[0], x[1], x[2], x[3]);
-          } else {
-            store1(out + e, x[0]);
-          }
+        for (int e = sub; e < E; e += L) {
+          const float x = load1(row + e);
+          store1(out + e, x > -INFINITY ? __expf(finite_top(x) - mt) * c : 0.0f);
         }
       }
     } else {
@@ -927,10 +908,6 @@ cudaError_t launch_topk(const RouteTopkParams &p, int num_sms, cudaStream_t st) 
   return launch_pdl(k_route_any<T, VEC, NCH>, dim3((unsigned)ctas), dim3(kRouterWarps * 32), smem, st, p);
 }
 
-// Lanes per token: enough warps for the device (16 per SM; 4 with lists of 16,
-// whose merges cost more: 4096 tokens, 256 experts, top 10 5.4 us, with 16 9.2) with as
-// few lanes as that takes -- every halving of L saves a merge and its shuffles
-// per token -- but at least eight experts per lane; with groups, whole lanes per group.
 template <typename T, int L, int R, bool kScored>
 cudaError_t launch_few(const RouteTopkParams &p, bool vec, int num_sms, cudaStream_t st) {
   const int64_t per_cta = (int64_t)kRouterWarps * (32 / L);
@@ -939,6 +916,10 @@ cudaError_t launch_few(const RouteTopkParams &p, bool vec, int num_sms, cudaStre
   return vec ? launch_pdl(k_route_few<T, L, R, kScored, true>, grid, block, 0, st, p)
              : launch_pdl(k_route_few<T, L, R, kScored, false>, grid, block, 0, st, p);
 }
+// Lanes per token: enough warps for the device (16 per SM; 4 with lists of 16,
+// whose merges cost more: 4096 tokens, 256 experts, top 10 5.4 us, with 16 9.2) with as
+// few lanes as that takes -- every halving of L saves a merge and its shuffles
+// per token -- but at least eight experts per lane; with groups, whole lanes per group.
 template <typename T, int R, bool kScored>
 cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   const int E = p.num_experts, G = p.num_groups;
