@@ -1568,10 +1568,14 @@ nvfp4_status run_mx_dgrad(const nvfp4_mxfp4_dgrad_args *a, int sms, cudaStream_t
                        static_cast<int *>(a->workspace), a->prof_begin, a->prof_end, sms, st);
 }
 
-// Decode: few rows per expert on average, and no more than 512 on any (an expert
-// gets a token once): the operand-swapped kernel, whose stages hold weights
-// instead of padding rows.
-bool mx_few_rows(int64_t T, int64_t k, int64_t E) { return T <= 512 && T * k <= 16 * E; }
+// Decode: the operand-swapped kernel, whose stages hold weights instead of
+// padding rows, for few routed rows in all and at most eight per expert.  Its
+// call's time over the pair kernel's, 8 to 256 experts, N x K from 2048 x 6144 to
+// 2048 x 512, skewed routing: 0.86 to 1.08 up to 128 rows, and 0.92 to 1.00 with 129
+// to 256 rows on 32 experts; on 64 experts 0.94 to 1.16 there.  Beyond: 32 experts
+// of 12 rows 0.95 to 1.09, 128 of 6 0.99 to 1.31, 8 of 24 0.95 to 1.38, 256 of 16 1.10
+// to 1.36.
+bool mx_few_rows(int64_t T, int64_t k, int64_t E) { return T * k <= 8 * E && T * k <= (E <= 32 ? 256 : 128); }
 // The m-tiles' rows: the pair kernel takes every other call.  Against 128 x 256
 // tiles over 8 to 128 experts of 24 to 1024 rows, in three shapes: 0.91 of the
 // call's time on average, 0.70 at 512 rows on 128 experts (2048 x 512), 1.10 where

@@ -605,3 +605,50 @@ def test_empty_sizes_are_refused(M, N, K):
     ids = torch.zeros(M, 1, device="cuda", dtype=torch.int32)
     with pytest.raises((nv.NVFP4Error, RuntimeError)):
         nv.nvfp4_mxfp4_grouped_gemm(ids, x, codes, sf, N, K, 1)
+
+
+@pytest.mark.parametrize("T,E,k,N,K,heavy", [(64, 64, 2, 2048, 736, 0), (128, 64, 1, 512, 352, 128),
+                                             (120, 40, 1, 256, 1056, 70), (16, 32, 8, 1024, 2048, 16),
+                                             (42, 16, 3, 768, 96, 42), (1, 256, 8, 256, 4128, 0), (65, 16, 1, 256, 64, 33),
+                                             (250, 32, 1, 512, 480, 190)])
+def test_grouped_decode(T, E, k, N, K, heavy):
+    """Few routed rows (the operand-swapped kernel), with more units than CTAs, K
+    that wraps its stages, and one expert that takes `heavy` of the tokens: its rows
+    in one to four groups of 32 and in two m-tiles; some choices dropped in the
+    second run."""
+    rng, wl, wc_d, wsf_d, ids = expert_case(T, E, k, N, K, seed=61)
+    for t in range(heavy):
+        if 3 not in ids[t]:
+            ids[t, t % k] = 3
+    x, h = bits(rng, T, K), bits(rng, T * k, K)
+    hv = mo.dequantize(*mo.quantize(h))
+    w = rng.uniform(-1, 1, (T, k)).astype(np.float32)
+    for drop in (0, 1):
+        if drop:
+            ids[::3, k - 1] = -1
+        d, S, perm, offsets = grouped_reference(mo.dequantize(*mo.quantize(x)), ids, wl)
+        n = len(perm)
+        ids_d = torch.from_numpy(np.ascontiguousarray(ids)).cuda()
+        for out_dtype in (torch.float32, torch.bfloat16):
+            call, (got, p, offs) = nv.prepare_mxfp4_grouped(ids_d, dev_bf16(x), wc_d, wsf_d, N, K, E,
+                                                            out_dtype=out_dtype)
+            got.fill_(-7.0)
+            for _ in range(3):
+                call()
+            assert nv.read_device_status(call.workspace) == 0
+            assert np.array_equal(p[:n].cpu().numpy(), perm) and np.array_equal(offs.cpu().numpy(), offsets)
+            if n:
+                assert_gemm_close(got[:n], d, S)
+            assert torch.all(got[n:] == -7.0)
+        want, term, prod = np.zeros((T, N)), np.zeros((T, N)), np.zeros((T, N))
+        for e in range(E):
+            r = slice(offsets[e], offsets[e + 1])
+            de, Se = product(hv[r], wl[e])
+            for i, pair in enumerate(perm[r]):
+                want[pair // k] += w[pair // k, pair % k] * de[i]
+                term[pair // k] += abs(w[pair // k, pair % k]) * np.abs(de[i])
+                prod[pair // k] += abs(w[pair // k, pair % k]) * Se[i]
+        y = nv.nvfp4_mxfp4_moe_down_combine(dev_bf16(h), p, offs, torch.from_numpy(w).cuda(), wc_d, wsf_d, N, K, E)
+        before = 2e-5 * prod + (k + 1) * 2.0 ** -24 * term
+        tol = before + 0.5 * o.bf16_ulp(np.abs(want) + before + 1e-30)
+        assert np.all(np.abs(y.float().cpu().numpy() - want) <= tol)
