@@ -17,7 +17,8 @@
 // merges it into its running 8 or 16 largest, then the lanes' lists are merged
 // pairwise by shuffles.  k_route_any, a warp per token: every other form
 // (top_k > 16; softmax scores with a bias or groups ranked by two scores; group
-// counts that are no power of two; 9 to 16 choices by score for few tokens).  In
+// counts that are no power of two; 9 to 16 choices by score for few tokens of up
+// to 512 experts).  In
 // both a key is an order-preserving integer whose low bits are
 // replaced by the inverted expert index, so that one integer maximum carries
 // the expert along and ties fall to the lowest index.  Where two neighbouring
@@ -916,15 +917,19 @@ cudaError_t launch_few(const RouteTopkParams &p, bool vec, int num_sms, cudaStre
   return vec ? launch_pdl(k_route_few<T, L, R, kScored, true>, grid, block, 0, st, p)
              : launch_pdl(k_route_few<T, L, R, kScored, false>, grid, block, 0, st, p);
 }
-// Lanes per token: enough warps for the device (16 per SM; 4 with lists of 16,
-// whose merges cost more: 4096 tokens, 256 experts, top 10 5.4 us, with 16 9.2) with as
-// few lanes as that takes -- every halving of L saves a merge and its shuffles
-// per token -- but at least eight experts per lane; with groups, whole lanes per group.
+// Lanes per token: enough warps for the device with as few lanes as that takes --
+// every halving of L saves a merge and its shuffles per token -- but at least eight
+// experts per lane; with groups, whole lanes per group.  Enough is 8 to 32 warps per
+// SM, in step with the experts, whose batches a lane takes one after the other: top
+// 8 of 160 experts, 8192 tokens, bf16 4.6 us with 8 warps and 6.2 with 16; of 1000,
+// 32768 tokens 29.1 with 32, 40.8 with 16; of 256, 16384 tokens fp32 with a bias 17.6 with 16,
+// 20.7 with 8, 18.1 with 32.  4 with lists of 16, whose merges cost more: 2048 tokens,
+// 256 experts, top 10 4.0 us, with 2 4.8, with 8 5.8.
 template <typename T, int R, bool kScored>
 cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
   const int E = p.num_experts, G = p.num_groups;
   int L = 32;
-  const int64_t enough = (int64_t)num_sms * (R == 8 ? 16 : 4) * 32;
+  const int64_t enough = (int64_t)num_sms * (R == 8 ? std::min(std::max(E / 16, 8), 32) : 4) * 32;
   while (L > R / 2 && (L > G || G == 1) && (p.tokens * (L / 2) >= enough || E < 8 * L)) L /= 2;
   L = std::max(L, G);
   const bool vec = E % 8 == 0 && (G == 1 || E % (8 * L) == 0) && p.ld * sizeof(T) % 16 == 0 &&
@@ -939,12 +944,13 @@ cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
 }
 // The forms that k_route_few takes: up to 16 choices; keys that need no row
 // statistics; a power of two of groups, up to 32 (whole lanes for each).  Lists
-// of 16 scored keys only for many tokens: few of 256 experts wait longer for
-// the few lanes' scores than for a warp's (4096 tokens 11.9 against 8.8 us, 65521
-// tokens 59.8 against 85.3).
+// of 16 scored keys only for many tokens or more than 512 experts: few tokens wait
+// longer for the few lanes' scores than for a warp's (fp32, bias, top 10, against the
+// other kernel: 4096 tokens of 256 experts 12.1 and 9.5 us, of 512 18.2 and 18.2, of 1000
+// 29.3 and 46.2; 16384 tokens of 256 20.9 and 24.7).
 bool takes_few(const RouteTopkParams &p, bool scored, int num_sms) {
   if (p.top_k > 16 || (p.softmax && (p.bias || p.rank_by_score))) return false;
-  if (p.top_k > 8 && scored && p.tokens < (int64_t)num_sms * 64) return false;
+  if (p.top_k > 8 && scored && p.num_experts <= 512 && p.tokens < (int64_t)num_sms * 64) return false;
   const int G = p.num_groups;
   return G <= 32 && (G & (G - 1)) == 0;
 }
