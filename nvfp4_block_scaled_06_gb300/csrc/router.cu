@@ -17,11 +17,11 @@
 // merges it into its running 8 or 16 largest, then the lanes' lists are merged
 // pairwise by shuffles.  k_route_any, a warp per token: every other form
 // (top_k > 16; softmax scores with a bias or groups ranked by two scores; group
-// counts that are no power of two; 9 to 16 choices by score for few tokens of up
-// to 512 experts).  In
-// both a key is an order-preserving integer whose low bits are
-// replaced by the inverted expert index, so that one integer maximum carries
-// the expert along and ties fall to the lowest index.  Where two neighbouring
+// counts that are no power of two; and for few tokens 9 to 16 choices by score of
+// up to 512 experts, and scored ones of up to 128 in ragged groups).  In both a key
+// is an order-preserving integer whose low bits are replaced by the inverted expert
+// index, so that one integer maximum carries the expert along and ties fall to the
+// lowest index.  Where two neighbouring
 // results (the largest rejected key included) agree in every bit that is left
 // of the key, the token's selection runs again on the whole keys (bf16 logits
 // without a bias lose no bits), as it does where a chosen key turns out to be an
@@ -947,11 +947,16 @@ cudaError_t pick_few(const RouteTopkParams &p, int num_sms, cudaStream_t st) {
 // of 16 scored keys only for many tokens or more than 512 experts: few tokens wait
 // longer for the few lanes' scores than for a warp's (fp32, bias, top 10, against the
 // other kernel: 4096 tokens of 256 experts 12.1 and 9.5 us, of 512 18.2 and 18.2, of 1000
-// 29.3 and 46.2; 16384 tokens of 256 20.9 and 24.7).
+// 29.3 and 46.2; 16384 tokens of 256 20.9 and 24.7).  Few tokens of up to 128 experts
+// by score in groups that are no whole batches of eight neither: 64 tokens of 44 in 4
+// groups 7.3 against 4.4 us, 512 of 100 in 4 6.5 and 5.0; 8192 of 100 8.9 and 10.8, 64 of
+// 264 in 8 6.8 and 8.5.
 bool takes_few(const RouteTopkParams &p, bool scored, int num_sms) {
   if (p.top_k > 16 || (p.softmax && (p.bias || p.rank_by_score))) return false;
   if (p.top_k > 8 && scored && p.num_experts <= 512 && p.tokens < (int64_t)num_sms * 64) return false;
   const int G = p.num_groups;
+  if (scored && G > 1 && p.num_experts <= 128 && p.group_size % 8 != 0 && p.tokens < (int64_t)num_sms * 16)
+    return false;
   return G <= 32 && (G & (G - 1)) == 0;
 }
 
