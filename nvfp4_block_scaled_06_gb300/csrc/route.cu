@@ -489,7 +489,7 @@ __device__ __forceinline__ void store_sums(__nv_bfloat16 *y, const float (&f)[4]
 }
 
 // A warp takes a token, or with few tokens (kSplit) one of `parts` interleaved
-// column ranges of it (32 tokens of 6144 columns, top 8: 4.5 us, with a warp each 22): its
+// column ranges of it (32 tokens of 6144 bf16 columns, top 8: 4.5 us, with a warp each 22): its
 // slots' row indices and weights are read once, and for top_k <= 8 the 16-byte
 // loads of all slots are in flight together before the sums (which keep the
 // slot order).  TD: bf16, or float (the MXFP4 experts' outputs, which are not
