@@ -453,7 +453,9 @@ size_t nvfp4_moe_down_workspace_bytes(const nvfp4_moe_down_args *args);
  * them): it is never chosen, and its softmax score is 0.  A logit of +inf
  * counts as the largest finite fp32.  Where fewer than top_k experts can be
  * chosen the remaining ids are -1 and their weights 0 (nvfp4_grouped_gemm
- * drops such pairs); chosen weights are 0 if their scores sum to 0.
+ * drops such pairs).  Renormalized weights are the quotients of the scores
+ * however small these are (SOFTMAX: the softmax over the chosen logits); they
+ * are 0 where SIGMOID scores are all 0 in fp32 (logits below -103.9).
  *   logits [num_tokens][ld] bf16 or fp32 (logits_dtype), expert_ids and
  *   route_weights [num_tokens][top_k].
  * Requirements: num_experts <= 1024, top_k <= 32, num_groups <= 32 and a

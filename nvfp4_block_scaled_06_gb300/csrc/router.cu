@@ -65,6 +65,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// Renormalised sigmoid scores of chosen logits that are all below -20 (m: their
+// largest): there s = exp(x) to within 2^-28, whose quotients exp(x - m) keep while
+// s itself runs out of bits (from -87 on) and exp(-x) overflows (from -88.7 on).
+// Where the largest score is 0 in fp32 all are 0.
+constexpr float kTinyScores = -20.0f, kZeroScores = -103.972f;   // (2^-150 = exp(-103.972))
+__device__ __forceinline__ float tiny_score(float x, float m) { return m >= kZeroScores ? expf(x - m) : 0.0f; }
 
 __device__ __forceinline__ float load1(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) {
@@ -278,7 +284,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_any(const RouteTopk
         w = expf(finite_top(xs) - row_max) * inv_sum;
       }
     } else {
-      w = id >= 0 ? sigmoid(xs) : 0.0f;
+      const float m = p.renormalize ? warp_max(xs) : 0.0f;
+      if (id >= 0) w = m < kTinyScores ? tiny_score(xs, m) : sigmoid(xs);
       if (p.renormalize) {
         const float s = warp_sum(w);
         w = s > 0.0f ? w / s : 0.0f;
@@ -664,9 +671,16 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_few(const RouteTopk
         if (!p.need_row_sum) total += w[q];
       }
     } else {
+      float xs[kSlots], m = -INFINITY;
 #pragma unroll
       for (int q = 0; q < kSlots; ++q) {
-        w[q] = id[q] >= 0 ? sigmoid(load1(row + id[q])) : 0.0f;
+        xs[q] = id[q] >= 0 ? load1(row + id[q]) : -INFINITY;
+        m = fmaxf(m, xs[q]);
+      }
+      m = p.renormalize ? max_tok(m) : 0.0f;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        w[q] = id[q] < 0 ? 0.0f : m < kTinyScores ? tiny_score(xs[q], m) : sigmoid(xs[q]);
         total += w[q];
       }
     }
@@ -778,10 +792,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32) k_route_topk_backward(const
         const float slope = a / ((1.0f + a) * (1.0f + a));
         if (p.renormalize) {
           // slope / S <= 1 whatever the size of S: 1 / S alone may overflow
-          const float s = id >= 0 ? sigmoid(xs) : 0.0f;
+          const float m = max_tok(xs);
+          const bool tiny = m < kTinyScores;       // slope = s there
+          const float s = id < 0 ? 0.0f : tiny ? tiny_score(xs, m) : sigmoid(xs);
           const float S = sum_tok(s);
           const float c = sum_tok(S > 0.0f ? d * (s / S) : 0.0f);
-          g = id >= 0 && S > 0.0f ? (d - c) * (slope / S) : 0.0f;
+          g = id >= 0 && S > 0.0f ? (d - c) * ((tiny ? s : slope) / S) : 0.0f;
         } else {
           g = id >= 0 ? d * slope : 0.0f;
         }

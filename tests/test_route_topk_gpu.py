@@ -416,3 +416,41 @@ def test_route_infinity_ties_with_the_largest_finite_logit(E, k):
             ids = got["expert_ids"].cpu().numpy()
             assert np.array_equal(ids[sure], want[sure]), (score, form, np.argwhere(ids != want)[:4])
             assert np.allclose(got["weights"].cpu().numpy()[sure], want_w[sure], rtol=W_TOL, atol=1e-30)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,k,bias", [(64, 8, False), (63, 5, True), (256, 12, False), (1000, 20, True), (8, 8, False),
+                                      (12, 12, False), (20, 20, True)])
+def test_route_sigmoid_far_below_zero(E, k, bias, dtype):
+    """Renormalised sigmoid weights and their gradient where the scores reach fp32's
+    smallest values: their ratios are those of the definition down to the largest
+    score's own underflow (logits of -103.9), below which all weights are 0."""
+    rng = np.random.default_rng(E)
+    # (largest logit, spread below it); the spread's rounding in x - max stays below 2^-19
+    rows = [(-70.0, 6.0), (-79.5, 6.0), (-81.0, 6.0), (-86.0, 6.0), (-88.5, 6.0), (-19.0, 60.0), (-21.0, 60.0),
+            (-35.0, 60.0), (-75.0, 20.0), (-79.9, 15.0), (-95.0, 6.0), (-103.0, 6.0)]
+    x = -200.0 - rng.random((len(rows) + 2, E))
+    for t, (v, spread) in enumerate(rows):
+        x[t] = v - rng.random(E) * spread
+        x[t, rng.integers(E)] = v
+    x[-2], x[-1] = -110.0 - rng.random(E), -3e38
+    xt = torch.from_numpy(x).to(dtype).cuda()
+    b = np.zeros(E) if bias else None
+    got = nv.nvfp4_route_topk(xt, k, bias=None if b is None else torch.zeros(E, device="cuda"), scale=2.5)
+    ids, w = got["expert_ids"].cpu().numpy(), host(got["weights"])
+    xh = host(xt)
+    # (with a bias the choice is by the fp32 scores, equal ones by index)
+    zero = np.take_along_axis(xh, ids, 1).max(1) < -103.9
+    assert zero[-2:].all() and not zero[:5].any()
+    s = np.take_along_axis(mo.scores(xh, "sigmoid"), ids, 1)[~zero]
+    want = 2.5 * s / s.sum(1, keepdims=True)
+    assert np.all(np.abs(w[~zero] - want) <= W_TOL * want)
+    assert np.all(w[zero] == 0)
+    g = rng.standard_normal(w.shape).astype(np.float32)
+    d = host(nv.nvfp4_route_topk_backward(xt, got["expert_ids"], torch.from_numpy(g).cuda(), scale=2.5))
+    gh = g.astype(np.float64)
+    want = mo.route_topk_backward(xh, ids, gh, "sigmoid", True, 2.5)[~zero]
+    tol = 2.0 ** -17 * backward_scale(xh, ids, gh, "sigmoid", True, 2.5)[~zero] + 1e-30
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(d[~zero] - want) <= tol) and np.all(d[zero] == 0)
