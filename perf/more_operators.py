@@ -246,8 +246,8 @@ def _plan(s):
     else:
         s["call"], (out, lse) = nv.prepare_kv_attention(
             s["q_rows"], cache, s["gk"], s["gv"], s["table"], s["kv_lens"],
-            q_offsets=None if s["q"] == 1 else s["offsets"], scale=s["scale"], causal=s["causal"],
-            window=s["window"], want_lse=True)
+            q_offsets=None if s["q"] == 1 else s["offsets"], max_q_len=max(s["qlens"]), scale=s["scale"],
+            causal=s["causal"], window=s["window"], want_lse=True)
         s["y"] = {"out": out, "lse": lse}
 
 
