@@ -658,6 +658,127 @@ nvfp4_status nvfp4_mxfp4_moe_down_combine(const nvfp4_mxfp4_moe_down_args *args,
 size_t nvfp4_mxfp4_moe_down_workspace_bytes(const nvfp4_mxfp4_moe_down_args *args);
 
 /* ------------------------------------------------------------------------ *
+ * Key-value cache in NVFP4 -- written token by token, read back, attended to.
+ *
+ * A cache is num_pages pages of page_size tokens.  Per page, key-value head and
+ * token it holds a row of head_dim channels for the key and one for the value:
+ *   codes [num_pages][num_kv_heads][page_size][head_dim/2]
+ *   sf    [num_pages][num_kv_heads][page_size][head_dim/16]   (E4M3 bytes)
+ * contiguous within a page, pages codes_page_stride / sf_page_stride bytes
+ * apart (a cache may be one layer's part of larger pages).  A row is packed as
+ * nvfp4_quantize packs a matrix row (row packing, 1x16 blocks) under a static
+ * scale: k_global_scale and v_global_scale, device float[num_kv_heads], finite
+ * and > 0; value = E2M1(code) * E4M3(byte) * g.  A slot is
+ * page * page_size + offset.
+ * Requirements (all calls): head_dim 64 or 128; page_size a power of two, 16 to
+ *   1024; num_pages < 2^31, num_kv_heads <= 1024; code and scale pointers and
+ *   page strides multiples of 16 bytes, strides at least a page's bytes.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint8_t *k_codes, *k_sf, *v_codes, *v_sf;
+  int64_t num_pages, num_kv_heads, page_size, head_dim;
+  int64_t codes_page_stride, sf_page_stride;   /* bytes */
+} nvfp4_kv_pages;
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_kv_write -- bf16 keys and values of num_tokens tokens into the cache.
+ * nvfp4_kv_read  -- their rows back: E2M1 * (E4M3 * g), rounded to out_dtype.
+ *
+ *   k, v: [num_tokens][num_kv_heads][head_dim], rows k_ld / v_ld and heads
+ *     k_head_ld / v_head_ld elements apart (parts of one fused projection
+ *     will do); bf16 for the write, out_dtype for the read.
+ *   slots: device int64[num_tokens], a token's slot.  Tokens whose slot is
+ *     outside the cache (-1: padding) are left out; the read leaves their rows
+ *     as they are.  The slots of one write are distinct: where two tokens share
+ *     one, its row may mix both.
+ * The write's infinities saturate (6 * 448 * g); a block that holds a NaN gets
+ * scale byte 0x7F and reads as NaN.
+ * Requirements: k and v 16-byte aligned, strides multiples of 16 bytes; slots
+ *   8-byte aligned.  No workspace.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  nvfp4_kv_pages cache;
+  const float *k_global_scale, *v_global_scale;
+  int64_t num_tokens;
+  const void *k, *v;             /* bf16 */
+  int64_t k_ld, k_head_ld, v_ld, v_head_ld;   /* elements */
+  const int64_t *slots;
+} nvfp4_kv_write_args;
+
+nvfp4_status nvfp4_kv_write(const nvfp4_kv_write_args *args, nvfp4_stream stream);
+
+typedef struct {
+  nvfp4_kv_pages cache;
+  const float *k_global_scale, *v_global_scale;
+  int64_t num_tokens;
+  const int64_t *slots;
+  int32_t out_dtype;             /* nvfp4_out_dtype of k and v */
+  void *k, *v;
+  int64_t k_ld, k_head_ld, v_ld, v_head_ld;   /* elements */
+} nvfp4_kv_read_args;
+
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_kv_attention -- attention of new tokens over the cache.
+ *
+ * Sequence b has kv_lens[b] keys, at the slots that its row of the page table
+ * names in order (key j: page page_table[b][j / page_size], offset j mod
+ * page_size), and its queries are rows q_offsets[b] .. q_offsets[b+1]-1 of q:
+ * the last ones of its keys' positions, which the caller has written before.
+ * q_offsets NULL: one query per sequence (total_q == num_seqs).  Query heads
+ * form num_kv_heads equal groups, one per key-value head.  For query i of n_q
+ * of a sequence with n keys, at position p = n - n_q + i:
+ *   s_j = scale * (q . K_j)   over the keys j < n  (causal: j <= p;
+ *         window > 0, causal only: and j > p - window)
+ *   out = sum_j softmax_j(s) V_j,  lse = ln sum_j exp(s_j)
+ * A query that sees no key gets zeros and lse = -inf.  Scores and sums are
+ * fp32; K and V enter the products exactly, q too (to 2^-28 of its row's
+ * largest magnitude), the softmax's numerators rounded to f16; out is rounded
+ * to bf16 once.  What a query does not see does not reach it, NaN neither;
+ * scores are finite for finite inputs below 2^100.
+ *   Device data are clamped, not checked: offsets to [0, total_q] and ascending
+ *   order, lengths to [0, max_pages * page_size]; keys of a page outside
+ *   [0, num_pages) are left out; of a sequence with more than max_q_len queries
+ *   the first max_q_len are computed.  Rows of q outside every sequence are
+ *   left as they are in out and lse.
+ *   q, out: bf16 [total_q][num_heads][head_dim], rows q_ld / out_ld and heads
+ *     q_head_ld / out_head_ld elements apart; lse: float [total_q][num_heads]
+ *     or NULL; page_table: int32 [num_seqs][table_ld], the first max_pages
+ *     columns used; max_q_len: the most queries of a sequence (a bound; it
+ *     picks the kernels).
+ * Requirements: those of the cache; num_heads a multiple of num_kv_heads, at
+ *   most 1024 times of it; total_q, num_seqs < 2^31; q and out 16-byte
+ *   aligned, strides % 8 == 0; page_table, kv_lens, q_offsets, lse 4-byte
+ *   aligned.
+ * Workspace: nvfp4_kv_attention_workspace_size(&args); it does not depend on
+ *   the device data.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  nvfp4_kv_pages cache;
+  const float *k_global_scale, *v_global_scale;
+  int64_t total_q, num_heads, num_seqs;
+  const void *q;                 /* bf16 */
+  int64_t q_ld, q_head_ld;       /* elements */
+  const int32_t *q_offsets;      /* [num_seqs + 1] or NULL */
+  int64_t max_q_len;
+  const int32_t *page_table;
+  int64_t table_ld, max_pages;
+  const int32_t *kv_lens;        /* [num_seqs] */
+  float scale;
+  int32_t causal;
+  int64_t window;                /* 0: none */
+  void *out;                     /* bf16 */
+  int64_t out_ld, out_head_ld;   /* elements */
+  float *lse;
+  void *workspace;
+  size_t workspace_bytes;
+} nvfp4_kv_attention_args;
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_attention_args *args, nvfp4_stream stream);
+size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_attention_args *args);
+
+/* ------------------------------------------------------------------------ *
  * Size queries and status.  (The *_workspace_bytes queries above answer 0 for
  * NULL and for sizes below 1, which their calls refuse.)
  * ------------------------------------------------------------------------ */

@@ -13,7 +13,8 @@ import ctypes as C
 import torch
 
 from ._binding import (DGRAD_DEQUANT_BF16, DGRAD_FP4_COLPACK, EXPORTS, DequantArgs, DgradArgs,
-                       GemmArgs, GroupedArgs, LoraArgs, MoeDownArgs, MxDequantArgs, MxDgradArgs,
+                       GemmArgs, GroupedArgs, KvAttentionArgs, KvPages, KvReadArgs, KvWriteArgs,
+                       LoraArgs, MoeDownArgs, MxDequantArgs, MxDgradArgs,
                        MxGemmArgs, MxGroupedArgs, MxMoeDownArgs, MxQuantArgs, NVFP4Error, OUT_BF16,
                        OUT_FP32, PACK_BOTH, PACK_COL, PACK_ROW, QuantArgs, RouteTopkArgs,
                        RouteTopkBackwardArgs, SCORE_SIGMOID, SCORE_SOFTMAX, SF_LINEAR, SF_SWIZZLED,
@@ -31,7 +32,8 @@ __all__ = [
     "nvfp4_mxfp4_dequantize", "prepare_mxfp4_dequantize", "nvfp4_mxfp4_sf_bytes",
     "nvfp4_mxfp4_gemm", "prepare_mxfp4_gemm", "nvfp4_mxfp4_dgrad", "prepare_mxfp4_dgrad",
     "nvfp4_mxfp4_grouped_gemm", "prepare_mxfp4_grouped", "nvfp4_mxfp4_moe_down_combine",
-    "prepare_mxfp4_moe_down",
+    "prepare_mxfp4_moe_down", "nvfp4_kv_cache", "nvfp4_kv_write", "prepare_kv_write",
+    "nvfp4_kv_read", "prepare_kv_read", "nvfp4_kv_attention", "prepare_kv_attention",
 ]
 
 _PACK = {"row": PACK_ROW, "col": PACK_COL, "both": PACK_BOTH}
@@ -765,3 +767,172 @@ def nvfp4_mxfp4_moe_down_combine(h, perm, expert_offsets, route_weights, w_codes
                                        num_experts, out)
     _run(call, stream)
     return out
+
+
+# ---------------------------------------------------------- key-value cache --
+
+_KV_PARTS = ("k_codes", "k_sf", "v_codes", "v_sf")
+
+
+def nvfp4_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int,
+                   device="cuda") -> dict:
+    """A zero-filled NVFP4 key-value cache, a dict of uint8 tensors: k_codes and
+    v_codes [num_pages, num_kv_heads, page_size, head_dim/2], k_sf and v_sf [..,
+    head_dim/16].  The calls below take any such dict; the tensors' pages may be
+    strided (one layer of a larger cache)."""
+    shape = (num_pages, num_kv_heads, page_size)
+    return {n: torch.zeros(*shape, head_dim // (2 if n.endswith("codes") else 16), dtype=torch.uint8, device=device)
+            for n in _KV_PARTS}
+
+
+def _kv_pages(cache, k_global_scale, v_global_scale):
+    """(KvPages, the tensors it points to) of a cache dict, checked."""
+    parts = [cache[n] for n in _KV_PARTS]
+    if not isinstance(parts[0], torch.Tensor) or parts[0].dim() != 4:
+        raise ValueError("k_codes must be a [pages, heads, page_size, head_dim/2] tensor")
+    P, H, S, half = parts[0].shape
+    hd = 2 * half
+    for n, t in zip(_KV_PARTS, parts):
+        shape = (P, H, S, half if n.endswith("codes") else hd // 16)
+        _need(t, n, (torch.uint8,), shape)
+        if P > 0 and not t[0].is_contiguous():
+            raise ValueError(f"{n} must be contiguous within a page")
+    strides = [t.stride(0) if P > 1 else t[0].numel() if P else 0 for t in parts]
+    if strides[0] != strides[2] or strides[1] != strides[3]:
+        raise ValueError("the pages of keys and values must have equal strides")
+    for n, g in (("k_global_scale", k_global_scale), ("v_global_scale", v_global_scale)):
+        _need(g, n, (torch.float32,), (H,))
+    dev = torch.cuda.current_device()
+    if parts[0].device.index != dev:
+        raise ValueError(f"the cache is on {parts[0].device}, the current device is cuda:{dev}")
+    c = KvPages(num_pages=P, num_kv_heads=H, page_size=S, head_dim=hd, codes_page_stride=strides[0],
+                sf_page_stride=strides[1], **{n: t.data_ptr() for n, t in zip(_KV_PARTS, parts)})
+    return c, (*parts, k_global_scale, v_global_scale)
+
+
+def _kv_rows(t, what: str, dtypes, heads: int, head_dim: int):
+    """(row stride, head stride) of a [tokens, heads, head_dim] tensor, checked."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{what} must be a [tokens, heads, head_dim] tensor")
+    _need(t, what, dtypes, (t.shape[0], heads, head_dim))
+    head = t.stride(1) if heads > 1 else head_dim
+    return (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (heads - 1) * head + head_dim)), head
+
+
+def prepare_kv_write(k, v, slots, cache, k_global_scale, v_global_scale) -> tuple[Prepared, dict]:
+    """Packs keys and values into the cache.  k, v bf16 [tokens, kv_heads,
+    head_dim] (rows and heads may be strided), slots int64 [tokens] = page *
+    page_size + offset (outside the cache, as -1: left out; otherwise distinct),
+    the scales fp32 [kv_heads], static.  Returns (Prepared call, cache)."""
+    lib = load()
+    c, keep = _kv_pages(cache, k_global_scale, v_global_scale)
+    k_ld, k_hld = _kv_rows(k, "k", (torch.bfloat16,), c.num_kv_heads, c.head_dim)
+    v_ld, v_hld = _kv_rows(v, "v", (torch.bfloat16,), c.num_kv_heads, c.head_dim)
+    T = k.shape[0]
+    _need(slots, "slots", (torch.int64,), (T,), T)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of tokens")
+    keep = (k, v, slots, *keep)
+    _same_device(*keep)
+    a = KvWriteArgs(cache=c, k_global_scale=k_global_scale.data_ptr(), v_global_scale=v_global_scale.data_ptr(),
+                    num_tokens=T, k=k.data_ptr(), v=v.data_ptr(), k_ld=k_ld, k_head_ld=k_hld, v_ld=v_ld,
+                    v_head_ld=v_hld, slots=slots.data_ptr())
+    return Prepared(lib.nvfp4_kv_write, a, keep, "nvfp4_kv_write"), cache
+
+
+def nvfp4_kv_write(k, v, slots, cache, k_global_scale, v_global_scale, stream=None) -> dict:
+    """See prepare_kv_write."""
+    call, cache = prepare_kv_write(k, v, slots, cache, k_global_scale, v_global_scale)
+    _run(call, stream)
+    return cache
+
+
+def prepare_kv_read(slots, cache, k_global_scale, v_global_scale, *, out_dtype=torch.bfloat16,
+                    out=None) -> tuple[Prepared, tuple]:
+    """Rows of the cache back as (k, v) [tokens, kv_heads, head_dim] in bf16 or
+    fp32; rows of slots outside the cache are left as they are (out given) or
+    undefined."""
+    lib = load()
+    c, keep = _kv_pages(cache, k_global_scale, v_global_scale)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a [tokens] tensor")
+    T = slots.shape[0]
+    _need(slots, "slots", (torch.int64,), (T,), T)
+    if out is None:
+        out = tuple(torch.empty((T, c.num_kv_heads, c.head_dim), dtype=out_dtype, device=slots.device)
+                    for _ in range(2))
+    k, v = out
+    k_ld, k_hld = _kv_rows(k, "out[0]", tuple(_OUT), c.num_kv_heads, c.head_dim)
+    v_ld, v_hld = _kv_rows(v, "out[1]", (k.dtype,), c.num_kv_heads, c.head_dim)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("out must have a row for each slot")
+    keep = (slots, k, v, *keep)
+    _same_device(*keep)
+    a = KvReadArgs(cache=c, k_global_scale=k_global_scale.data_ptr(), v_global_scale=v_global_scale.data_ptr(),
+                   num_tokens=T, slots=slots.data_ptr(), out_dtype=_OUT[k.dtype], k=k.data_ptr(), v=v.data_ptr(),
+                   k_ld=k_ld, k_head_ld=k_hld, v_ld=v_ld, v_head_ld=v_hld)
+    return Prepared(lib.nvfp4_kv_read, a, keep, "nvfp4_kv_read"), (k, v)
+
+
+def nvfp4_kv_read(slots, cache, k_global_scale, v_global_scale, *, stream=None, **form) -> tuple:
+    """See prepare_kv_read."""
+    call, out = prepare_kv_read(slots, cache, k_global_scale, v_global_scale, **form)
+    _run(call, stream)
+    return out
+
+
+def prepare_kv_attention(q, cache, k_global_scale, v_global_scale, page_table, kv_lens, *, q_offsets=None,
+                         max_q_len: int | None = None, scale: float | None = None, causal: bool = True,
+                         window: int = 0, want_lse: bool = False, out=None) -> tuple[Prepared, tuple]:
+    """Attention of new tokens over the cache.  q bf16 [rows, heads, head_dim]
+    (rows and heads may be strided); page_table int32 [seqs, pages], kv_lens
+    int32 [seqs]: a sequence's keys, the new tokens' among them; q_offsets int32
+    [seqs+1]: the rows of each sequence's queries, the last positions of its keys
+    (None: one query per sequence); max_q_len: the most queries of a sequence, if
+    known (rows beyond it are not computed).  scale: 1/sqrt(head_dim) by default;
+    causal: query at position p sees keys up to p, with window w only the last w
+    of them.  Returns (Prepared call, (out bf16 [rows, heads, head_dim], lse fp32
+    [rows, heads] or None)); a query without keys gets zeros and -inf."""
+    lib = load()
+    c, keep = _kv_pages(cache, k_global_scale, v_global_scale)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [rows, heads, head_dim] tensor")
+    Tq, Hq, hd = q.shape
+    q_ld, q_hld = _kv_rows(q, "q", (torch.bfloat16,), Hq, c.head_dim)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [seqs, pages] tensor")
+    B, pages = page_table.shape
+    _need(page_table, "page_table", (torch.int32,), (B, pages))
+    _need(kv_lens, "kv_lens", (torch.int32,), (B,), B)
+    if q_offsets is not None:
+        _need(q_offsets, "q_offsets", (torch.int32,), (B + 1,), B + 1)
+    elif Tq != B:
+        raise ValueError("without q_offsets q must have one row per sequence")
+    if max_q_len is None:
+        max_q_len = 1 if q_offsets is None else Tq
+    if out is None:
+        out = torch.empty((Tq, Hq, hd), dtype=torch.bfloat16, device=q.device)
+    out_ld, out_hld = _kv_rows(out, "out", (torch.bfloat16,), Hq, hd)
+    if out.shape[0] != Tq:
+        raise ValueError("out must have a row for each row of q")
+    lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device) if want_lse else None
+    keep = (q, page_table, kv_lens, q_offsets, out, lse, *keep)
+    _same_device(*keep)
+    a = KvAttentionArgs(cache=c, k_global_scale=k_global_scale.data_ptr(), v_global_scale=v_global_scale.data_ptr(),
+                        total_q=Tq, num_heads=Hq, num_seqs=B, q=q.data_ptr(), q_ld=q_ld, q_head_ld=q_hld,
+                        q_offsets=None if q_offsets is None else q_offsets.data_ptr(), max_q_len=max_q_len,
+                        page_table=page_table.data_ptr(), table_ld=_ld(page_table), max_pages=pages,
+                        kv_lens=kv_lens.data_ptr(), scale=hd ** -0.5 if scale is None else float(scale),
+                        causal=1 if causal else 0, window=int(window), out=out.data_ptr(), out_ld=out_ld,
+                        out_head_ld=out_hld, lse=None if lse is None else lse.data_ptr())
+    ws = _workspace(a, lib.nvfp4_kv_attention_workspace_size, q.device)
+    call = Prepared(lib.nvfp4_kv_attention, a, (*keep, ws), "nvfp4_kv_attention")
+    call.workspace = ws
+    return call, (out, lse)
+
+
+def nvfp4_kv_attention(q, cache, k_global_scale, v_global_scale, page_table, kv_lens, *, stream=None, **form):
+    """See prepare_kv_attention; returns out, with want_lse (out, lse)."""
+    call, (out, lse) = prepare_kv_attention(q, cache, k_global_scale, v_global_scale, page_table, kv_lens, **form)
+    _run(call, stream)
+    return out if lse is None else (out, lse)

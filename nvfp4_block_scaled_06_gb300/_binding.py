@@ -36,6 +36,7 @@ EXPORTS = [
     "nvfp4_mxfp4_gemm_workspace_bytes", "nvfp4_mxfp4_dgrad", "nvfp4_mxfp4_dgrad_workspace_bytes",
     "nvfp4_mxfp4_grouped_gemm", "nvfp4_mxfp4_grouped_workspace_bytes",
     "nvfp4_mxfp4_moe_down_combine", "nvfp4_mxfp4_moe_down_workspace_bytes",
+    "nvfp4_kv_write", "nvfp4_kv_read", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size",
 ]
 
 DGRAD_DEQUANT_BF16, DGRAD_FP4_COLPACK = 0, 1
@@ -250,6 +251,53 @@ class MxMoeDownArgs(C.Structure):
     ]
 
 
+class KvPages(C.Structure):
+    _fields_ = [
+        ("k_codes", C.c_void_p), ("k_sf", C.c_void_p), ("v_codes", C.c_void_p), ("v_sf", C.c_void_p),
+        ("num_pages", C.c_int64), ("num_kv_heads", C.c_int64), ("page_size", C.c_int64), ("head_dim", C.c_int64),
+        ("codes_page_stride", C.c_int64), ("sf_page_stride", C.c_int64),
+    ]
+
+
+class KvWriteArgs(C.Structure):
+    _fields_ = [
+        ("cache", KvPages),
+        ("k_global_scale", C.c_void_p), ("v_global_scale", C.c_void_p),
+        ("num_tokens", C.c_int64),
+        ("k", C.c_void_p), ("v", C.c_void_p),
+        ("k_ld", C.c_int64), ("k_head_ld", C.c_int64), ("v_ld", C.c_int64), ("v_head_ld", C.c_int64),
+        ("slots", C.c_void_p),
+    ]
+
+
+class KvReadArgs(C.Structure):
+    _fields_ = [
+        ("cache", KvPages),
+        ("k_global_scale", C.c_void_p), ("v_global_scale", C.c_void_p),
+        ("num_tokens", C.c_int64),
+        ("slots", C.c_void_p),
+        ("out_dtype", C.c_int32),
+        ("k", C.c_void_p), ("v", C.c_void_p),
+        ("k_ld", C.c_int64), ("k_head_ld", C.c_int64), ("v_ld", C.c_int64), ("v_head_ld", C.c_int64),
+    ]
+
+
+class KvAttentionArgs(C.Structure):
+    _fields_ = [
+        ("cache", KvPages),
+        ("k_global_scale", C.c_void_p), ("v_global_scale", C.c_void_p),
+        ("total_q", C.c_int64), ("num_heads", C.c_int64), ("num_seqs", C.c_int64),
+        ("q", C.c_void_p), ("q_ld", C.c_int64), ("q_head_ld", C.c_int64),
+        ("q_offsets", C.c_void_p), ("max_q_len", C.c_int64),
+        ("page_table", C.c_void_p), ("table_ld", C.c_int64), ("max_pages", C.c_int64),
+        ("kv_lens", C.c_void_p),
+        ("scale", C.c_float), ("causal", C.c_int32), ("window", C.c_int64),
+        ("out", C.c_void_p), ("out_ld", C.c_int64), ("out_head_ld", C.c_int64),
+        ("lse", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -279,7 +327,8 @@ def load(path: str | None = None):
                         ("nvfp4_mxfp4_dgrad", "nvfp4_mxfp4_dgrad_workspace_bytes", MxDgradArgs),
                         ("nvfp4_mxfp4_grouped_gemm", "nvfp4_mxfp4_grouped_workspace_bytes", MxGroupedArgs),
                         ("nvfp4_mxfp4_moe_down_combine", "nvfp4_mxfp4_moe_down_workspace_bytes",
-                         MxMoeDownArgs)]:
+                         MxMoeDownArgs),
+                        ("nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size", KvAttentionArgs)]:
         f = getattr(lib, fn)
         f.argtypes = [C.POINTER(st), vp]
         f.restype = C.c_int
@@ -288,7 +337,8 @@ def load(path: str | None = None):
         w.restype = C.c_size_t
     for fn, st in [("nvfp4_route_topk", RouteTopkArgs),
                    ("nvfp4_route_topk_backward", RouteTopkBackwardArgs),
-                   ("nvfp4_mxfp4_quantize", MxQuantArgs), ("nvfp4_mxfp4_dequantize", MxDequantArgs)]:
+                   ("nvfp4_mxfp4_quantize", MxQuantArgs), ("nvfp4_mxfp4_dequantize", MxDequantArgs),
+                   ("nvfp4_kv_write", KvWriteArgs), ("nvfp4_kv_read", KvReadArgs)]:
         f = getattr(lib, fn)
         f.argtypes = [C.POINTER(st), vp]
         f.restype = C.c_int

@@ -1832,6 +1832,138 @@ nvfp4_status run_mx_moe_down(const nvfp4_mxfp4_moe_down_args *a, const MxMoeDown
                                         status, layout_makes_inverse(P, pl.prow_max), pl.goffsets + a->num_experts));
 }
 
+// ---------------------------------------------------------- key-value cache --
+nvfp4_status validate_kv_pages(const nvfp4_kv_pages &c) {
+  if (!c.k_codes || !c.k_sf || !c.v_codes || !c.v_sf) return NVFP4_ERR_INVALID_ARG;
+  if (any_empty({c.num_pages, c.num_kv_heads, c.page_size, c.head_dim})) return NVFP4_ERR_INVALID_ARG;
+  if ((c.head_dim != 64 && c.head_dim != 128) || c.page_size < 16 || c.page_size > 1024 ||
+      (c.page_size & (c.page_size - 1)) != 0 || c.num_pages > 0x7FFFFFFFll || c.num_kv_heads > 1024)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t rows = c.num_kv_heads * c.page_size;
+  if (c.num_pages > 1 && (c.codes_page_stride < rows * (c.head_dim / 2) || c.sf_page_stride < rows * (c.head_dim / 16)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(c.k_codes, 16) || !aligned(c.k_sf, 16) || !aligned(c.v_codes, 16) || !aligned(c.v_sf, 16) ||
+      c.codes_page_stride % 16 != 0 || c.sf_page_stride % 16 != 0)
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+int log2_of(int64_t v) {
+  int s = 0;
+  while ((1ll << s) < v) ++s;
+  return s;
+}
+
+// Rows [tokens][heads][head_dim] with the given strides do not overlap.
+bool kv_rows_ok(int64_t heads, int64_t hd, int64_t ld, int64_t head_ld) {
+  return (heads == 1 || head_ld >= hd) && ld >= (heads - 1) * head_ld + hd;
+}
+
+nvfp4_status validate_kv_copy(const nvfp4_kv_pages &c, const float *gk, const float *gv, int64_t tokens,
+                              const int64_t *slots, const void *k, const void *v, int64_t k_ld, int64_t k_head_ld,
+                              int64_t v_ld, int64_t v_head_ld, int64_t item) {
+  if (!gk || !gv || !slots || !k || !v || tokens < 1) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status s = validate_kv_pages(c); s != NVFP4_OK) return s;
+  if (!kv_rows_ok(c.num_kv_heads, c.head_dim, k_ld, k_head_ld) || !kv_rows_ok(c.num_kv_heads, c.head_dim, v_ld, v_head_ld))
+    return NVFP4_ERR_INVALID_ARG;
+  if (tokens > 0x7FFFFFFFll) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || (k_ld | k_head_ld | v_ld | v_head_ld) * item % 16 != 0 ||
+      !aligned(slots, 8) || !all_words_aligned({gk, gv}))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+KvPages kv_pages(const nvfp4_kv_pages &c) {
+  KvPages q{};
+  q.k_codes = c.k_codes;
+  q.k_sf = c.k_sf;
+  q.v_codes = c.v_codes;
+  q.v_sf = c.v_sf;
+  q.codes_stride = c.codes_page_stride;
+  q.sf_stride = c.sf_page_stride;
+  q.num_pages = c.num_pages;
+  q.kv_heads = (int)c.num_kv_heads;
+  q.page_shift = log2_of(c.page_size);
+  q.head_dim = (int)c.head_dim;
+  return q;
+}
+
+struct KvAttnPlan {
+  size_t ws = 0;
+  int nt = 1;                          // rows per tile / 8
+  int64_t *prefix = nullptr;
+  float *part_o = nullptr, *part_ml = nullptr;
+};
+
+void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
+  const int64_t group = a->num_heads / a->cache.num_kv_heads;
+  pl->nt = group * (a->q_offsets ? a->max_q_len : 1) <= 8 ? 1 : 2;
+  const size_t slots = 2 * (size_t)kv_few_spans((int)a->cache.head_dim, pl->nt, plan_sms()) * 8 * pl->nt;
+  Carve c(a->workspace);
+  pl->prefix = c.take<int64_t>((size_t)(a->num_seqs + 1) * 8);
+  pl->part_o = c.take<float>(slots * (size_t)a->cache.head_dim * 4);
+  pl->part_ml = c.take<float>(slots * 8);
+  pl->ws = c.off;
+}
+
+nvfp4_status validate_kv_attention(const nvfp4_kv_attention_args *a) {
+  if (!a || !a->k_global_scale || !a->v_global_scale || !a->q || !a->page_table || !a->kv_lens || !a->out)
+    return NVFP4_ERR_INVALID_ARG;
+  if (any_empty({a->total_q, a->num_heads, a->num_seqs, a->max_pages, a->max_q_len})) return NVFP4_ERR_INVALID_ARG;
+  if (nvfp4_status s = validate_kv_pages(a->cache); s != NVFP4_OK) return s;
+  if (!kv_rows_ok(a->num_heads, a->cache.head_dim, a->q_ld, a->q_head_ld) ||
+      !kv_rows_ok(a->num_heads, a->cache.head_dim, a->out_ld, a->out_head_ld) || a->table_ld < a->max_pages ||
+      (!a->q_offsets && a->total_q != a->num_seqs) || a->window < 0 || (a->window > 0 && !a->causal) ||
+      !(a->scale > 0.0f) || a->scale > 3.0e38f)
+    return NVFP4_ERR_INVALID_ARG;
+  if (a->num_heads % a->cache.num_kv_heads != 0 || a->num_heads / a->cache.num_kv_heads > 1024 ||
+      a->total_q > 0x7FFFFFFFll || a->num_seqs > 0x7FFFFFFFll || a->max_pages > 0x7FFFFFFFll)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(a->q, 16) || !aligned(a->out, 16) || (a->q_ld | a->q_head_ld | a->out_ld | a->out_head_ld) % 8 != 0 ||
+      !all_words_aligned({a->k_global_scale, a->v_global_scale, a->page_table, a->kv_lens, a->q_offsets, a->lse}))
+    return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+
+nvfp4_status run_kv_attention(const nvfp4_kv_attention_args *a, const KvAttnPlan &pl, int sms, cudaStream_t st) {
+  KvAttnParams p{};
+  p.k_codes = a->cache.k_codes;
+  p.k_sf = a->cache.k_sf;
+  p.v_codes = a->cache.v_codes;
+  p.v_sf = a->cache.v_sf;
+  p.codes_stride = a->cache.codes_page_stride;
+  p.sf_stride = a->cache.sf_page_stride;
+  p.num_pages = (int)a->cache.num_pages;
+  p.page_shift = log2_of(a->cache.page_size);
+  p.gk = a->k_global_scale;
+  p.gv = a->v_global_scale;
+  p.q = static_cast<const __nv_bfloat16 *>(a->q);
+  p.q_ld = a->q_ld;
+  p.q_head_ld = a->q_head_ld;
+  p.total_q = (int)a->total_q;
+  p.kv_heads = (int)a->cache.num_kv_heads;
+  p.group = (int)(a->num_heads / a->cache.num_kv_heads);
+  p.seqs = (int)a->num_seqs;
+  p.q_offsets = a->q_offsets;
+  p.max_q = (int)std::min<int64_t>(a->max_q_len, a->total_q);
+  p.table = a->page_table;
+  p.table_ld = a->table_ld;
+  p.max_pages = (int)a->max_pages;
+  p.kv_lens = a->kv_lens;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.causal = a->causal != 0;
+  p.window = a->window;
+  p.out = static_cast<__nv_bfloat16 *>(a->out);
+  p.out_ld = a->out_ld;
+  p.out_head_ld = a->out_head_ld;
+  p.lse = a->lse;
+  p.prefix = pl.prefix;
+  p.part_o = pl.part_o;
+  p.part_ml = pl.part_ml;
+  p.status = reinterpret_cast<int *>(a->workspace);
+  return cuda_status(launch_kv_few(p, (int)a->cache.head_dim, pl.nt, sms, st));
+}
+
 }  // namespace
 
 namespace nvfp4 {
@@ -2226,6 +2358,52 @@ nvfp4_status nvfp4_mxfp4_moe_down_combine(const nvfp4_mxfp4_moe_down_args *a, nv
   plan_mx_moe_down(a, &pl);
   if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.ws)) != NVFP4_OK) return s;
   return run_mx_moe_down(a, pl, d.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_kv_write(const nvfp4_kv_write_args *a, nvfp4_stream stream) {
+  if (!a) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status s = validate_kv_copy(a->cache, a->k_global_scale, a->v_global_scale, a->num_tokens, a->slots, a->k, a->v,
+                                    a->k_ld, a->k_head_ld, a->v_ld, a->v_head_ld, 2);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  KvCopyParams p{kv_pages(a->cache), a->k_global_scale, a->v_global_scale, a->slots, a->num_tokens,
+                 const_cast<void *>(a->k), const_cast<void *>(a->v), a->k_ld, a->k_head_ld, a->v_ld, a->v_head_ld};
+  return cuda_status(launch_kv_write(p, d.sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *a, nvfp4_stream stream) {
+  if (!a || (a->out_dtype != NVFP4_OUT_BF16 && a->out_dtype != NVFP4_OUT_FP32)) return NVFP4_ERR_INVALID_ARG;
+  const bool fp32 = a->out_dtype == NVFP4_OUT_FP32;
+  nvfp4_status s = validate_kv_copy(a->cache, a->k_global_scale, a->v_global_scale, a->num_tokens, a->slots, a->k, a->v,
+                                    a->k_ld, a->k_head_ld, a->v_ld, a->v_head_ld, fp32 ? 4 : 2);
+  if (s != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  KvCopyParams p{kv_pages(a->cache), a->k_global_scale, a->v_global_scale, a->slots, a->num_tokens,
+                 a->k, a->v, a->k_ld, a->k_head_ld, a->v_ld, a->v_head_ld};
+  return cuda_status(launch_kv_read(p, fp32, d.sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_attention_args *a) {
+  if (!a || any_empty({a->total_q, a->num_heads, a->num_seqs, a->max_q_len, a->cache.num_kv_heads, a->cache.head_dim}))
+    return 0;
+  nvfp4_kv_attention_args c = *a;
+  c.workspace = nullptr;
+  KvAttnPlan pl;
+  plan_kv_attention(&c, &pl);
+  return pl.ws;
+}
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_attention_args *a, nvfp4_stream stream) {
+  nvfp4_status s = validate_kv_attention(a);
+  if (s != NVFP4_OK) return s;
+  KvAttnPlan pl;
+  plan_kv_attention(a, &pl);
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, pl.ws)) != NVFP4_OK) return s;
+  DevInfo d;
+  if ((s = device_info(&d)) != NVFP4_OK) return s;
+  return run_kv_attention(a, pl, d.sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -284,6 +284,53 @@ struct RouteGradParams {
 };
 cudaError_t launch_route_topk_backward(const RouteGradParams &p, bool bf16, int num_sms, cudaStream_t st);
 
+// ---------------------------------------------------------- key-value cache --
+struct KvPages {
+  uint8_t *k_codes, *k_sf, *v_codes, *v_sf;
+  int64_t codes_stride, sf_stride;   // bytes from page to page
+  int64_t num_pages;
+  int kv_heads, page_shift, head_dim;
+};
+struct KvCopyParams {
+  KvPages c;
+  const float *gk, *gv;              // [kv_heads]
+  const int64_t *slots;              // [tokens]
+  int64_t tokens;
+  void *k, *v;                       // bf16 rows to write, or bf16 / fp32 rows read back
+  int64_t k_ld, k_head_ld, v_ld, v_head_ld;   // elements
+};
+cudaError_t launch_kv_write(const KvCopyParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_read(const KvCopyParams &p, bool fp32, int num_sms, cudaStream_t st);
+
+struct KvAttnParams {
+  const uint8_t *k_codes, *k_sf, *v_codes, *v_sf;
+  int64_t codes_stride, sf_stride;   // bytes from page to page
+  int num_pages, page_shift;
+  const float *gk, *gv;              // [kv_heads]
+  const __nv_bfloat16 *q;
+  int64_t q_ld, q_head_ld;           // elements
+  int total_q, kv_heads, group, seqs;
+  const int32_t *q_offsets;          // [seqs + 1], or null: one row per sequence
+  int max_q;
+  const int32_t *table;
+  int64_t table_ld;
+  int max_pages;
+  const int32_t *kv_lens;
+  float scale_log2;                  // softmax scale * log2(e)
+  int causal;
+  int64_t window;                    // 0: none
+  __nv_bfloat16 *out;
+  int64_t out_ld, out_head_ld;
+  float *lse;                        // [total_q][heads] or null
+  int64_t *prefix;                   // [seqs + 1]: units before a sequence
+  float *part_o, *part_ml;           // partial results of the spans
+  int *status;
+};
+// Warps of the attention kernel (spans of the work) and the bytes of its
+// partial results, for head_dim and rows per tile 8 * nt.
+int kv_few_spans(int head_dim, int nt, int num_sms);
+cudaError_t launch_kv_few(const KvAttnParams &p, int head_dim, int nt, int num_sms, cudaStream_t st);
+
 // ------------------------------------------------------------- tensor maps --
 // Encodes a 2-D row-major tensor map; returns false on failure.
 bool make_map_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner,
