@@ -18,7 +18,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "gemm_pair.cu", "gemm_skinny.cu", "gemv.cu", "route.cu",
            "static_scratch.cu", "dequant.cu", "router.cu", "mx.cu", "kv_cache.cu",
-           "kv_attention.cu"]
+           "kv_attention.cu", "kv_prompt.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "mxfp4.cuh", "encode.cuh", "kv.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1890,19 +1890,37 @@ KvPages kv_pages(const nvfp4_kv_pages &c) {
 
 struct KvAttnPlan {
   size_t ws = 0;
-  int nt = 1;                          // rows per tile / 8
-  int64_t *prefix = nullptr;
-  float *part_o = nullptr, *part_ml = nullptr;
+  int nt = 0;                          // rows of the kernel for few rows / 8; 0: not run
+  bool prompt = false;                 // some sequence may have more rows
+  int64_t *prefix = nullptr, *item_prefix = nullptr, max_items = 0;
+  float *part_o = nullptr, *part_ml = nullptr, *pr_part_o = nullptr, *pr_part_ml = nullptr;
+  int4 *items = nullptr;
+  int *item_count = nullptr;
 };
 
 void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
-  const int64_t group = a->num_heads / a->cache.num_kv_heads;
-  pl->nt = group * (a->q_offsets ? a->max_q_len : 1) <= 8 ? 1 : 2;
-  const size_t slots = 2 * (size_t)kv_few_spans((int)a->cache.head_dim, pl->nt, plan_sms()) * 8 * pl->nt;
+  const int64_t group = a->num_heads / a->cache.num_kv_heads, hd = a->cache.head_dim;
+  const int64_t rows = group * (a->q_offsets ? std::min(a->max_q_len, a->total_q) : 1);
+  const int64_t few = rows <= 16 ? rows : group;      // beyond: single tokens' rows
+  pl->nt = few <= 8 ? 1 : few <= 16 ? 2 : 0;
+  pl->prompt = rows > 8 * pl->nt;
+  const int sms = plan_sms();
   Carve c(a->workspace);
-  pl->prefix = c.take<int64_t>((size_t)(a->num_seqs + 1) * 8);
-  pl->part_o = c.take<float>(slots * (size_t)a->cache.head_dim * 4);
-  pl->part_ml = c.take<float>(slots * 8);
+  if (pl->nt > 0) {
+    const size_t slots = 2 * (size_t)kv_few_spans(pl->nt, sms) * 8 * pl->nt;
+    pl->prefix = c.take<int64_t>((size_t)(a->num_seqs + 1) * 8);
+    pl->part_o = c.take<float>(slots * (size_t)hd * 4);
+    pl->part_ml = c.take<float>(slots * 8);
+  }
+  if (pl->prompt) {
+    pl->max_items = kv_prompt_max_items(a->total_q, group, a->num_seqs);
+    const size_t slots = (size_t)kv_prompt_slots(sms);
+    pl->items = c.take<int4>((size_t)pl->max_items * sizeof(int4));
+    pl->item_prefix = c.take<int64_t>((size_t)(pl->max_items + 1) * 8);
+    pl->item_count = c.take<int>(4);
+    pl->pr_part_o = c.take<float>(slots * (size_t)hd * 4);
+    pl->pr_part_ml = c.take<float>(slots * 8);
+  }
   pl->ws = c.off;
 }
 
@@ -1960,8 +1978,19 @@ nvfp4_status run_kv_attention(const nvfp4_kv_attention_args *a, const KvAttnPlan
   p.prefix = pl.prefix;
   p.part_o = pl.part_o;
   p.part_ml = pl.part_ml;
+  p.few_rows = 8 * pl.nt;
+  p.items = pl.items;
+  p.item_prefix = pl.item_prefix;
+  p.item_count = pl.item_count;
+  p.max_items = pl.max_items;
+  p.pr_part_o = pl.pr_part_o;
+  p.pr_part_ml = pl.pr_part_ml;
   p.status = reinterpret_cast<int *>(a->workspace);
-  return cuda_status(launch_kv_few(p, (int)a->cache.head_dim, pl.nt, sms, st));
+  p.timeout_ns = g_timeout_ns.load();
+  p.stall_probe = p.timeout_ns == 0;
+  if (pl.prompt)
+    if (cudaError_t e = launch_kv_prompt(p, (int)a->cache.head_dim, sms, st); e != cudaSuccess) return cuda_status(e);
+  return pl.nt > 0 ? cuda_status(launch_kv_few(p, (int)a->cache.head_dim, pl.nt, sms, st)) : NVFP4_OK;
 }
 
 }  // namespace

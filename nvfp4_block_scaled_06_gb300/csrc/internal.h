@@ -322,14 +322,25 @@ struct KvAttnParams {
   __nv_bfloat16 *out;
   int64_t out_ld, out_head_ld;
   float *lse;                        // [total_q][heads] or null
+  int few_rows;                      // sequences of up to this many rows per key-value head go to the kernel for few
   int64_t *prefix;                   // [seqs + 1]: units before a sequence
   float *part_o, *part_ml;           // partial results of the spans
+  int4 *items;                       // [max_items]: the prompt kernel's row tiles
+  int64_t *item_prefix;              // [max_items + 1]: key tiles before an item
+  int *item_count;
+  int64_t max_items;
+  float *pr_part_o, *pr_part_ml;     // the prompt kernel's partial results
   int *status;
+  uint64_t timeout_ns;
+  int stall_probe;                   // test hook: first wait on a barrier nothing arrives at
 };
-// Warps of the attention kernel (spans of the work) and the bytes of its
-// partial results, for head_dim and rows per tile 8 * nt.
-int kv_few_spans(int head_dim, int nt, int num_sms);
+// Few rows (8 * nt) per sequence and key-value head.  Spans: warps of the kernel.
+int kv_few_spans(int nt, int num_sms);
 cudaError_t launch_kv_few(const KvAttnParams &p, int head_dim, int nt, int num_sms, cudaStream_t st);
+// The sequences with more rows than p.few_rows.  Slots: rows of partial results.
+int64_t kv_prompt_max_items(int64_t total_q, int64_t group, int64_t seqs);
+int64_t kv_prompt_slots(int num_sms);
+cudaError_t launch_kv_prompt(const KvAttnParams &p, int head_dim, int num_sms, cudaStream_t st);
 
 // ------------------------------------------------------------- tensor maps --
 // Encodes a 2-D row-major tensor map; returns false on failure.

@@ -23,8 +23,8 @@
 // units of log2): P stays below 2^8, and the usual step needs no reduction
 // over lanes and no rescaling.
 //
-// Work: 16-key units of all (sequence, head, row tile) segments in one line, cut
-// into equal spans, one per warp; a warp's ring of asynchronous copies runs on
+// Work: 16-key units of all (sequence, head) segments in one line, cut into equal
+// spans, one per warp; a warp's ring of asynchronous copies runs on
 // over segment borders.  Segments that lie in more than one span leave partial
 // (o, m, l) per span, which a second kernel sums in order.
 #include <math_constants.h>
@@ -65,27 +65,28 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-// Units of one segment of sequence b and its first unit; tiles of 8 NT rows.
+// The segments of sequence b: first unit, units (0: no rows, or more than this
+// kernel takes), rows.
 struct Seg {
   KvSeq s;
-  int u0, units, tiles;
+  int u0, units, rows;
 };
-template <int NT>
 __device__ __forceinline__ Seg seg_of(const KvAttnParams &p, int b) {
   Seg g;
   g.s = kv_seq(p, b);
+  const int64_t rows = (int64_t)g.s.qn * p.group;
+  g.rows = rows > p.few_rows ? 0 : (int)rows;
   g.u0 = g.s.lo >> 4;
-  g.units = max(1, (int)(((int64_t)g.s.hi + 15) >> 4) - g.u0);
-  g.tiles = (int)(((int64_t)g.s.qn * p.group + 8 * NT - 1) / (8 * NT));
+  g.units = g.rows > 0 ? max(1, (int)(((int64_t)g.s.hi + 15) >> 4) - g.u0) : 0;
   return g;
 }
 __device__ __forceinline__ int64_t units_of(const KvAttnParams &p, const Seg &g) {
-  return (int64_t)g.units * g.tiles * p.kv_heads;
+  return (int64_t)g.units * p.kv_heads;
 }
 
 // A position in the line of units.
 struct Cursor {
-  int b, h, tile, u;   // u: unit within the segment
+  int b, h, u;         // u: unit within the segment
   Seg g;
 };
 
@@ -94,18 +95,15 @@ __device__ __forceinline__ int64_t span_of(int64_t u, int64_t total, int64_t spa
   return ((u + 1) * spans - 1) / total;
 }
 
-template <int NT>
 __device__ __forceinline__ void next_unit(const KvAttnParams &p, Cursor &c) {
   if (++c.u < c.g.units) return;
   c.u = 0;
-  if (++c.tile < c.g.tiles) return;
-  c.tile = 0;
   if (++c.h < p.kv_heads) return;
   c.h = 0;
   do {
     if (++c.b >= p.seqs) return;
-    c.g = seg_of<NT>(p, c.b);
-  } while (c.g.tiles == 0);
+    c.g = seg_of(p, c.b);
+  } while (c.g.units == 0);
 }
 
 template <int HD, int NT>
@@ -129,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   const int each = (entries + kWarps * 32 - 1) / (kWarps * 32);   // entries of a thread
   const int e0 = min(tid * each, entries), e1 = min(e0 + each, entries);
   int64_t sum = 0;
-  for (int b = e0 * per; b < min(e1 * per, p.seqs); ++b) sum += units_of(p, seg_of<NT>(p, b));
+  for (int b = e0 * per; b < min(e1 * per, p.seqs); ++b) sum += units_of(p, seg_of(p, b));
   int64_t scan = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +142,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
     pre[e] = base;
     for (int b = e * per; b < min((e + 1) * per, p.seqs); ++b) {
       if (blockIdx.x == 0) p.prefix[b] = base;
-      base += units_of(p, seg_of<NT>(p, b));
+      base += units_of(p, seg_of(p, b));
     }
   }
   int64_t total = 0;
@@ -153,9 +151,9 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   __syncthreads();
   if (total == 0) return;
 
-  const int64_t spans = (int64_t)gridDim.x * kWarps, span = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t spans = min((int64_t)gridDim.x * kWarps, total), span = (int64_t)blockIdx.x * kWarps + warp;
+  if (span >= spans) return;
   const int64_t u_begin = span_start(span, total, spans), u_end = span_start(span + 1, total, spans);
-  if (u_begin >= u_end) return;
 
   Cursor cur;
   {
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
     int64_t at = pre[lo];
     cur.b = lo * per;
     for (;; ++cur.b) {                              // (ends before p.seqs: u_begin < total)
-      cur.g = seg_of<NT>(p, cur.b);
+      cur.g = seg_of(p, cur.b);
       const int64_t n = units_of(p, cur.g);
       if (u_begin < at + n) break;
       at += n;
@@ -175,8 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
     const int64_t r = u_begin - at;
     const int64_t seg = r / cur.g.units;
     cur.u = (int)(r - seg * cur.g.units);
-    cur.tile = (int)(seg % cur.g.tiles);
-    cur.h = (int)(seg / cur.g.tiles);
+    cur.h = (int)seg;
   }
   Cursor ahead = cur;                               // of the copies
 
@@ -220,7 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   for (; issued < S - 1; ++issued) {
     if (issued < count) {
       copy_unit((int)issued);
-      next_unit<NT>(p, ahead);
+      next_unit(p, ahead);
     }
     cp_async_commit();
   }
@@ -239,7 +236,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   for (int64_t i = 0; i < count; ++i, ++u) {
     if (fresh) {
       fresh = false;
-      const int rows = cur.g.s.qn * p.group - cur.tile * F::kRows;   // of this tile
+      const int rows = cur.g.rows;
       const float gk = p.gk[cur.h];
       all_lo = 0;
       all_hi = 0x7FFFFFFF;
@@ -249,7 +246,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         float mx = 0.0f;
         const int r = nt * 8 + g;
         if (r < rows) {
-          const int rr = cur.tile * F::kRows + r, tok = rr / p.group, head = cur.h * p.group + rr % p.group;
+          const int tok = r / p.group, head = cur.h * p.group + r % p.group;
           const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(cur.g.s.q0 + tok) * p.q_ld +
                                                              (int64_t)head * p.q_head_ld + t * (HD / 4));
 #pragma unroll
@@ -275,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = (int)(top >> 23);
         // a power of two that brings the row's maximum to [2^13, 2^14); 1 for rows with an infinity or a NaN
-        const int up = e == 255 ? 127 : min(267 - e, 250);
+        const int up = e == 255 ? 127 : min(267 - e, 190);
         const float mul = __uint_as_float((uint32_t)up << 23);
         mx = __uint_as_float((uint32_t)(254 - up) << 23) * (p.scale_log2 * gk);
 #pragma unroll
@@ -288,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
           // row 8 nt + 2 t + k is held by the lanes of g = 2 t + k
           sc[nt][k] = __shfl_sync(0xffffffffu, mx, (2 * t + k) * 4);
           const int r2 = nt * 8 + 2 * t + k;
-          const int tok = (cur.tile * F::kRows + r2) / p.group;
+          const int tok = r2 / p.group;
           const int64_t pos = (int64_t)cur.g.s.n - cur.g.s.qt + tok;
           see_hi[nt][k] = p.causal ? (int)max((int64_t)0, pos + 1) : cur.g.s.n;
           see_lo[nt][k] = p.window > 0 ? (int)max((int64_t)0, pos + 1 - p.window) : 0;
@@ -313,7 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
 
     if (issued < count) {
       copy_unit(fill);
-      next_unit<NT>(p, ahead);
+      next_unit(p, ahead);
     }
     ++issued;
     cp_async_commit();
@@ -491,10 +488,10 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
           float sum_l = l[nt][k];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) sum_l += __shfl_xor_sync(0xffffffffu, sum_l, d);
-          const int r = nt * 8 + 2 * t + k, rr = cur.tile * F::kRows + r;
-          if (rr >= cur.g.s.qn * p.group) continue;
+          const int r = nt * 8 + 2 * t + k;
+          if (r >= cur.g.rows) continue;
           if (whole_seg) {
-            const int tok = rr / p.group, head = cur.h * p.group + rr % p.group;
+            const int tok = r / p.group, head = cur.h * p.group + r % p.group;
             const float f = sum_l == 0.0f ? 0.0f : p.gv[cur.h] / sum_l;
             uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)(cur.g.s.q0 + tok) * p.out_ld +
                                                    (int64_t)head * p.out_head_ld + g * (HD / 8));
@@ -517,7 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
           }
         }
       if (i + 1 == count) break;
-      next_unit<NT>(p, cur);
+      next_unit(p, cur);
       fresh = true;
     } else {
       ++cur.u;
@@ -530,7 +527,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
 // spans' partial results dealt to its warps in order, one 16-byte (8-byte) run
 // of channels per lane.
 template <int HD, int NT>
-__global__ void __launch_bounds__(256) k_kv_combine(const KvAttnParams p, int spans) {
+__global__ void __launch_bounds__(256) k_kv_combine(const KvAttnParams p, int max_spans) {
   constexpr int kRows = 8 * NT, kV = HD / 32, kW = 8;
   __shared__ float sh_o[kW][HD];
   __shared__ float sh_m[kW], sh_l[kW];
@@ -538,15 +535,12 @@ __global__ void __launch_bounds__(256) k_kv_combine(const KvAttnParams p, int sp
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x;
-  const int64_t total = p.prefix[p.seqs];
-  const Seg g = seg_of<NT>(p, b);
-  const int64_t segs = (int64_t)g.tiles * p.kv_heads;
-  for (int64_t x = blockIdx.y; x < segs * kRows; x += gridDim.y) {
-    const int64_t seg = x / kRows;
-    const int r = (int)(x % kRows), tile = (int)(seg % g.tiles), h = (int)(seg / g.tiles);
-    const int rr = tile * kRows + r;
-    if (rr >= g.s.qn * p.group) continue;
-    const int64_t first = p.prefix[b] + seg * g.units;
+  const Seg g = seg_of(p, b);
+  if (g.units == 0) return;
+  const int64_t total = p.prefix[p.seqs], spans = min((int64_t)max_spans, total);
+  for (int x = blockIdx.y; x < p.kv_heads * g.rows; x += gridDim.y) {
+    const int r = x % g.rows, h = x / g.rows;
+    const int64_t first = p.prefix[b] + (int64_t)h * g.units;
     const int64_t c0 = span_of(first, total, spans), c1 = span_of(first + g.units - 1, total, spans);
     if (c0 == c1) continue;
     float m = -CUDART_INF_F, l = 0.0f, o[kV];
@@ -592,7 +586,7 @@ __global__ void __launch_bounds__(256) k_kv_combine(const KvAttnParams p, int sp
 #pragma unroll
       for (int v = 0; v < kV; ++v) o[v] += sh_o[w][lane * kV + v] * f;
     }
-    const int tok = rr / p.group, head = h * p.group + rr % p.group;
+    const int tok = r / p.group, head = h * p.group + r % p.group;
     const float f = ll == 0.0f ? 0.0f : p.gv[h] / ll;
     __nv_bfloat16 *dst = p.out + (int64_t)(g.s.q0 + tok) * p.out_ld + (int64_t)head * p.out_head_ld + lane * kV;
     if constexpr (kV == 4)
@@ -619,8 +613,7 @@ cudaError_t run_few(const KvAttnParams &p, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-int kv_few_spans(int head_dim, int nt, int num_sms) {
-  (void)head_dim;
+int kv_few_spans(int nt, int num_sms) {
   return num_sms * (nt == 1 ? 4 : 2) * kWarps;
 }
 
