@@ -10,13 +10,14 @@
 //
 // Bound: the tensor cores, 4 x 128 x 256 x head_dim operations per step and 4096
 // multiply-adds a cycle; next to them 32768 exponentials (32 a cycle) and the
-// decode of 2 x 128 x head_dim cached values.  Roles of a CTA's 13 warps:
+// decode of 2 x 128 x head_dim cached values.  Roles of a CTA's warps:
 //   0-3, 4-7  softmax of one half each, a thread per row: S from tensor memory,
 //             P back into the same columns as f16, O's rescaling and the result
 //   8-11      a thread per key: packed row -> f16 row in the swizzled K or V
 //             tile (a cached value is decoded once per 256 rows)
 //   12        issues the MMAs: P V of one half and S of its next step while the
-//             softmax of the other half runs
+//             softmax of the other half runs (13-15 idle: registers move by
+//             warpgroup)
 // V's tile lies as K's does, a key per row; it enters as the transposed operand.
 //
 // Work: the steps of all (row tile, head) segments in one line, cut into equal
@@ -25,6 +26,8 @@
 // order by a second kernel.  A first kernel lists the row tiles.
 #include <float.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "kv.cuh"
@@ -35,7 +38,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kRowsTile = 256;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
+// Registers per thread of the three kinds of warpgroups (softmax twice): as many as the launch's 512 x 128.
+constexpr int kRegsSoftmax = 184, kRegsTiles = 88, kRegsMma = 56;
+static_assert(128 * (2 * kRegsSoftmax + kRegsTiles + kRegsMma) == kThreads * 128, "");
 constexpr float kRaiseBy = 8.0f;
 constexpr uint64_t kKvDrainNs = 200000000ull;
 
@@ -80,6 +86,31 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// Waits for this thread's loads from tensor memory; what x holds is used after it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]),
+                 "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]),
+                 "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
+                 "+r"(x[30]), "+r"(x[31])::"memory");
+}
+// One lane of a converged warp, the same each time; a branch on it keeps the
+// MMAs' operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r)::"memory");
+  return r != 0;
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
@@ -127,13 +158,15 @@ __global__ void __launch_bounds__(1024) k_kv_list(const KvAttnParams p) {
     __syncthreads();
     if (lane == 31) wsum[warp] = s;
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
+    int64_t t = wsum[lane];                    // the warps' sums, added up by every warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += x;
     }
-    return before + s - v;
+    total = __shfl_sync(0xffffffffu, t, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, t, max(warp - 1, 0));
+    return (warp > 0 ? before : 0) + s - v;
   };
   int64_t items = 0, units = 0;
   for (int b0 = 0; b0 < p.seqs; b0 += 1024) {
@@ -230,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
   uint64_t *s_ready = bars + 4 * S, *p_ready = s_ready + 2, *o_full = s_ready + 4, *q_ready = s_ready + 6;
   uint64_t *drain = s_ready + 8, *never = s_ready + 9;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -291,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
     }
     if (warp < 8) {
       // -------------------------------------------------------------- softmax --
+      regs_up<kRegsSoftmax>();
       const int half = warp >> 2, row = (warp & 3) * 32 + lane;     // of the half
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_col = tmem + lane_off + half * 128, o_col = tmem + lane_off + T::kO + half * HD;
@@ -306,8 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           continue;
         }
         const bool live = half * 128 + row < rows;
-        const int64_t rr = (int64_t)w.it.y * kRowsTile + half * 128 + row;
-        const int tok = live ? (int)(rr / p.group) : 0, head = w.h * p.group + (live ? (int)(rr % p.group) : 0);
+        // row r of the tile: token tok0 + (rem0 + r) / group, head (rem0 + r) % group of the group
+        const int tok0 = (int)((int64_t)w.it.y * kRowsTile / p.group);
+        const uint32_t rem0 = (uint32_t)((int64_t)w.it.y * kRowsTile % p.group) + half * 128, grp = p.group;
+        const int tok = tok0 + (int)((rem0 + row) / grp), head = w.h * p.group + (int)((rem0 + row) % grp);
         // the keys [see_lo, see_hi) of this row; rows past the last see all and hold zeros
         int see_lo = 0, see_hi = 0x7FFFFFFF;
         if (live) {
@@ -316,36 +352,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           if (p.window > 0) see_lo = (int)max((int64_t)0, pos + 1 - p.window);
         }
         const int all_lo = __reduce_max_sync(0xffffffffu, see_lo), all_hi = __reduce_min_sync(0xffffffffu, see_hi);
-        float sc;
+        // Q: 16-byte runs of a row on consecutive lanes; a row's lanes agree on its power of two
+        float sc = 0.0f;
         {
-          uint32_t x[HD / 2];
-          const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(s.q0 + tok) * p.q_ld +
-                                                             (int64_t)head * p.q_head_ld);
-          uint32_t m2 = 0;
+          constexpr int kL = HD / 8, kR = 32 / kL;   // lanes of a row, rows at a time
+          const float gsc = p.scale_log2 * p.gk[w.h];
+          const int c = lane % kL;
+          const int64_t own = (int64_t)(s.q0 + tok) * p.q_ld + (int64_t)head * p.q_head_ld;
+          uint4 v[32 / kR];
 #pragma unroll
-          for (int i = 0; i < HD / 8; ++i) {
-            const uint4 v = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+          for (int i = 0; i < 32 / kR; ++i) {
+            const int src = i * kR + lane / kL;
+            const int64_t at = __shfl_sync(0xffffffffu, own, src);
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (half * 128 + (warp & 3) * 32 + src < rows) v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + at) + c);
           }
 #pragma unroll
-          for (int i = 0; i < HD / 2; ++i) m2 = __vmaxu2(m2, x[i] & 0x7FFF7FFFu);
-          const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7);
-          // a power of two that brings the row's maximum to [2^13, 2^14); 1 for rows with an infinity or a NaN
-          const int up = e == 255 ? 127 : min(267 - e, 190);
-          const float mul = __uint_as_float((uint32_t)up << 23);
-          sc = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * (p.scale_log2 * p.gk[w.h]), FLT_MIN);
-          const uint32_t dst = smem_u32(sq) + row * 128;
+          for (int i = 0; i < 32 / kR; ++i) {
+            const int rw = (warp & 3) * 32 + i * kR + lane / kL;
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t m2 = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
+                                   __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
 #pragma unroll
-          for (int c = 0; c < HD / 8; ++c) {
+            for (int o = 1; o < kL; o <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+            const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7);
+            // a power of two that brings the row's maximum to [2^13, 2^14); 1 for rows with an infinity or a NaN
+            const int up = e == 255 ? 127 : min(267 - e, 190);
+            const float mul = __uint_as_float((uint32_t)up << 23);
             uint32_t h[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = pack_h2(bf16lo(x[4 * c + i]) * mul, bf16hi(x[4 * c + i]) * mul);
-            sts128(dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+            for (int k = 0; k < 4; ++k) h[k] = pack_h2(bf16lo(x[k]) * mul, bf16hi(x[k]) * mul);
+            sts128(smem_u32(sq) + rw * 128 + (c >> 3) * 16384 + (((c & 7) ^ (rw & 7)) << 4), h[0], h[1], h[2], h[3]);
+            const int back = __shfl_sync(0xffffffffu, 254 - up, lane % kR * kL);
+            if (lane / kR == i) sc = fmaxf(__uint_as_float((uint32_t)back << 23) * gsc, FLT_MIN);
           }
         }
         fence_proxy_async_shared();
         tc_fence_before();
         mbar_arrive(q_ready + half);
+        {
+          // the next segment's row of Q on its way to L2
+          Walk nx = w;
+          if (nx.next(p)) {
+            const KvSeq s2 = kv_seq(p, nx.it.x);
+            const int64_t r2 = (int64_t)nx.it.y * kRowsTile + half * 128 + row;
+            if (r2 < (int64_t)s2.qn * p.group) {
+              const __nv_bfloat16 *src = p.q + (s2.q0 + r2 / p.group) * p.q_ld +
+                                         (nx.h * p.group + r2 % p.group) * p.q_head_ld;
+#pragma unroll
+              for (int i = 0; i < HD; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
+            }
+          }
+        }
         float m = -CUDART_INF_F, l = 0.0f;
         for (int j = w.j0; j < w.j1; ++j, ++tiles, ++steps) {
           if (!(ok = warp_wait(s_ready + half, steps & 1))) break;
@@ -353,17 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           const int key0 = (w.it.z + j) * 128;
           const uint32_t *km = kmask[tiles & 3];
           const bool whole = key0 >= all_lo && key0 + 128 <= all_hi && (km[0] & km[1] & km[2] & km[3]) == 0xFFFFFFFFu;
-          // 32 keys' scores as S * sc, -inf where the row does not see them
-          auto load = [&](int c, uint32_t (&x)[32]) {
-            tmem_ld_32x32b_x32(s_col + c * 32, x);
-            tmem_ld_wait();
-            if (!whole) {
-              const uint32_t bits = km[c];
-              const int rel = key0 + c * 32;
+          // -inf where the row does not see a key, of the 32 from chunk c on
+          auto mask = [&](int c, uint32_t (&x)[32]) {
+            if (whole) return;
+            // of the row's range: the bits from its first key on and below its last
+            const int from = min(max(see_lo - key0 - c * 32, 0), 32), to = min(max(see_hi - key0 - c * 32, 0), 32);
+            const uint32_t bits = km[c] & (uint32_t)((1ull << to) - 1) & ~(uint32_t)((1ull << from) - 1);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((bits >> i) & 1u) || rel + i < see_lo || rel + i >= see_hi) x[i] = 0xFF800000u;
-            }
+            for (int i = 0; i < 32; ++i) x[i] = bits & (1u << i) ? x[i] : 0xFF800000u;
           };
           uint32_t pk[64];
           float sum;
@@ -374,7 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 uint32_t x[32];
-                load(c, x);
+                tmem_ld_32x32b_x32(s_col + c * 32, x);
+                tmem_ld_wait_for(x);
+                mask(c, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
               }
@@ -388,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
                 for (int c = 0; c < HD / 32; ++c) {
                   uint32_t x[32];
                   tmem_ld_32x32b_x32(o_col + c * 32, x);
-                  tmem_ld_wait();
+                  tmem_ld_wait_for(x);
 #pragma unroll
                   for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
                   tmem_st_x32(o_col + c * 32, x);
@@ -399,10 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
             const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(-ref, -ref);
             uint64_t acc[2] = {0, 0};
             uint32_t top = 0;
+            uint32_t buf[2][32];
+            tmem_ld_32x32b_x32(s_col, buf[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              load(c, x);
+              uint32_t (&x)[32] = buf[c & 1];
+              tmem_ld_wait_for(x);
+              if (c < 3) tmem_ld_32x32b_x32(s_col + (c + 1) * 32, buf[(c + 1) & 1]);
+              mask(c, x);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const uint64_t y = fma2(((uint64_t)x[2 * i + 1] << 32) | x[2 * i], sc2, ref2);
@@ -450,41 +511,81 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
         }
         const bool full = w.j0 == 0 && w.j1 == w.it.w;
         const int64_t prow = (2 * cta + (first_seg ? 0 : 1)) * kRowsTile + half * 128 + row;
-        const float f = !full ? 1.0f : l == 0.0f ? 0.0f : p.gv[w.h] / l;
-        __nv_bfloat16 *dst = p.out + (int64_t)(s.q0 + tok) * p.out_ld + (int64_t)head * p.out_head_ld;
+        // 256 bytes of each of the warp's rows at a time go through its rows of Q, which no MMA reads any more
+        // (o_full), so that 16 lanes write one row; own: this thread's row of the destination in 16-byte runs
+        const uint32_t stage = smem_u32(sq) + (warp & 3) * 32 * 128;
+        auto put = [&](int q, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          sts128(stage + lane * 128 + (q >> 3) * 16384 + (((q & 7) ^ (lane & 7)) << 4), a0, a1, a2, a3);
+        };
+        auto flush = [&](auto width, uint4 *base, int64_t own) {
+          constexpr int kL = decltype(width)::value / 16, kR = 32 / kL;   // lanes of a row, rows at a time
+          const int q = lane % kL;
+          uint4 v[32 / kR];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32 / kR; ++i) {
+            const int rw = i * kR + lane / kL;
+            v[i] = lds128(stage + rw * 128 + (q >> 3) * 16384 + (((q & 7) ^ (rw & 7)) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < 32 / kR; ++i) {
+            const int rw = i * kR + lane / kL;
+            const int64_t at = __shfl_sync(0xffffffffu, own, rw);
+            if (half * 128 + (warp & 3) * 32 + rw < rows) base[at + q] = v[i];
+          }
+          __syncwarp();
+        };
+        auto nans = [&](int c, uint32_t (&x)[32]) {      // columns 32 c ...
+          if (!__any_sync(0xffffffffu, nan_blocks != 0)) return;
+          const uint32_t nb = nan_blocks >> (2 * c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = (nb >> (i >> 4)) & 1u ? 0x7FC00000u : x[i];
+        };
+        if (full) {
+          const float f = l == 0.0f ? 0.0f : p.gv[w.h] / l;
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(o_col + c * 32, x);
+            tmem_ld_wait_for(x);
+            nans(c, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = pack_bf2(__uint_as_float(x[8 * i + 2 * k]) * f, __uint_as_float(x[8 * i + 2 * k + 1]) * f);
+              put(4 * c + i, h[0], h[1], h[2], h[3]);
+            }
+          }
+          flush(std::integral_constant<int, HD * 2>(), reinterpret_cast<uint4 *>(p.out),
+                ((int64_t)(s.q0 + tok) * p.out_ld + (int64_t)head * p.out_head_ld) / 8);
+          if (live && p.lse)
+            p.lse[(int64_t)(s.q0 + tok) * p.kv_heads * p.group + head] = (m + __log2f(l)) * CUDART_LN2_F;
+        } else {
+          constexpr int kCols = HD / 2;                  // of a round: 2 HD bytes of a row
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(o_col + c * 32, x);
-          tmem_ld_wait();
+          for (int rd = 0; rd < 2; ++rd) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float y = __uint_as_float(x[i]) * f;
-            if ((nan_blocks >> (2 * c + (i >> 4))) & 1u) y = CUDART_NAN_F;
-            x[i] = __float_as_uint(y);
+            for (int c = 0; c < kCols / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(o_col + rd * kCols + c * 32, x);
+              tmem_ld_wait_for(x);
+              nans(rd * (kCols / 32) + c, x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) put(8 * c + i, x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+            flush(std::integral_constant<int, HD * 2>(), reinterpret_cast<uint4 *>(p.pr_part_o) + rd * (HD / 8),
+                  prow * (HD / 4));
           }
-          if (!live) continue;
-          if (full) {
-            uint32_t h[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) h[i] = pack_bf2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d4[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-          } else {
-            uint4 *d4 = reinterpret_cast<uint4 *>(p.pr_part_o + prow * HD + c * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d4[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          }
+          if (live) *reinterpret_cast<float2 *>(p.pr_part_ml + prow * 2) = make_float2(m, l);
         }
-        if (live && !full) *reinterpret_cast<float2 *>(p.pr_part_ml + prow * 2) = make_float2(m, l);
-        if (live && full && p.lse)
-          p.lse[(int64_t)(s.q0 + tok) * p.kv_heads * p.group + head] = (m + __log2f(l)) * CUDART_LN2_F;
         tc_fence_before();
         first_seg = false;
       } while (w.next(p));
     } else if (warp < 12) {
       // -------------------------------------------------------- K and V tiles --
+      regs_down<kRegsTiles>();
       const int key_in = tid - 256;                 // this thread's key of a tile
       const uint32_t sk = smem_u32(smem) + 2 * T::kHalf, sv = sk + S * T::kHalf;
       const uint32_t row_off = key_in * 128, sw = key_in & 7;
@@ -589,95 +690,101 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           phase ^= 1;
         }
       }
-    } else if (lane == 0) {
+    } else {
       // ------------------------------------------------------------ MMA issue --
-      // (only lane 0 walks: the search above needed the whole warp)
-      constexpr uint32_t id_s = idesc_f16(128, 128, 0), id_o = idesc_f16(128, HD, 1);
-      const uint64_t qd = sdesc_k_sw128(smem), kd = sdesc_k_sw128(smem + 2 * T::kHalf);
-      const uint64_t vd = sdesc_mn_sw128(smem_u32(smem) + (2 + S) * T::kHalf, 16384);
-      uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
-      int st_k = 0, st_v = 0;
-      uint32_t ph_k = 0, ph_v = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!abort_flag && mbar_wait(bar, parity, p.timeout_ns)) return true;
-        give_up();
-        return false;
-      };
-      if (p.stall_probe) ok = wait(never, 0);       // the expiry path under test
-      auto issue_s = [&](int half) {
+      regs_down<kRegsMma>();
+      // (the whole warp walks and waits, one lane issues)
+      if (warp == 12) {
+        constexpr uint32_t id_s = idesc_f16(128, 128, 0), id_o = idesc_f16(128, HD, 1);
+        const uint64_t qd = sdesc_k_sw128(smem), kd = sdesc_k_sw128(smem + 2 * T::kHalf);
+        const uint64_t vd = sdesc_mn_sw128(smem_u32(smem) + (2 + S) * T::kHalf, 16384);
+        uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+        int st_k = 0, st_v = 0;
+        uint32_t ph_k = 0, ph_v = 0;
+        bool ok = true;
+        if (p.stall_probe) ok = warp_wait(never, 0);   // the expiry path under test
+        auto issue_s = [&](int half) {
+          const uint64_t a = qd + (uint64_t)((half * T::kHalf) >> 4), b = kd + (uint64_t)((st_k * T::kHalf) >> 4);
+          if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint64_t off = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2);
-          asm volatile(
-              "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + half * 128),
-              "l"(qd + (uint64_t)((half * T::kHalf) >> 4) + off), "l"(kd + (uint64_t)((st_k * T::kHalf) >> 4) + off),
-              "r"(id_s), "r"(k ? 1u : 0u)
-              : "memory");
-        }
-        tc_commit(s_ready + half);
-      };
-      auto issue_pv = [&](int half, bool first) {
+            for (int k = 0; k < HD / 16; ++k)          // (the kind::f16 MMA; the descriptor says f16)
+              tc_mma_bf16(tmem + half * 128, a + ((k >> 2) * 1024 + (k & 3) * 2), b + ((k >> 2) * 1024 + (k & 3) * 2),
+                          id_s, k ? 1u : 0u);
+            tc_commit(s_ready + half);
+          }
+          __syncwarp();
+        };
+        auto issue_pv = [&](int half, bool first) {
+          const uint64_t b = vd + (uint64_t)((st_v * T::kHalf) >> 4);
+          const uint32_t d = tmem + T::kO + half * HD, a = tmem + half * 128, acc = first ? 0u : 1u;
+          if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_f16_ts(tmem + T::kO + half * HD, tmem + half * 128 + k * 8,
-                        vd + (uint64_t)((st_v * T::kHalf) >> 4) + (uint64_t)(k * 128), id_o, first && k == 0 ? 0u : 1u);
-      };
-      if (ok) do {
-        const KvSeq s = kv_seq(p, w.it.x);
-        const bool two = (int64_t)s.qn * p.group - (int64_t)w.it.y * kRowsTile > 128;
-        if (!(ok = wait(q_ready, q_seen[0]++ & 1))) break;
-        if (two && !(ok = wait(q_ready + 1, q_seen[1]++ & 1))) break;
-        if (!(ok = wait(k_full + st_k, ph_k))) break;
-        tc_fence_after();
-        issue_s(0);
-        if (two) issue_s(1);
-        tc_commit(k_empty + st_k);
-        if (++st_k == S) {
-          st_k = 0;
-          ph_k ^= 1;
-        }
-        for (int j = w.j0; j < w.j1; ++j) {
-          const bool more = j + 1 < w.j1;
-          if (!(ok = wait(v_full + st_v, ph_v))) break;
-          if (!(ok = wait(p_ready, p_seen[0]++ & 1))) break;
+            for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, a + k * 8, b + k * 128, id_o, k ? 1u : acc);
+          }
+          __syncwarp();
+        };
+        auto commit = [&](uint64_t *bar) {
+          if (elect_one()) tc_commit(bar);
+          __syncwarp();
+        };
+        if (ok) do {
+          const KvSeq s = kv_seq(p, w.it.x);
+          const bool two = (int64_t)s.qn * p.group - (int64_t)w.it.y * kRowsTile > 128;
+          if (!(ok = warp_wait(k_full + st_k, ph_k))) break;
+          if (!(ok = warp_wait(q_ready, q_seen[0]++ & 1))) break;
           tc_fence_after();
-          issue_pv(0, j == w.j0);
-          if (more) {
-            if (!(ok = wait(k_full + st_k, ph_k))) break;
-            tc_fence_after();
-            issue_s(0);
-          } else {
-            tc_commit(o_full);
-          }
+          issue_s(0);
           if (two) {
-            if (!(ok = wait(p_ready + 1, p_seen[1]++ & 1))) break;
+            if (!(ok = warp_wait(q_ready + 1, q_seen[1]++ & 1))) break;
             tc_fence_after();
-            issue_pv(1, j == w.j0);
-            if (more)
-              issue_s(1);
-            else
-              tc_commit(o_full + 1);
+            issue_s(1);
           }
-          tc_commit(v_empty + st_v);
-          if (++st_v == S) {
-            st_v = 0;
-            ph_v ^= 1;
+          commit(k_empty + st_k);
+          if (++st_k == S) {
+            st_k = 0;
+            ph_k ^= 1;
           }
-          if (more) {
-            tc_commit(k_empty + st_k);
-            if (++st_k == S) {
-              st_k = 0;
-              ph_k ^= 1;
+          for (int j = w.j0; j < w.j1; ++j) {
+            const bool more = j + 1 < w.j1;
+            if (!(ok = warp_wait(v_full + st_v, ph_v))) break;
+            if (!(ok = warp_wait(p_ready, p_seen[0]++ & 1))) break;
+            tc_fence_after();
+            issue_pv(0, j == w.j0);
+            if (more) {
+              if (!(ok = warp_wait(k_full + st_k, ph_k))) break;
+              tc_fence_after();
+              issue_s(0);
+            } else {
+              commit(o_full);
+            }
+            if (two) {
+              if (!(ok = warp_wait(p_ready + 1, p_seen[1]++ & 1))) break;
+              tc_fence_after();
+              issue_pv(1, j == w.j0);
+              if (more)
+                issue_s(1);
+              else
+                commit(o_full + 1);
+            }
+            commit(v_empty + st_v);
+            if (++st_v == S) {
+              st_v = 0;
+              ph_v ^= 1;
+            }
+            if (more) {
+              commit(k_empty + st_k);
+              if (++st_k == S) {
+                st_k = 0;
+                ph_k ^= 1;
+              }
             }
           }
-        }
-        if (!ok) break;
-      } while (w.next(p));
-      // every MMA issued here completes before tensor memory is freed
-      tc_commit(drain);
-      mbar_wait(drain, 0, kKvDrainNs);
+          if (!ok) break;
+        } while (w.next(p));
+        // every MMA issued here completes before tensor memory is freed
+        commit(drain);
+        mbar_wait(drain, 0, kKvDrainNs);
+      }
     }
     __syncwarp();
   }
@@ -687,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-// Segments that lie in several spans: block = (border between two spans, 32
+// Segments that lie in several spans: block = (border between two spans, 8
 // rows); the border right behind a segment's first span stands for it.
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv_join(const KvAttnParams p, int ctas) {
@@ -710,7 +817,7 @@ __global__ void __launch_bounds__(256) k_kv_join(const KvAttnParams p, int ctas)
   const KvSeq s = kv_seq(p, it.x);
   const int64_t rows = min((int64_t)s.qn * p.group - (int64_t)it.y * kRowsTile, (int64_t)kRowsTile);
   const int first_slot = pr_start(c0, total, spans) < first ? 1 : 0;
-  for (int r = blockIdx.y * 32 + warp; r < min((int64_t)blockIdx.y * 32 + 32, rows); r += 8) {
+  for (int r = blockIdx.y * 8 + warp; r < rows; r += 8 * gridDim.y) {
     float m = -CUDART_INF_F, l = 0.0f, o[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) o[v] = 0.0f;
@@ -756,7 +863,7 @@ cudaError_t run_prompt(const KvAttnParams &p, int num_sms, cudaStream_t st) {
       e != cudaSuccess)
     return e;
   if (num_sms < 2) return cudaSuccess;
-  return launch_pdl(k_kv_join<HD>, dim3(num_sms - 1, kRowsTile / 32), dim3(256), 0, st, p, num_sms);
+  return launch_pdl(k_kv_join<HD>, dim3(num_sms - 1, kRowsTile / 8), dim3(256), 0, st, p, num_sms);
 }
 
 }  // namespace
