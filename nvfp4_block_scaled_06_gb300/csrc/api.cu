@@ -1894,7 +1894,7 @@ struct KvAttnPlan {
   bool prompt = false;                 // some sequence may have more rows
   int64_t *prefix = nullptr, *item_prefix = nullptr, max_items = 0;
   float *part_o = nullptr, *part_ml = nullptr, *pr_part_o = nullptr, *pr_part_ml = nullptr;
-  int4 *items = nullptr;
+  int4 *items = nullptr, *borders = nullptr;
   int *item_count = nullptr;
 };
 
@@ -1918,6 +1918,7 @@ void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
     pl->items = c.take<int4>((size_t)pl->max_items * sizeof(int4));
     pl->item_prefix = c.take<int64_t>((size_t)(pl->max_items + 1) * 8);
     pl->item_count = c.take<int>(4);
+    pl->borders = c.take<int4>((size_t)sms * sizeof(int4));
     pl->pr_part_o = c.take<float>(slots * (size_t)hd * 4);
     pl->pr_part_ml = c.take<float>(slots * 8);
   }
@@ -1982,6 +1983,7 @@ nvfp4_status run_kv_attention(const nvfp4_kv_attention_args *a, const KvAttnPlan
   p.items = pl.items;
   p.item_prefix = pl.item_prefix;
   p.item_count = pl.item_count;
+  p.borders = pl.borders;
   p.max_items = pl.max_items;
   p.pr_part_o = pl.pr_part_o;
   p.pr_part_ml = pl.pr_part_ml;

@@ -328,6 +328,7 @@ struct KvAttnParams {
   int4 *items;                       // [max_items]: the prompt kernel's row tiles
   int64_t *item_prefix;              // [max_items + 1]: key tiles before an item
   int *item_count;
+  int4 *borders;                     // [ctas]: {item or -1, head, last span, slot of the first} at a span's start
   int64_t max_items;
   float *pr_part_o, *pr_part_ml;     // the prompt kernel's partial results
   int *status;

@@ -4,9 +4,9 @@
 // The product's rows are (new token, query head of the group) of one sequence
 // and key-value head, 256 to a tile (two M = 128 halves), its keys come 128 at a
 // time:  S = Q K^T (f16 operands, exact K, q scaled by a power of two per row),
-// P = exp2(S - m), O += P V, m a running reference of the row as in the kernel
-// for few rows: it is raised, and O and l rescaled, only when a numerator would
-// exceed 2^8.
+// P = exp2(S - m), O += P V, m a running reference of the row: its first keys'
+// maximum, raised, with O and l rescaled, when a step's numerators sum to more
+// than 2^10, and within a step before one would leave f16.
 //
 // Bound: the tensor cores, 4 x 128 x 256 x head_dim operations per step and 4096
 // multiply-adds a cycle; next to them 32768 exponentials (32 a cycle) and the
@@ -16,8 +16,7 @@
 //   8-11      a thread per key: packed row -> f16 row in the swizzled K or V
 //             tile (a cached value is decoded once per 256 rows)
 //   12        issues the MMAs: P V of one half and S of its next step while the
-//             softmax of the other half runs (13-15 idle: registers move by
-//             warpgroup)
+//             softmax of the other half runs
 // V's tile lies as K's does, a key per row; it enters as the transposed operand.
 //
 // Work: the steps of all (row tile, head) segments in one line, cut into equal
@@ -38,11 +37,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kRowsTile = 256;
-constexpr int kThreads = 16 * 32;
-// Registers per thread of the three kinds of warpgroups (softmax twice): as many as the launch's 512 x 128.
-constexpr int kRegsSoftmax = 184, kRegsTiles = 88, kRegsMma = 56;
-static_assert(128 * (2 * kRegsSoftmax + kRegsTiles + kRegsMma) == kThreads * 128, "");
-constexpr float kRaiseBy = 8.0f;
+constexpr int kThreads = 13 * 32;
+constexpr float kRaiseSum = 1024.0f;  // of a tile's numerators, beyond which the next raises the reference
+constexpr int kTwo = 1 << 30;       // in an item's key tiles: it has rows in both halves
+constexpr int kOver = 3;            // what a segment costs beside its key tiles, in key tiles
 constexpr uint64_t kKvDrainNs = 200000000ull;
 
 template <int HD>
@@ -50,7 +48,8 @@ struct Pr {
   static constexpr int kStages = HD == 128 ? 2 : 3;   // of K and of V
   static constexpr int kHalf = 128 * HD * 2;          // 128 f16 rows: Q of one half, a K or V tile
   static constexpr int kO = 256;                      // first column of O in tensor memory (S: 0 and 128)
-  static constexpr size_t kSmem = (size_t)(2 + 2 * kStages) * kHalf + 1024;
+  static constexpr int kStaging = 16384;              // results of one half on their way out, 128 bytes a row
+  static constexpr size_t kSmem = (size_t)(2 + 2 * kStages) * kHalf + 2 * kStaging + 1024;
 };
 
 // Instruction descriptor: kind::f16 with f16 A and B, fp32 D; tb: B is MN-major.
@@ -67,6 +66,8 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t a, uint32_t chunk) {
   d |= (uint64_t)2 << 61;
   return d;
 }
+// K-major operand, 128-byte swizzle (sdesc_k_sw128 on a shared-memory address).
+__device__ __forceinline__ uint64_t sdesc_k_sw128_u(uint32_t a) { return sdesc_mn_sw128(a, 16); }
 // D(tmem) (+)= A(tmem) * B(smem), f16.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
                                               uint32_t accumulate) {
@@ -104,13 +105,11 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r)::"memory");
   return r != 0;
 }
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]),
+                 "+r"(x[15])::"memory");
 }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
@@ -127,12 +126,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 __device__ __forceinline__ int64_t pr_start(int64_t c, int64_t total, int64_t spans) { return c * total / spans; }
 __device__ __forceinline__ int64_t pr_owner(int64_t u, int64_t total, int64_t spans) {
   return ((u + 1) * spans - 1) / total;
@@ -198,7 +191,9 @@ __global__ void __launch_bounds__(1024) k_kv_list(const KvAttnParams p) {
         const int64_t end = p.causal ? (int64_t)s.n - s.qt + tok1 + 1 : s.n;
         const int t0 = (int)(max(min(first, (int64_t)s.n - 1), (int64_t)0) >> 7);
         nt = max((int64_t)1, ((end + 127) >> 7) - t0);
-        it = make_int4(b0 + lo, tile, t0, (int)nt);
+        const bool two = (int64_t)s.qn * p.group - (int64_t)tile * kRowsTile > 128;
+        it = make_int4(b0 + lo, tile, t0, (int)nt | (two ? kTwo : 0));
+        nt += kOver;
       }
       const int64_t u = scan(nt, sum);
       // (offsets that make sequences share rows can name more tiles than there are rows for: those are dropped)
@@ -230,21 +225,38 @@ __device__ __forceinline__ int find_item(const int64_t *prefix, int count, int64
   return lo;
 }
 
-// A CTA's way through the segments of its span.
+// A CTA's way through the segments of its span.  A segment counts as its key
+// tiles and kOver more in front, for what it costs beside them.
 struct Walk {
   int item, h, j0, j1;      // key tiles [j0, j1) of the segment's
-  int4 it;
-  int64_t left;             // units of the span from j0 on
-  __device__ __forceinline__ void clip() { j1 = (int)min((int64_t)it.w, j0 + left); }
+  int seq, tile, t0, nt;    // the item: sequence, row tile, first key tile, key tiles
+  int left, r;              // units of the span from the segment's place r on
+  bool two;                 // rows in both halves
+  __device__ __forceinline__ void load(const KvAttnParams &p) {
+    const int4 it = __ldg(p.items + item);
+    seq = it.x;
+    tile = it.y;
+    t0 = it.z;
+    nt = it.w & (kTwo - 1);
+    two = (it.w & kTwo) != 0;
+  }
+  __device__ __forceinline__ void clip() {
+    j0 = max(r - kOver, 0);
+    j1 = max(min(nt, r + left - kOver), 0);
+  }
+  // On to the next segment with a key tile in the span.
   __device__ __forceinline__ bool next(const KvAttnParams &p) {
-    left -= j1 - j0;
-    if (left <= 0) return false;
-    if (++h == p.kv_heads) {
-      h = 0;
-      it = __ldg(p.items + ++item);
-    }
-    j0 = 0;
-    clip();
+    do {
+      left -= nt + kOver - r;
+      if (left <= 0) return false;
+      if (++h == p.kv_heads) {
+        h = 0;
+        ++item;
+        load(p);
+      }
+      r = 0;
+      clip();
+    } while (j0 >= j1);
     return true;
   }
 };
@@ -255,31 +267,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
   using T = Pr<HD>;
   constexpr int S = T::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * S + 2 * S + 8 + 2];
+  __shared__ __align__(8) uint64_t bars[4 * S + 10];
   __shared__ uint32_t tmem_holder;
   __shared__ uint32_t kmask[4][4];          // keys that exist, of the last four tiles
   __shared__ volatile int abort_flag, nan_flag;
-  uint64_t *k_full = bars, *k_empty = bars + S, *v_full = bars + 2 * S, *v_empty = bars + 3 * S;
-  uint64_t *s_ready = bars + 4 * S, *p_ready = s_ready + 2, *o_full = s_ready + 4, *q_ready = s_ready + 6;
-  uint64_t *drain = s_ready + 8, *never = s_ready + 9;
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // barriers and buffers by their shared-memory addresses
+  const uint32_t bar = smem_u32(bars);
+  const uint32_t k_full = bar, k_empty = bar + 8 * S, v_full = bar + 16 * S, v_empty = bar + 24 * S;   // (empty 8 S behind full)
+  const uint32_t s_ready = bar + 32 * S, p_ready = s_ready + 16, o_full = s_ready + 32, q_ready = s_ready + 48;
+  const uint32_t drain = s_ready + 64, never = s_ready + 72;
+  const uint32_t smem = (smem_u32(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(k_full + i, 4);
-      mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, 4);
-      mbar_init(v_empty + i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_ready + i, 1);
-      mbar_init(p_ready + i, 128);
-      mbar_init(o_full + i, 1);
-      mbar_init(q_ready + i, 128);
-    }
-    mbar_init(drain, 1);
-    mbar_init(never, 1);
+    for (int i = 0; i < 4 * S; ++i) mbar_init(bars + i, (i / S) & 1 ? 1 : 4);   // full: four warps, empty: a commit
+    for (int i = 0; i < 8; ++i) mbar_init(bars + 4 * S + i, (i >> 1) & 1 ? 128 : 1);   // p, q: a half's threads
+    mbar_init(bars + 4 * S + 8, 1);
+    mbar_init(bars + 4 * S + 9, 1);
     abort_flag = 0;
     nan_flag = 0;
     fence_barrier_init();
@@ -300,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
     record_timeout(p.status);
   };
   // every lane of a warp agrees on whether the wait ended
-  auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait(bar, parity, p.timeout_ns));
+  auto warp_wait = [&](uint32_t at, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait_u(at, parity, p.timeout_ns));
     if (!ok && lane == 0) give_up();
     return ok;
   };
@@ -309,41 +313,73 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
   const int count = *p.item_count;
   const int64_t total = count > 0 ? p.item_prefix[count] * p.kv_heads : 0;
   const int64_t spans = min((int64_t)gridDim.x, total), cta = blockIdx.x;
-  if (cta < spans) {
+  if (cta < spans && note_bounds(tmem == 0, p.status)) {
     Walk w;
+    bool any;
     {
       const int64_t u0 = pr_start(cta, total, spans);
-      w.left = pr_start(cta + 1, total, spans) - u0;
+      w.left = (int)(pr_start(cta + 1, total, spans) - u0);
       w.item = find_item(p.item_prefix, count, u0 / p.kv_heads);
       // (prefix counts the units of one head: item i's lie from prefix[i] * kv_heads on)
-      w.it = __ldg(p.items + w.item);
-      const int64_t r = u0 - p.item_prefix[w.item] * p.kv_heads;
-      w.h = (int)(r / w.it.w);
-      w.j0 = (int)(r - (int64_t)w.h * w.it.w);
+      w.load(p);
+      const int64_t base = p.item_prefix[w.item] * p.kv_heads;
+      w.h = (int)((u0 - base) / (w.nt + kOver));
+      const int64_t first = base + (int64_t)w.h * (w.nt + kOver);
+      w.r = (int)(u0 - first);
       w.clip();
+      // the first border inside a segment stands for it in the joining kernel
+      if (tid == 0) {
+        const int64_t c0 = pr_owner(first + kOver, total, spans);
+        p.borders[cta] = make_int4(w.j0 > 0 && c0 == cta - 1 ? w.item : -1, w.h,
+                                   (int)pr_owner(first + w.nt + kOver - 1, total, spans),
+                                   pr_start(c0, total, spans) < first ? 1 : 0);
+      }
+      any = w.j0 < w.j1 || w.next(p);
     }
-    if (warp < 8) {
+    if (!any) {
+    } else if (warp < 8) {
       // -------------------------------------------------------------- softmax --
-      regs_up<kRegsSoftmax>();
       const int half = warp >> 2, row = (warp & 3) * 32 + lane;     // of the half
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_col = tmem + lane_off + half * 128, o_col = tmem + lane_off + T::kO + half * HD;
-      uint8_t *sq = smem + half * T::kHalf;
       uint32_t tiles = 0, segs = 0, steps = 0;      // key tiles passed; segments and steps of this half
       bool first_seg = true, ok = true;
-      do {
-        const KvSeq s = kv_seq(p, w.it.x);
-        const int64_t rows = (int64_t)s.qn * p.group - (int64_t)w.it.y * kRowsTile;
-        if (rows <= half * 128) {                    // nothing in this half
-          tiles += w.j1 - w.j0;
-          first_seg = false;
-          continue;
+      const uint32_t sq = smem + half * T::kHalf + (warp & 3) * 32 * 128;   // this warp's rows of Q
+      // A segment as this thread sees it.
+      KvSeq s;
+      int tok, head;
+      int64_t rows;
+      auto open = [&] {
+        s = kv_seq(p, w.seq);
+        rows = (int64_t)s.qn * p.group - (int64_t)w.tile * kRowsTile - half * 128;   // of this half
+        const uint32_t grp = p.group, at = (uint32_t)((int64_t)w.tile * kRowsTile % p.group) + half * 128 + row;
+        tok = (int)((int64_t)w.tile * kRowsTile / p.group + at / grp);
+        head = w.h * p.group + (int)(at % grp);
+      };
+      // Its bf16 rows of Q into the buffer, 16-byte runs of a row on consecutive lanes; rows past the last are zero.
+      auto ask_q = [&] {
+        if (rows > 0) {
+          constexpr int kL = HD / 8, kR = 32 / kL;
+          const int c = lane % kL;
+          const int64_t own = (int64_t)(s.q0 + tok) * p.q_ld + (int64_t)head * p.q_head_ld;
+#pragma unroll 4
+          for (int i = 0; i < 32 / kR; ++i) {
+            const int rw = i * kR + lane / kL;
+            const int64_t at = __shfl_sync(0xffffffffu, own, rw);
+            const bool in = (warp & 3) * 32 + rw < rows;
+            cp_async_16(sq + rw * 128 + (c >> 3) * 16384 + (((c & 7) ^ (rw & 7)) << 4),
+                        p.q + (in ? at + c * 8 : 0), in ? 16u : 0u);
+          }
         }
-        const bool live = half * 128 + row < rows;
-        // row r of the tile: token tok0 + (rem0 + r) / group, head (rem0 + r) % group of the group
-        const int tok0 = (int)((int64_t)w.it.y * kRowsTile / p.group);
-        const uint32_t rem0 = (uint32_t)((int64_t)w.it.y * kRowsTile % p.group) + half * 128, grp = p.group;
-        const int tok = tok0 + (int)((rem0 + row) / grp), head = w.h * p.group + (int)((rem0 + row) % grp);
+        cp_async_commit();
+      };
+      open();
+      ask_q();
+      do {
+        if (rows <= 0) {                             // nothing in this half
+          tiles += w.j1 - w.j0;
+        } else {
+        const bool live = row < rows;
         // the keys [see_lo, see_hi) of this row; rows past the last see all and hold zeros
         int see_lo = 0, see_hi = 0x7FFFFFFF;
         if (live) {
@@ -352,156 +388,162 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           if (p.window > 0) see_lo = (int)max((int64_t)0, pos + 1 - p.window);
         }
         const int all_lo = __reduce_max_sync(0xffffffffu, see_lo), all_hi = __reduce_min_sync(0xffffffffu, see_hi);
-        // Q: 16-byte runs of a row on consecutive lanes; a row's lanes agree on its power of two
-        float sc = 0.0f;
-        {
-          constexpr int kL = HD / 8, kR = 32 / kL;   // lanes of a row, rows at a time
-          const float gsc = p.scale_log2 * p.gk[w.h];
-          const int c = lane % kL;
-          const int64_t own = (int64_t)(s.q0 + tok) * p.q_ld + (int64_t)head * p.q_head_ld;
-          uint4 v[32 / kR];
-#pragma unroll
-          for (int i = 0; i < 32 / kR; ++i) {
-            const int src = i * kR + lane / kL;
-            const int64_t at = __shfl_sync(0xffffffffu, own, src);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (half * 128 + (warp & 3) * 32 + src < rows) v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + at) + c);
-          }
-#pragma unroll
-          for (int i = 0; i < 32 / kR; ++i) {
-            const int rw = (warp & 3) * 32 + i * kR + lane / kL;
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t m2 = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
-                                   __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
-#pragma unroll
-            for (int o = 1; o < kL; o <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
-            const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7);
-            // a power of two that brings the row's maximum to [2^13, 2^14); 1 for rows with an infinity or a NaN
-            const int up = e == 255 ? 127 : min(267 - e, 190);
-            const float mul = __uint_as_float((uint32_t)up << 23);
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = pack_h2(bf16lo(x[k]) * mul, bf16hi(x[k]) * mul);
-            sts128(smem_u32(sq) + rw * 128 + (c >> 3) * 16384 + (((c & 7) ^ (rw & 7)) << 4), h[0], h[1], h[2], h[3]);
-            const int back = __shfl_sync(0xffffffffu, 254 - up, lane % kR * kL);
-            if (lane / kR == i) sc = fmaxf(__uint_as_float((uint32_t)back << 23) * gsc, FLT_MIN);
-          }
+        // this thread's row to f16, times a power of two that brings its maximum to [2^13, 2^14) (1 for a row with
+        // an infinity or a NaN)
+        cp_async_wait<0>();
+        __syncwarp();
+        const uint32_t mine = sq + lane * 128, xr = (lane & 7) << 4;
+        uint32_t m2 = 0;
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+          const uint4 v = lds128(mine + (c >> 3) * 16384 + (((c & 7) << 4) ^ xr));
+          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
+        const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), up = e == 255 ? 127 : min(267 - e, 190);
+        const float mul = __uint_as_float((uint32_t)up << 23);
+        const float sc = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * (p.scale_log2 * p.gk[w.h]), FLT_MIN);
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+          const uint32_t at = mine + (c >> 3) * 16384 + (((c & 7) << 4) ^ xr);
+          const uint4 v = lds128(at);
+          sts128(at, pack_h2(bf16lo(v.x) * mul, bf16hi(v.x) * mul), pack_h2(bf16lo(v.y) * mul, bf16hi(v.y) * mul),
+                 pack_h2(bf16lo(v.z) * mul, bf16hi(v.z) * mul), pack_h2(bf16lo(v.w) * mul, bf16hi(v.w) * mul));
         }
         fence_proxy_async_shared();
         tc_fence_before();
-        mbar_arrive(q_ready + half);
-        {
-          // the next segment's row of Q on its way to L2
-          Walk nx = w;
-          if (nx.next(p)) {
-            const KvSeq s2 = kv_seq(p, nx.it.x);
-            const int64_t r2 = (int64_t)nx.it.y * kRowsTile + half * 128 + row;
-            if (r2 < (int64_t)s2.qn * p.group) {
-              const __nv_bfloat16 *src = p.q + (s2.q0 + r2 / p.group) * p.q_ld +
-                                         (nx.h * p.group + r2 % p.group) * p.q_head_ld;
-#pragma unroll
-              for (int i = 0; i < HD; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
-            }
-          }
-        }
+        mbar_arrive_u(q_ready + 8 * half);
         float m = -CUDART_INF_F, l = 0.0f;
+        float last = 0.0f;                           // the last tile's sum of numerators
         for (int j = w.j0; j < w.j1; ++j, ++tiles, ++steps) {
-          if (!(ok = warp_wait(s_ready + half, steps & 1))) break;
+          if (!(ok = warp_wait(s_ready + 8 * half, steps & 1))) break;
           tc_fence_after();
-          const int key0 = (w.it.z + j) * 128;
+          const int key0 = (w.t0 + j) * 128;
           const uint32_t *km = kmask[tiles & 3];
           const bool whole = key0 >= all_lo && key0 + 128 <= all_hi && (km[0] & km[1] & km[2] & km[3]) == 0xFFFFFFFFu;
-          // -inf where the row does not see a key, of the 32 from chunk c on
-          auto mask = [&](int c, uint32_t (&x)[32]) {
-            if (whole) return;
-            // of the row's range: the bits from its first key on and below its last
-            const int from = min(max(see_lo - key0 - c * 32, 0), 32), to = min(max(see_hi - key0 - c * 32, 0), 32);
-            const uint32_t bits = km[c] & (uint32_t)((1ull << to) - 1) & ~(uint32_t)((1ull << from) - 1);
+          if (!whole) {                              // -inf where the row does not see a key
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              // of the row's range: the bits from its first key on and below its last
+              const int from = min(max(see_lo - key0 - c * 32, 0), 32), to = min(max(see_hi - key0 - c * 32, 0), 32);
+              const uint32_t bits = km[c] & (uint32_t)((1ull << to) - 1) & ~(uint32_t)((1ull << from) - 1);
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(s_col + c * 32, x);
+              tmem_ld_wait_for(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = bits & (1u << i) ? x[i] : 0xFF800000u;
+              for (int i = 0; i < 32; ++i) x[i] = bits & (1u << i) ? x[i] : 0xFF800000u;
+              tmem_st_x32(s_col + c * 32, x);
+            }
+            tmem_st_wait();
+          }
+          // O and l follow a raised reference: times f, a power of two (or 0 for a first maximum)
+          auto rescale = [&](float f) {
+            l *= f;
+            if (j == w.j0) return;                   // O starts with this tile
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(o_col + c * 32, x);
+              tmem_ld_wait_for(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+              tmem_st_x32(o_col + c * 32, x);
+            }
+            tmem_st_wait();
           };
-          uint32_t pk[64];
-          float sum;
-          bool scan = __any_sync(0xffffffffu, m == -CUDART_INF_F);
-          while (true) {
-            if (scan) {
+          // numerators are not negative, so a tile's sum bounds them
+          const bool fresh = m == -CUDART_INF_F, over = last > kRaiseSum;
+          if (__any_sync(0xffffffffu, fresh || over)) {
+            float f = 1.0f;
+            if (__any_sync(0xffffffffu, fresh)) {
               float mx = -CUDART_INF_F;
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 uint32_t x[32];
                 tmem_ld_32x32b_x32(s_col + c * 32, x);
                 tmem_ld_wait_for(x);
-                mask(c, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
               }
-              mx *= sc;
-              const bool up = mx > m + kRaiseBy;
-              const float f = up ? ex2(m - mx) : 1.0f;
-              if (up) m = mx;
-              l *= f;
-              if (j > w.j0 && __any_sync(0xffffffffu, up)) {
+              if (fresh && mx > -CUDART_INF_F) {
+                m = ceilf(mx * sc);
+                f = 0.0f;
+              }
+            }
+            if (!fresh && over) {                    // by the last tile's sum, to a power of two
+              const int e = (int)(__float_as_uint(last) >> 23) - 126;     // (at most 2^16 a tile: below 17)
+              m += (float)e;
+              f = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+            }
+            rescale(f);
+          }
+          float ref = m == -CUDART_INF_F ? 0.0f : m;
+          const uint64_t sc2 = pack2(sc, sc);
+          float sum = 0.0f;
+          uint32_t x[32], pk[16];
+          // a chunk's numerators, two to a word, and their sum
+          auto numerators = [&] {
+            const uint64_t ref2 = pack2(-ref, -ref);
+            uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t y = fma2(((uint64_t)x[2 * i + 1] << 32) | x[2 * i], sc2, ref2);
+              const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
+              acc[i & 3] = add2(acc[i & 3], pack2(e0, e1));
+              pk[i] = pack_h2(e0, e1);
+            }
+            acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+            return lo2(acc[0]) + hi2(acc[0]);
+          };
 #pragma unroll 1
-                for (int c = 0; c < HD / 32; ++c) {
-                  uint32_t x[32];
-                  tmem_ld_32x32b_x32(o_col + c * 32, x);
-                  tmem_ld_wait_for(x);
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_32x32b_x32(s_col + c * 32, x);
+            tmem_ld_wait_for(x);
+            float part = numerators();
+            if (__any_sync(0xffffffffu, part > 65504.0f)) {
+              // A numerator may be beyond f16 (2^16 times the reference's): the row's reference is raised to this
+              // chunk's largest score, O, l and the numerators written before follow, and the chunk is done again.
+              float mx = -CUDART_INF_F;
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                  tmem_st_x32(o_col + c * 32, x);
-                }
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
+              const float e = part > 65504.0f ? fmaxf(ceilf(mx * sc - m), 0.0f) : 0.0f;
+              const float f = e < 127.0f ? __uint_as_float((uint32_t)(127 - (int)e) << 23) : 0.0f;
+              m += e;
+              ref = m == -CUDART_INF_F ? 0.0f : m;
+              rescale(f);
+              sum *= f;
+              const uint32_t f2 = pack_h2(f, f);
+#pragma unroll 1
+              for (int d = 0; d < c; ++d) {
+                uint32_t y[16];
+                tmem_ld_32x32b_x16(s_col + d * 16, y);
+                tmem_ld_wait_for(y);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = hmul2(y[i], f2);
+                tmem_st_32x32b_x16(s_col + d * 16, y);
               }
+              part = numerators();
             }
-            const float ref = m == -CUDART_INF_F ? 0.0f : m;
-            const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(-ref, -ref);
-            uint64_t acc[2] = {0, 0};
-            uint32_t top = 0;
-            uint32_t buf[2][32];
-            tmem_ld_32x32b_x32(s_col, buf[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t (&x)[32] = buf[c & 1];
-              tmem_ld_wait_for(x);
-              if (c < 3) tmem_ld_32x32b_x32(s_col + (c + 1) * 32, buf[(c + 1) & 1]);
-              mask(c, x);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint64_t y = fma2(((uint64_t)x[2 * i + 1] << 32) | x[2 * i], sc2, ref2);
-                const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
-                acc[i & 1] = add2(acc[i & 1], pack2(e0, e1));
-                pk[c * 16 + i] = pack_h2(e0, e1);
-                top = hmax2(top, pk[c * 16 + i]);
-              }
-            }
-            sum = (lo2(acc[0]) + hi2(acc[0])) + (lo2(acc[1]) + hi2(acc[1]));
-            // f16 256 = 0x5C00; numerators are not negative, so their bits are in order
-            const bool over = max(top & 0xFFFFu, top >> 16) > 0x5C00u;
-            if (scan || !__any_sync(0xffffffffu, over)) break;
-            scan = true;
+            sum += part;
+            tmem_st_32x32b_x16(s_col + c * 16, pk);
           }
           l += sum;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = pk[c * 32 + i];
-            tmem_st_x32(s_col + c * 32, x);
-          }
+          last = sum;
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(p_ready + half);
+          mbar_arrive_u(p_ready + 8 * half);
         }
         if (!ok) break;
-        if (!(ok = warp_wait(o_full + half, segs & 1))) break;
+        if (!(ok = warp_wait(o_full + 8 * half, segs & 1))) break;
         tc_fence_after();
         ++segs;
 
         // A value row with a NaN scale entered the sums as zeros; the rows that see it get their NaN here.
         uint32_t nan_blocks = 0;
         if (nan_flag && live) {
-          const int k0 = max((w.it.z + w.j0) * 128, see_lo), k1 = min(min((w.it.z + w.j1) * 128, see_hi), s.n);
+          const int k0 = max((w.t0 + w.j0) * 128, see_lo), k1 = min(min((w.t0 + w.j1) * 128, see_hi), s.n);
           for (int k = k0; k < k1; ++k) {
-            const int id = __ldg(p.table + (int64_t)w.it.x * p.table_ld + (k >> p.page_shift));
+            const int id = __ldg(p.table + (int64_t)w.seq * p.table_ld + (k >> p.page_shift));
             if (id < 0 || id >= p.num_pages) continue;
             const uint8_t *sf = p.v_sf + id * p.sf_stride +
                                 (((int64_t)w.h << p.page_shift) + (k & ((1 << p.page_shift) - 1))) * (HD / 16);
@@ -509,85 +551,79 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
               if ((__ldg(sf + i) & 0x7Fu) == 0x7Fu) nan_blocks |= 1u << i;
           }
         }
-        const bool full = w.j0 == 0 && w.j1 == w.it.w;
+        const bool full = w.j0 == 0 && w.j1 == w.nt;
         const int64_t prow = (2 * cta + (first_seg ? 0 : 1)) * kRowsTile + half * 128 + row;
-        // 256 bytes of each of the warp's rows at a time go through its rows of Q, which no MMA reads any more
-        // (o_full), so that 16 lanes write one row; own: this thread's row of the destination in 16-byte runs
-        const uint32_t stage = smem_u32(sq) + (warp & 3) * 32 * 128;
-        auto put = [&](int q, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-          sts128(stage + lane * 128 + (q >> 3) * 16384 + (((q & 7) ^ (lane & 7)) << 4), a0, a1, a2, a3);
-        };
-        auto flush = [&](auto width, uint4 *base, int64_t own) {
-          constexpr int kL = decltype(width)::value / 16, kR = 32 / kL;   // lanes of a row, rows at a time
-          const int q = lane % kL;
-          uint4 v[32 / kR];
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 32 / kR; ++i) {
-            const int rw = i * kR + lane / kL;
-            v[i] = lds128(stage + rw * 128 + (q >> 3) * 16384 + (((q & 7) ^ (rw & 7)) << 4));
-          }
-#pragma unroll
-          for (int i = 0; i < 32 / kR; ++i) {
-            const int rw = i * kR + lane / kL;
-            const int64_t at = __shfl_sync(0xffffffffu, own, rw);
-            if (half * 128 + (warp & 3) * 32 + rw < rows) base[at + q] = v[i];
-          }
-          __syncwarp();
-        };
-        auto nans = [&](int c, uint32_t (&x)[32]) {      // columns 32 c ...
-          if (!__any_sync(0xffffffffu, nan_blocks != 0)) return;
-          const uint32_t nb = nan_blocks >> (2 * c);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (nb >> (i >> 4)) & 1u ? 0x7FC00000u : x[i];
-        };
-        if (full) {
-          const float f = l == 0.0f ? 0.0f : p.gv[w.h] / l;
-#pragma unroll
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld_32x32b_x32(o_col + c * 32, x);
-            tmem_ld_wait_for(x);
-            nans(c, x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t h[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                h[k] = pack_bf2(__uint_as_float(x[8 * i + 2 * k]) * f, __uint_as_float(x[8 * i + 2 * k + 1]) * f);
-              put(4 * c + i, h[0], h[1], h[2], h[3]);
-            }
-          }
-          flush(std::integral_constant<int, HD * 2>(), reinterpret_cast<uint4 *>(p.out),
-                ((int64_t)(s.q0 + tok) * p.out_ld + (int64_t)head * p.out_head_ld) / 8);
-          if (live && p.lse)
-            p.lse[(int64_t)(s.q0 + tok) * p.kv_heads * p.group + head] = (m + __log2f(l)) * CUDART_LN2_F;
-        } else {
-          constexpr int kCols = HD / 2;                  // of a round: 2 HD bytes of a row
+        // 128 bytes of each row at a time, through shared memory, so that eight lanes write one row; base: this
+        // thread's row of the destination
+        const int64_t base = full ? ((int64_t)(s.q0 + tok) * p.out_ld + (int64_t)head * p.out_head_ld) * 2
+                                  : prow * HD * 4;
+        uint8_t *dst = full ? reinterpret_cast<uint8_t *>(p.out) : reinterpret_cast<uint8_t *>(p.pr_part_o);
+        const float f = !full ? 1.0f : l == 0.0f ? 0.0f : p.gv[w.h] / l;
+        const uint32_t stage = smem + (2 + 2 * S) * T::kHalf + half * T::kStaging + (warp & 3) * 32 * 128;
+        const int64_t rows_now = rows;
+        if (live && !full) *reinterpret_cast<float2 *>(p.pr_part_ml + prow * 2) = make_float2(m, l);
+        if (live && full && p.lse)
+          p.lse[(int64_t)(s.q0 + tok) * p.kv_heads * p.group + head] = (m + __log2f(l)) * CUDART_LN2_F;
+        // the next segment's Q meanwhile (no MMA reads this one's any more)
+        first_seg = false;
+        const bool more = w.next(p);
+        if (more) {
+          open();
+          ask_q();
+        }
+        const int cols = full ? 64 : 32;             // of a round
+        const uint32_t put = stage + lane * 128, xl = (lane & 7) << 4;
 #pragma unroll 1
-          for (int rd = 0; rd < 2; ++rd) {
+        for (int c0 = 0; c0 < HD; c0 += cols) {
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 32) {
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(o_col + c0 + c, x);
+            tmem_ld_wait_for(x);
+            if (__any_sync(0xffffffffu, nan_blocks != 0)) {
+              const uint32_t nb = nan_blocks >> ((c0 + c) >> 4);
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) {
-              uint32_t x[32];
-              tmem_ld_32x32b_x32(o_col + rd * kCols + c * 32, x);
-              tmem_ld_wait_for(x);
-              nans(rd * (kCols / 32) + c, x);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) put(8 * c + i, x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              for (int i = 0; i < 32; ++i) x[i] = (nb >> (i >> 4)) & 1u ? 0x7FC00000u : x[i];
             }
-            flush(std::integral_constant<int, HD * 2>(), reinterpret_cast<uint4 *>(p.pr_part_o) + rd * (HD / 8),
-                  prow * (HD / 4));
+            if (full) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  h[k] = pack_bf2(__uint_as_float(x[8 * i + 2 * k]) * f, __uint_as_float(x[8 * i + 2 * k + 1]) * f);
+                sts128(put + ((((c >> 3) + i) << 4) ^ xl), h[0], h[1], h[2], h[3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sts128(put + ((i << 4) ^ xl), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
           }
-          if (live) *reinterpret_cast<float2 *>(p.pr_part_ml + prow * 2) = make_float2(m, l);
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 8; ++i) {
+            const int rw = i * 4 + (lane >> 3);
+            const uint4 v = lds128(stage + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
+            const int64_t at = __shfl_sync(0xffffffffu, base, rw);
+            if ((warp & 3) * 32 + rw < rows_now)
+              *reinterpret_cast<uint4 *>(dst + at + c0 * (full ? 2 : 4) + (lane & 7) * 16) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
+        if (!more) break;
+        continue;
+        }
         first_seg = false;
-      } while (w.next(p));
+        if (!w.next(p)) break;
+        open();
+        ask_q();
+      } while (true);
+      cp_async_wait<0>();
     } else if (warp < 12) {
       // -------------------------------------------------------- K and V tiles --
-      regs_down<kRegsTiles>();
       const int key_in = tid - 256;                 // this thread's key of a tile
-      const uint32_t sk = smem_u32(smem) + 2 * T::kHalf, sv = sk + S * T::kHalf;
+      const uint32_t sk = smem + 2 * T::kHalf, sv = sk + S * T::kHalf;
       const uint32_t row_off = key_in * 128, sw = key_in & 7;
       struct At {
         int b, h, key, n;
@@ -604,13 +640,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
       auto take = [&] {                             // the next tile of the span
         At t{0, 0, 0, 0, more};
         if (more) {
-          if (a.it.x != ab) {
-            ab = a.it.x;
+          if (a.seq != ab) {
+            ab = a.seq;
             an = kv_seq(p, ab).n;
           }
           t.b = ab;
           t.h = a.h;
-          t.key = (a.it.z + aj) * 128 + key_in;
+          t.key = (a.t0 + aj) * 128 + key_in;
           t.n = an;
           if (++aj == a.j1) {
             more = a.next(p);
@@ -653,33 +689,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
       };
       At t0 = take(), t1 = take();
       int id0 = page_of(t0), id1 = page_of(t1);
-      Row k = read(t0, id0, p.k_codes, p.k_sf);
+      Row cur = read(t0, id0, p.k_codes, p.k_sf);
       uint32_t tiles = 0, phase = 0;
       int st = 0;
-      while (t0.on) {
-        Row v = read(t0, id0, p.v_codes, p.v_sf);
-        const At t2 = take();
-        const int id2 = page_of(t2);
-        if (!warp_wait(k_empty + st, phase ^ 1)) break;
-        const uint32_t have = __ballot_sync(0xffffffffu, k.ok);
-        if (lane == 0) kmask[tiles & 3][warp - 8] = have;
-        write(k, sk + st * T::kHalf);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + st);
-        k = read(t1, id1, p.k_codes, p.k_sf);
-        if (!warp_wait(v_empty + st, phase ^ 1)) break;
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-          if ((((v.s[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if (((v.s[i] >> (8 * y)) & 0x7Fu) == 0x7Fu) v.s[i] &= ~(0xFFu << (8 * y));
-            nan_flag = 1;
+      bool ok = true;
+      while (ok && t0.on) {
+        At t2;
+        int id2;
+#pragma unroll 1
+        for (int val = 0; val < 2; ++val) {         // the tile's keys, then its values: one copy of the code
+          // the row after this one
+          Row nxt = read(val ? t1 : t0, val ? id1 : id0, val ? p.k_codes : p.v_codes, val ? p.k_sf : p.v_sf);
+          if (val == 0) {
+            t2 = take();
+            id2 = page_of(t2);
           }
+          const uint32_t full = (val ? v_full : k_full) + 8 * st;
+          if (!(ok = warp_wait(full + 8 * S, phase ^ 1))) break;
+          if (val == 0) {
+            const uint32_t have = __ballot_sync(0xffffffffu, cur.ok);
+            if (lane == 0) kmask[tiles & 3][warp - 8] = have;
+          } else {
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i) {
+              if ((((cur.s[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (((cur.s[i] >> (8 * y)) & 0x7Fu) == 0x7Fu) cur.s[i] &= ~(0xFFu << (8 * y));
+                nan_flag = 1;
+              }
+            }
+          }
+          write(cur, (val ? sv : sk) + st * T::kHalf);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_u(full);
+          cur = nxt;
         }
-        write(v, sv + st * T::kHalf);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + st);
         t0 = t1;
         t1 = t2;
         id0 = id1;
@@ -692,98 +737,109 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
       }
     } else {
       // ------------------------------------------------------------ MMA issue --
-      regs_down<kRegsMma>();
       // (the whole warp walks and waits, one lane issues)
       if (warp == 12) {
         constexpr uint32_t id_s = idesc_f16(128, 128, 0), id_o = idesc_f16(128, HD, 1);
-        const uint64_t qd = sdesc_k_sw128(smem), kd = sdesc_k_sw128(smem + 2 * T::kHalf);
-        const uint64_t vd = sdesc_mn_sw128(smem_u32(smem) + (2 + S) * T::kHalf, 16384);
-        uint32_t q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
-        int st_k = 0, st_v = 0;
-        uint32_t ph_k = 0, ph_v = 0;
+        const uint64_t qd = sdesc_k_sw128_u(smem), kd = sdesc_k_sw128_u(smem + 2 * T::kHalf);
+        const uint64_t vd = sdesc_mn_sw128(smem + (2 + S) * T::kHalf, 16384);
+        uint32_t q_seen = 0, p_seen = 0;              // phases, a bit for each half
+        int st = 0;                                   // stage of the tile at hand, of K and of V
+        uint32_t ph = 0;
         bool ok = true;
         if (p.stall_probe) ok = warp_wait(never, 0);   // the expiry path under test
-        auto issue_s = [&](int half) {
-          const uint64_t a = qd + (uint64_t)((half * T::kHalf) >> 4), b = kd + (uint64_t)((st_k * T::kHalf) >> 4);
+        // Halves and stages are compile-time constants, and tensor memory, all of it, starts at 0: the MMAs' operands
+        // are constants then, which keeps an issue at a few instructions (with them in registers an MMA took 105
+        // cycles to issue, against 64 to run).
+        auto issue_s = [&](auto half, auto stage) {
+          constexpr int H = decltype(half)::value, K = decltype(stage)::value * (T::kHalf >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)          // (the kind::f16 MMA; the descriptor says f16)
-              tc_mma_bf16(tmem + half * 128, a + ((k >> 2) * 1024 + (k & 3) * 2), b + ((k >> 2) * 1024 + (k & 3) * 2),
-                          id_s, k ? 1u : 0u);
-            tc_commit(s_ready + half);
+              tc_mma_bf16(H * 128, qd + (H * (T::kHalf >> 4) + (k >> 2) * 1024 + (k & 3) * 2),
+                          kd + (K + (k >> 2) * 1024 + (k & 3) * 2), id_s, k ? 1u : 0u);
+            tc_commit_u(s_ready + 8 * H);
           }
           __syncwarp();
         };
-        auto issue_pv = [&](int half, bool first) {
-          const uint64_t b = vd + (uint64_t)((st_v * T::kHalf) >> 4);
-          const uint32_t d = tmem + T::kO + half * HD, a = tmem + half * 128, acc = first ? 0u : 1u;
+        auto issue_pv = [&](auto half, auto stage, bool first) {
+          constexpr int H = decltype(half)::value, V = decltype(stage)::value * (T::kHalf >> 4);
+          const uint32_t acc = first ? 0u : 1u;
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, a + k * 8, b + k * 128, id_o, k ? 1u : acc);
+            for (int k = 0; k < 8; ++k)
+              tc_mma_f16_ts(T::kO + H * HD, H * 128 + k * 8, vd + (V + k * 128), id_o, k ? 1u : acc);
           }
           __syncwarp();
         };
-        auto commit = [&](uint64_t *bar) {
-          if (elect_one()) tc_commit(bar);
+        auto commit = [&](uint32_t at) {
+          if (elect_one()) tc_commit_u(at);
           __syncwarp();
+        };
+        using H0 = std::integral_constant<int, 0>;
+        using H1 = std::integral_constant<int, 1>;
+        // S of a segment's first key tile
+        auto begin = [&](auto stage) {
+          constexpr int K = decltype(stage)::value;
+          if (!warp_wait(k_full + 8 * K, ph) || !warp_wait(q_ready, q_seen & 1)) return false;
+          q_seen ^= 1;
+          tc_fence_after();
+          issue_s(H0(), stage);
+          if (w.two) {
+            if (!warp_wait(q_ready + 8, q_seen >> 1)) return false;
+            q_seen ^= 2;
+            tc_fence_after();
+            issue_s(H1(), stage);
+          }
+          commit(k_empty + 8 * K);
+          return true;
+        };
+        // P V of a tile, S of the next
+        auto step = [&](auto stage, bool first, bool more) {
+          constexpr int V = decltype(stage)::value, K = (V + 1) % S;
+          using Next = std::integral_constant<int, K>;
+          if (!warp_wait(v_full + 8 * V, ph) || !warp_wait(p_ready, p_seen & 1)) return false;
+          p_seen ^= 1;
+          tc_fence_after();
+          issue_pv(H0(), stage, first);
+          if (more) {
+            if (!warp_wait(k_full + 8 * K, K == 0 ? ph ^ 1 : ph)) return false;
+            tc_fence_after();
+            issue_s(H0(), Next());
+          } else {
+            commit(o_full);
+          }
+          if (w.two) {
+            if (!warp_wait(p_ready + 8, p_seen >> 1)) return false;
+            p_seen ^= 2;
+            tc_fence_after();
+            issue_pv(H1(), stage, first);
+            if (more)
+              issue_s(H1(), Next());
+            else
+              commit(o_full + 8);
+          }
+          commit(v_empty + 8 * V);
+          if (more) commit(k_empty + 8 * K);
+          return true;
+        };
+        auto at_stage = [&](auto f) {
+          if (st == 0) return f(std::integral_constant<int, 0>());
+          if (S == 2 || st == 1) return f(std::integral_constant<int, 1>());
+          return f(std::integral_constant<int, S - 1>());
         };
         if (ok) do {
-          const KvSeq s = kv_seq(p, w.it.x);
-          const bool two = (int64_t)s.qn * p.group - (int64_t)w.it.y * kRowsTile > 128;
-          if (!(ok = warp_wait(k_full + st_k, ph_k))) break;
-          if (!(ok = warp_wait(q_ready, q_seen[0]++ & 1))) break;
-          tc_fence_after();
-          issue_s(0);
-          if (two) {
-            if (!(ok = warp_wait(q_ready + 1, q_seen[1]++ & 1))) break;
-            tc_fence_after();
-            issue_s(1);
-          }
-          commit(k_empty + st_k);
-          if (++st_k == S) {
-            st_k = 0;
-            ph_k ^= 1;
-          }
-          for (int j = w.j0; j < w.j1; ++j) {
-            const bool more = j + 1 < w.j1;
-            if (!(ok = warp_wait(v_full + st_v, ph_v))) break;
-            if (!(ok = warp_wait(p_ready, p_seen[0]++ & 1))) break;
-            tc_fence_after();
-            issue_pv(0, j == w.j0);
-            if (more) {
-              if (!(ok = warp_wait(k_full + st_k, ph_k))) break;
-              tc_fence_after();
-              issue_s(0);
-            } else {
-              commit(o_full);
-            }
-            if (two) {
-              if (!(ok = warp_wait(p_ready + 1, p_seen[1]++ & 1))) break;
-              tc_fence_after();
-              issue_pv(1, j == w.j0);
-              if (more)
-                issue_s(1);
-              else
-                commit(o_full + 1);
-            }
-            commit(v_empty + st_v);
-            if (++st_v == S) {
-              st_v = 0;
-              ph_v ^= 1;
-            }
-            if (more) {
-              commit(k_empty + st_k);
-              if (++st_k == S) {
-                st_k = 0;
-                ph_k ^= 1;
-              }
+          ok = at_stage([&](auto c) { return begin(c); });
+          for (int j = w.j0; ok && j < w.j1; ++j) {
+            ok = at_stage([&](auto c) { return step(c, j == w.j0, j + 1 < w.j1); });
+            if (++st == S) {
+              st = 0;
+              ph ^= 1;
             }
           }
-          if (!ok) break;
-        } while (w.next(p));
+        } while (ok && w.next(p));
         // every MMA issued here completes before tensor memory is freed
         commit(drain);
-        mbar_wait(drain, 0, kKvDrainNs);
+        mbar_wait_u(drain, 0, kKvDrainNs);
       }
     }
     __syncwarp();
@@ -795,34 +851,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
 }
 
 // Segments that lie in several spans: block = (border between two spans, 8
-// rows); the border right behind a segment's first span stands for it.
+// rows); the border behind a segment's first span stands for it.
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv_join(const KvAttnParams p, int ctas) {
   constexpr int kV = HD / 32;
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int count = *p.item_count;
+  const int c = blockIdx.x + 1, count = *p.item_count;
+  const int4 bd = __ldg(p.borders + c);
   const int64_t total = count > 0 ? p.item_prefix[count] * p.kv_heads : 0;
-  const int64_t spans = min((int64_t)ctas, total), c = blockIdx.x + 1;
-  if (c >= spans) return;
-  const int64_t u = pr_start(c, total, spans);
-  const int item = find_item(p.item_prefix, count, u / p.kv_heads);
-  const int4 it = __ldg(p.items + item);
-  const int64_t base = p.item_prefix[item] * p.kv_heads;
-  const int h = (int)((u - base) / it.w);
-  const int64_t first = base + (int64_t)h * it.w;
-  if (first == u || pr_owner(first, total, spans) != c - 1) return;
-  const int64_t c0 = c - 1, c1 = pr_owner(first + it.w - 1, total, spans);
+  if (c >= min((int64_t)ctas, total) || bd.x < 0) return;
+  const int4 it = __ldg(p.items + bd.x);      // (its key tiles are not needed)
+  const int h = bd.y, c0 = c - 1, c1 = bd.z, first_slot = bd.w;
   const KvSeq s = kv_seq(p, it.x);
   const int64_t rows = min((int64_t)s.qn * p.group - (int64_t)it.y * kRowsTile, (int64_t)kRowsTile);
-  const int first_slot = pr_start(c0, total, spans) < first ? 1 : 0;
   for (int r = blockIdx.y * 8 + warp; r < rows; r += 8 * gridDim.y) {
     float m = -CUDART_INF_F, l = 0.0f, o[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) o[v] = 0.0f;
-    for (int64_t x = c0; x <= c1; ++x) {
-      const int64_t prow = (2 * x + (x == c0 ? first_slot : 0)) * kRowsTile + r;
+#pragma unroll 2
+    for (int x = c0; x <= c1; ++x) {
+      const int64_t prow = (2ll * x + (x == c0 ? first_slot : 0)) * kRowsTile + r;
       const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.pr_part_ml) + prow);
       const float *src = p.pr_part_o + prow * HD + lane * kV;
       float y[kV];
