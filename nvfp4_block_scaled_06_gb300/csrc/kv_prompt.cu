@@ -737,8 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
       }
     } else {
       // ------------------------------------------------------------ MMA issue --
-      // (the whole warp walks and waits, one lane issues)
-      if (warp == 12) {
+      if (warp == 12 && elect_one()) {
         constexpr uint32_t id_s = idesc_f16(128, 128, 0), id_o = idesc_f16(128, HD, 1);
         const uint64_t qd = sdesc_k_sw128_u(smem), kd = sdesc_k_sw128_u(smem + 2 * T::kHalf);
         const uint64_t vd = sdesc_mn_sw128(smem + (2 + S) * T::kHalf, 16384);
@@ -746,99 +745,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
         int st = 0;                                   // stage of the tile at hand, of K and of V
         uint32_t ph = 0;
         bool ok = true;
-        if (p.stall_probe) ok = warp_wait(never, 0);   // the expiry path under test
-        // Halves and stages are compile-time constants, and tensor memory, all of it, starts at 0: the MMAs' operands
-        // are constants then, which keeps an issue at a few instructions (with them in registers an MMA took 105
-        // cycles to issue, against 64 to run).
-        auto issue_s = [&](auto half, auto stage) {
-          constexpr int H = decltype(half)::value, K = decltype(stage)::value * (T::kHalf >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k)          // (the kind::f16 MMA; the descriptor says f16)
-              tc_mma_bf16(H * 128, qd + (H * (T::kHalf >> 4) + (k >> 2) * 1024 + (k & 3) * 2),
-                          kd + (K + (k >> 2) * 1024 + (k & 3) * 2), id_s, k ? 1u : 0u);
-            tc_commit_u(s_ready + 8 * H);
-          }
-          __syncwarp();
+        // (one lane walks, waits and issues: with the whole warp a step's waits, votes and elections cost 400 cycles)
+        auto twait = [&](uint32_t at, uint32_t par) {
+          if (mbar_try_wait_u(at, par)) return true;
+          if (!abort_flag && mbar_wait_u(at, par, p.timeout_ns)) return true;
+          give_up();
+          return false;
         };
-        auto issue_pv = [&](auto half, auto stage, bool first) {
-          constexpr int H = decltype(half)::value, V = decltype(stage)::value * (T::kHalf >> 4);
-          const uint32_t acc = first ? 0u : 1u;
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16_ts(T::kO + H * HD, H * 128 + k * 8, vd + (V + k * 128), id_o, k ? 1u : acc);
-          }
-          __syncwarp();
-        };
-        auto commit = [&](uint32_t at) {
-          if (elect_one()) tc_commit_u(at);
-          __syncwarp();
-        };
-        using H0 = std::integral_constant<int, 0>;
-        using H1 = std::integral_constant<int, 1>;
-        // S of a segment's first key tile
-        auto begin = [&](auto stage) {
-          constexpr int K = decltype(stage)::value;
-          if (!warp_wait(k_full + 8 * K, ph) || !warp_wait(q_ready, q_seen & 1)) return false;
-          q_seen ^= 1;
-          tc_fence_after();
-          issue_s(H0(), stage);
-          if (w.two) {
-            if (!warp_wait(q_ready + 8, q_seen >> 1)) return false;
-            q_seen ^= 2;
-            tc_fence_after();
-            issue_s(H1(), stage);
-          }
-          commit(k_empty + 8 * K);
-          return true;
-        };
-        // P V of a tile, S of the next
-        auto step = [&](auto stage, bool first, bool more) {
-          constexpr int V = decltype(stage)::value, K = (V + 1) % S;
-          using Next = std::integral_constant<int, K>;
-          if (!warp_wait(v_full + 8 * V, ph) || !warp_wait(p_ready, p_seen & 1)) return false;
-          p_seen ^= 1;
-          tc_fence_after();
-          issue_pv(H0(), stage, first);
-          if (more) {
-            if (!warp_wait(k_full + 8 * K, K == 0 ? ph ^ 1 : ph)) return false;
-            tc_fence_after();
-            issue_s(H0(), Next());
-          } else {
-            commit(o_full);
-          }
-          if (w.two) {
-            if (!warp_wait(p_ready + 8, p_seen >> 1)) return false;
-            p_seen ^= 2;
-            tc_fence_after();
-            issue_pv(H1(), stage, first);
-            if (more)
-              issue_s(H1(), Next());
-            else
-              commit(o_full + 8);
-          }
-          commit(v_empty + 8 * V);
-          if (more) commit(k_empty + 8 * K);
-          return true;
-        };
-        auto at_stage = [&](auto f) {
-          if (st == 0) return f(std::integral_constant<int, 0>());
-          if (S == 2 || st == 1) return f(std::integral_constant<int, 1>());
-          return f(std::integral_constant<int, S - 1>());
-        };
+        if (p.stall_probe) ok = twait(never, 0);   // the expiry path under test
         if (ok) do {
-          ok = at_stage([&](auto c) { return begin(c); });
-          for (int j = w.j0; ok && j < w.j1; ++j) {
-            ok = at_stage([&](auto c) { return step(c, j == w.j0, j + 1 < w.j1); });
-            if (++st == S) {
+#pragma unroll 1
+          for (int j = w.j0 - 1; ok && j < w.j1; ++j) {
+            const bool pv = j >= w.j0, more = j + 1 < w.j1;
+            const int next = !pv ? st : st + 1 == S ? 0 : st + 1;
+            if (pv && !(ok = twait(v_full + 8 * st, ph))) break;
+#pragma unroll 1
+            for (int half = 0; half < (w.two ? 2 : 1); ++half) {
+              if (pv) {
+                if (!(ok = twait(p_ready + 8 * half, (p_seen >> half) & 1))) break;
+                p_seen ^= 1u << half;
+                tc_fence_after();
+                const uint64_t b = vd + (uint32_t)(st * (T::kHalf >> 4));
+                const uint32_t d = T::kO + half * HD, a = half * 128;
+#pragma unroll 8
+                for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, a + k * 8, b + k * 128, id_o, j > w.j0 || k ? 1u : 0u);
+              } else {
+                if (!(ok = twait(q_ready + 8 * half, (q_seen >> half) & 1))) break;
+                q_seen ^= 1u << half;
+                tc_fence_after();
+              }
+              if (more) {
+                if (half == 0) {
+                  if (!(ok = twait(k_full + 8 * next, pv && next == 0 ? ph ^ 1 : ph))) break;
+                  tc_fence_after();
+                }
+                const uint64_t a = qd + (uint32_t)(half * (T::kHalf >> 4)), b = kd + (uint32_t)(next * (T::kHalf >> 4));
+#pragma unroll 8
+                for (int k = 0; k < HD / 16; ++k)
+                  tc_mma_bf16(half * 128, a + ((k >> 2) * 1024 + (k & 3) * 2), b + ((k >> 2) * 1024 + (k & 3) * 2), id_s, k ? 1u : 0u);
+                tc_commit_u(s_ready + 8 * half);
+              } else {
+                tc_commit_u(o_full + 8 * half);
+              }
+            }
+            if (!ok) break;
+            if (pv) tc_commit_u(v_empty + 8 * st);
+            if (more) tc_commit_u(k_empty + 8 * next);
+            if (pv && ++st == S) {
               st = 0;
               ph ^= 1;
             }
           }
         } while (ok && w.next(p));
         // every MMA issued here completes before tensor memory is freed
-        commit(drain);
+        tc_commit_u(drain);
         mbar_wait_u(drain, 0, kKvDrainNs);
       }
     }
