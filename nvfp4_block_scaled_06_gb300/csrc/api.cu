@@ -1892,23 +1892,23 @@ struct KvAttnPlan {
   size_t ws = 0;
   int nt = 0;                          // rows of the kernel for few rows / 8; 0: not run
   bool prompt = false;                 // some sequence may have more rows
-  int64_t *prefix = nullptr, *item_prefix = nullptr, max_items = 0;
+  int64_t *item_prefix = nullptr, max_items = 0;
   float *part_o = nullptr, *part_ml = nullptr, *pr_part_o = nullptr, *pr_part_ml = nullptr;
-  int4 *items = nullptr, *borders = nullptr;
+  int4 *items = nullptr, *borders = nullptr, *few_borders = nullptr;
   int *item_count = nullptr;
 };
 
 void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
   const int64_t group = a->num_heads / a->cache.num_kv_heads, hd = a->cache.head_dim;
   const int64_t rows = group * (a->q_offsets ? std::min(a->max_q_len, a->total_q) : 1);
-  const int64_t few = rows <= 16 ? rows : group;      // beyond: single tokens' rows
-  pl->nt = few <= 8 ? 1 : few <= 16 ? 2 : 0;
+  const int64_t few = rows <= 24 ? rows : group;      // beyond: single tokens' rows
+  pl->nt = few <= 24 ? (int)ceil_div(few, 8) : 0;
   pl->prompt = rows > 8 * pl->nt;
   const int sms = plan_sms();
   Carve c(a->workspace);
   if (pl->nt > 0) {
-    const size_t slots = 2 * (size_t)kv_few_spans(pl->nt, sms) * 8 * pl->nt;
-    pl->prefix = c.take<int64_t>((size_t)(a->num_seqs + 1) * 8);
+    const size_t spans = (size_t)kv_few_spans(pl->nt, sms), slots = 2 * spans * 8 * pl->nt;
+    pl->few_borders = c.take<int4>(spans * sizeof(int4));
     pl->part_o = c.take<float>(slots * (size_t)hd * 4);
     pl->part_ml = c.take<float>(slots * 8);
   }
@@ -1976,7 +1976,8 @@ nvfp4_status run_kv_attention(const nvfp4_kv_attention_args *a, const KvAttnPlan
   p.out_ld = a->out_ld;
   p.out_head_ld = a->out_head_ld;
   p.lse = a->lse;
-  p.prefix = pl.prefix;
+  p.few_borders = pl.few_borders;
+  p.few_rows_most = (int)std::min<int64_t>(8 * pl.nt, p.group * (a->q_offsets ? (int64_t)p.max_q : 1));
   p.part_o = pl.part_o;
   p.part_ml = pl.part_ml;
   p.few_rows = 8 * pl.nt;

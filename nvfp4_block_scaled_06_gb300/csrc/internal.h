@@ -323,7 +323,8 @@ struct KvAttnParams {
   int64_t out_ld, out_head_ld;
   float *lse;                        // [total_q][heads] or null
   int few_rows;                      // sequences of up to this many rows per key-value head go to the kernel for few
-  int64_t *prefix;                   // [seqs + 1]: units before a sequence
+  int few_rows_most;                 // the most of them that a sequence can have
+  int4 *few_borders;                 // [spans]: {sequence or -1, head, last span, slot of the first} at a span's start
   float *part_o, *part_ml;           // partial results of the spans
   int4 *items;                       // [max_items]: the prompt kernel's row tiles
   int64_t *item_prefix;              // [max_items + 1]: key tiles before an item
@@ -335,7 +336,8 @@ struct KvAttnParams {
   uint64_t timeout_ns;
   int stall_probe;                   // test hook: first wait on a barrier nothing arrives at
 };
-// Few rows (8 * nt) per sequence and key-value head.  Spans: warps of the kernel.
+// Few rows (8 * nt, nt up to 3) per sequence and key-value head.  Spans: CTAs of the kernel.
+constexpr int kv_few_ctas(int nt) { return nt == 1 ? 3 : 2; }   // per SM
 int kv_few_spans(int nt, int num_sms);
 cudaError_t launch_kv_few(const KvAttnParams &p, int head_dim, int nt, int num_sms, cudaStream_t st);
 // The sequences with more rows than p.few_rows.  Slots: rows of partial results.
