@@ -1907,7 +1907,7 @@ void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
   const int sms = plan_sms();
   Carve c(a->workspace);
   if (pl->nt > 0) {
-    const size_t spans = (size_t)kv_few_spans(pl->nt, sms), slots = 2 * spans * 8 * pl->nt;
+    const size_t spans = (size_t)kv_few_spans((int)hd, pl->nt, sms), slots = 2 * spans * 8 * pl->nt;
     pl->few_borders = c.take<int4>(spans * sizeof(int4));
     pl->part_o = c.take<float>(slots * (size_t)hd * 4);
     pl->part_ml = c.take<float>(slots * 8);

@@ -337,8 +337,8 @@ struct KvAttnParams {
   int stall_probe;                   // test hook: first wait on a barrier nothing arrives at
 };
 // Few rows (8 * nt, nt up to 3) per sequence and key-value head.  Spans: CTAs of the kernel.
-constexpr int kv_few_ctas(int nt) { return nt == 1 ? 3 : 2; }   // per SM
-int kv_few_spans(int nt, int num_sms);
+constexpr int kv_few_ctas(int head_dim, int nt) { return nt == 1 ? (head_dim == 64 ? 4 : 3) : 2; }   // per SM
+int kv_few_spans(int head_dim, int nt, int num_sms);
 cudaError_t launch_kv_few(const KvAttnParams &p, int head_dim, int nt, int num_sms, cudaStream_t st);
 // The sequences with more rows than p.few_rows.  Slots: rows of partial results.
 int64_t kv_prompt_max_items(int64_t total_q, int64_t group, int64_t seqs);

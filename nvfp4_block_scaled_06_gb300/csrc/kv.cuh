@@ -78,4 +78,23 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b) {
   return s;
 }
 
+// a / b for non-negative a, with the 32-bit division where both fit (a 64-bit one
+// takes some 500 cycles, several of which once stood before a kernel's first load).
+__device__ __forceinline__ int64_t kv_div(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// `total` places in `spans` runs that differ by one place at most.
+struct KvCut {
+  int64_t total, spans, per, longer;   // the first `longer` runs have per + 1 places
+  __device__ __forceinline__ KvCut(int64_t t, int64_t most) : total(t), spans(min(t, most)) {
+    per = spans > 0 ? kv_div(total, spans) : 0;
+    longer = total - per * spans;
+  }
+  __device__ __forceinline__ int64_t start(int64_t w) const { return w * per + min(w, longer); }
+  __device__ __forceinline__ int64_t owner(int64_t u) const {
+    const int64_t head = longer * (per + 1);
+    return u < head ? kv_div(u, per + 1) : longer + kv_div(u - head, per);
+  }
+};
+
 }  // namespace nvfp4

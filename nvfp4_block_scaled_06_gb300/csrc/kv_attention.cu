@@ -23,12 +23,16 @@
 // units of log2): P stays below 2^8, and the usual step needs no reduction
 // over lanes and no rescaling.
 //
-// Work: 32-key units of all (sequence, head) segments in one line, cut into equal
-// spans, one per CTA, whose warps take its units in turn; a warp's ring of
-// asynchronous copies runs on over segment borders.  At a segment's end the
-// warps' (o, m, l) are joined in shared memory; segments that lie in several spans
-// leave one partial result per span, which a second kernel sums in order.
+// Work: a line of items, cut into equal spans, one per CTA.  An item is a
+// (sequence, head) with its 32-key units, which the span's warps take in turn and
+// whose (o, m, l) they join in shared memory; items that lie in several spans
+// leave one partial result per span, which a second kernel sums in order.  Where
+// sequences are short against a span an item is four heads of one, a warp each,
+// with nothing to join.  A warp's ring of asynchronous copies runs on over the
+// items' borders.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "kv.cuh"
@@ -41,6 +45,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kMaxEntries = 256;    // prefix entries held in shared memory
 constexpr int kKeys = 32;           // of a unit: two 16-key tiles of the MMA, each in one page
+constexpr int kOver = 4;            // what an item costs beside its units, in units
+constexpr int kSoloMost = 32;       // units of a sequence whose heads may go to one warp each
 constexpr float kRaise = 8.0f;
 
 template <int HD, int NT>
@@ -50,7 +56,7 @@ struct Few {
   static constexpr int kCodes = kKeys * HD / 2;           // a unit's codes of K (or V)
   static constexpr int kSf = kKeys * HD / 16;             // and its scales
   static constexpr int kStage = 2 * (kCodes + kSf);
-  static constexpr int kCtas = kv_few_ctas(NT);           // per SM
+  static constexpr int kCtas = kv_few_ctas(HD, NT);       // per SM
   static constexpr int kPitch = HD + 4;                   // floats of a row of the warps' results
   static constexpr size_t kRing = (size_t)kWarps * kStages * kStage;
   static constexpr size_t kSmem = kRing + (size_t)kWarps * kRows * kPitch * 4;
@@ -58,19 +64,19 @@ struct Few {
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
-// The segments of sequence b: first unit, units (0: no rows, or more than this
-// kernel takes), rows.
+// Sequence b: first unit, units per head (0: no rows, or more than this kernel
+// takes), rows per head.
 struct Seg {
   KvSeq s;
   int u0, units, rows;
@@ -84,27 +90,58 @@ __device__ __forceinline__ Seg seg_of(const KvAttnParams &p, int b) {
   g.units = g.rows > 0 ? max(1, (int)(((int64_t)g.s.hi + kKeys - 1) / kKeys) - g.u0) : 0;
   return g;
 }
-__device__ __forceinline__ int64_t units_of(const KvAttnParams &p, const Seg &g) {
-  return (int64_t)g.units * p.kv_heads;
-}
 
-__device__ __forceinline__ int64_t span_start(int64_t w, int64_t total, int64_t spans) { return w * total / spans; }
-__device__ __forceinline__ int64_t span_of(int64_t u, int64_t total, int64_t spans) {
-  return ((u + 1) * spans - 1) / total;
-}
+// The line's rule: with `solo` units or fewer a sequence's items are four heads
+// each and are not cut (they are the span's that their first place lies in).
+struct Line {
+  int solo;
+  int64_t begin, end;         // this span's places
+  __device__ __forceinline__ bool is_solo(const Seg &g) const { return g.units <= solo; }
+  __device__ __forceinline__ int items(const KvAttnParams &p, const Seg &g) const {
+    return g.units == 0 ? 0 : is_solo(g) ? (p.kv_heads + kWarps - 1) / kWarps : p.kv_heads;
+  }
+  __device__ __forceinline__ int places(const Seg &g) const {      // of an item
+    return (is_solo(g) ? kWarps * g.units : g.units) + kOver;
+  }
+};
 
-// A position in the line of units: sequence, head, unit of the segment.
+// An item of the span and this warp's units of it.
 struct Cursor {
-  int b, h, u;
+  int b, item;
   Seg g;
-  // On to the next segment; false past the last.
-  __device__ __forceinline__ bool next(const KvAttnParams &p) {
-    if (++h < p.kv_heads) return true;
-    h = 0;
-    do {
-      if (++b >= p.seqs) return false;
-      g = seg_of(p, b);
-    } while (g.units == 0);
+  int64_t at;                 // the item's first place
+  int h, u, end, step;        // head; units u, u + step ... below end
+  int j0, j1;                 // the span's units of the item (all warps')
+  bool solo;
+  __device__ __forceinline__ void open(const KvAttnParams &p, const Line &l, int warp) {
+    solo = l.is_solo(g);
+    if (solo) {
+      h = item * kWarps + warp;
+      const bool mine = at >= l.begin && at < l.end && h < p.kv_heads;
+      j0 = u = 0;
+      j1 = end = mine ? g.units : 0;
+      step = 1;
+    } else {
+      h = item;
+      j0 = (int)max(l.begin - at - kOver, (int64_t)0);
+      j1 = (int)max(min(l.end - at - kOver, (int64_t)g.units), (int64_t)0);
+      u = j0 + warp;
+      end = j1;
+      step = kWarps;
+    }
+  }
+  // On to the span's next item; false past the last.
+  __device__ __forceinline__ bool next(const KvAttnParams &p, const Line &l, int warp) {
+    at += l.places(g);
+    if (at >= l.end) return false;
+    if (++item == l.items(p, g)) {
+      item = 0;
+      do {
+        if (++b >= p.seqs) return false;
+        g = seg_of(p, b);
+      } while (g.units == 0);
+    }
+    open(p, l, warp);
     return true;
   }
 };
@@ -118,135 +155,178 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   constexpr int kMt = HD / 16;        // 16-channel tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t pre[kMaxEntries + 1];
-  __shared__ int64_t wsum[kWarps];
-  __shared__ int limits[kWarps][S][2];
+  __shared__ int64_t wsum[2][kWarps];
+  __shared__ int limits[kWarps][S];
   __shared__ float2 warp_ml[kWarps][F::kRows];
   float *warp_o = reinterpret_cast<float *>(smem + F::kRing);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   griddep_launch_dependents();
   griddep_wait();
 
-  // Units before each entry of `per` sequences, by a scan over the block.
+  // All units, then the places before each entry of `per` sequences, by scans over the block.
   const int per = (p.seqs + kMaxEntries - 1) / kMaxEntries;
   const int entries = (p.seqs + per - 1) / per;
   const int each = (entries + kWarps * 32 - 1) / (kWarps * 32);   // entries of a thread
-  const int e0 = min(tid * each, entries), e1 = min(e0 + each, entries);
-  int64_t sum = 0;
-  for (int b = e0 * per; b < min(e1 * per, p.seqs); ++b) sum += units_of(p, seg_of(p, b));
-  int64_t scan = sum;
+  const int b0 = min(tid * each * per, p.seqs), b1 = min(b0 + each * per, p.seqs);
+  Line line;
+  int64_t total;
+  {
+    const Seg seg0 = seg_of(p, min(b0, p.seqs - 1));
+    auto seg = [&](int b) { return b == b0 ? seg0 : seg_of(p, b); };
+    int64_t units = 0;
+    for (int b = b0; b < b1; ++b) units += seg(b).units;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += v;
+    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+    if (lane == 0) wsum[0][warp] = units;
+    __syncthreads();
+    units = 0;
+    for (int w = 0; w < kWarps; ++w) units += wsum[0][w];
+    // four heads of a sequence are at most a span of the units
+    line.solo = p.kv_heads < kWarps ? 0 : (int)min(kv_div(units * p.kv_heads, (int64_t)gridDim.x * kWarps), (int64_t)kSoloMost);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seg g2 = seg(b);
+      sum += (int64_t)line.items(p, g2) * line.places(g2);
+    }
+    int64_t scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) wsum[1][warp] = scan;
+    __syncthreads();
+    int64_t base = scan - sum;
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += wsum[1][w];
+      total += wsum[1][w];
+    }
+    for (int b = b0; b < b1; ++b) {
+      if (b % per == 0) pre[b / per] = base;
+      const Seg g2 = seg(b);
+      base += (int64_t)line.items(p, g2) * line.places(g2);
+    }
+    __syncthreads();
   }
-  if (lane == 31) wsum[warp] = scan;
-  __syncthreads();
-  int64_t base = scan - sum;
-  for (int w = 0; w < warp; ++w) base += wsum[w];
-  for (int e = e0; e < e1; ++e) {
-    pre[e] = base;
-    for (int b = e * per; b < min((e + 1) * per, p.seqs); ++b) base += units_of(p, seg_of(p, b));
-  }
-  int64_t total = 0;
-  for (int w = 0; w < kWarps; ++w) total += wsum[w];
-  __syncthreads();
 
-  const int64_t spans = min((int64_t)gridDim.x, total), span = blockIdx.x;
-  if (span >= spans) {
+  const KvCut cut(total, gridDim.x);
+  const int64_t span = blockIdx.x;
+  if (span >= cut.spans) {
     if (tid == 0) p.few_borders[span] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const int64_t u_begin = span_start(span, total, spans), u_end = span_start(span + 1, total, spans);
+  line.begin = cut.start(span);
+  line.end = cut.start(span + 1);
 
-  Cursor cur;                                       // of the segment at hand
-  int64_t seg0;                                     // its first unit in the line
+  Cursor cur;                                       // the item at hand
   {
-    int lo = 0, hi = entries;                       // the last entry that starts at or before u_begin
+    int lo = 0, hi = entries;                       // the last entry that starts at or before the span
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u_begin) lo = mid; else hi = mid;
+      if (pre[mid] <= line.begin) lo = mid; else hi = mid;
     }
-    int64_t at = pre[lo];
+    cur.at = pre[lo];
     cur.b = lo * per;
-    for (;; ++cur.b) {                              // (ends before p.seqs: u_begin < total)
+    int places;
+    for (;; ++cur.b) {                              // (ends before p.seqs: the span starts before the line's end)
       cur.g = seg_of(p, cur.b);
-      const int64_t n = units_of(p, cur.g);
-      if (u_begin < at + n) break;
-      at += n;
+      places = line.places(cur.g);
+      const int64_t n = (int64_t)line.items(p, cur.g) * places;
+      if (line.begin < cur.at + n) break;
+      cur.at += n;
     }
-    cur.h = (int)((u_begin - at) / cur.g.units);
-    seg0 = at + (int64_t)cur.h * cur.g.units;
-    cur.u = (int)(u_begin - seg0);
+    cur.item = (int)kv_div(line.begin - cur.at, places);
+    cur.at += (int64_t)cur.item * places;
+    cur.open(p, line, warp);
+    // the first border inside a cut item stands for it in the summing kernel
+    if (tid == 0) {
+      const int64_t c0 = cut.owner(cur.at + kOver);
+      p.few_borders[span] = make_int4(!cur.solo && cur.j0 > 0 && c0 == span - 1 ? cur.b : -1, cur.h,
+                                      (int)cut.owner(cur.at + places - 1), cut.start(c0) < cur.at ? 1 : 0);
+    }
   }
-  // the first border inside a segment stands for it in the summing kernel
-  if (tid == 0) {
-    const int64_t c0 = span_of(seg0, total, spans);
-    p.few_borders[span] = make_int4(cur.u > 0 && c0 == span - 1 ? cur.b : -1, cur.h,
-                                    (int)span_of(seg0 + cur.g.units - 1, total, spans),
-                                    span_start(c0, total, spans) < seg0 ? 1 : 0);
-  }
+
+  // An item's rows of q as they are, this lane's: row 8 nt + g, HD / 4 channels from t * HD / 4 on.
+  uint32_t xq[NT][HD / 8];
+  float gsc;
+  auto ask_q = [&](const Cursor &c) {
+    gsc = p.scale_log2 * p.gk[min(c.h, p.kv_heads - 1)];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g, tok = r / p.group, head = c.h * p.group + r % p.group;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(c.g.s.q0 + tok) * p.q_ld +
+                                                         (int64_t)head * p.q_head_ld + t * (HD / 4));
+#pragma unroll
+      for (int v = 0; v < HD / 32; ++v) {
+        const uint4 y = r < c.g.rows && c.j0 < c.j1 ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+        xq[nt][4 * v] = y.x; xq[nt][4 * v + 1] = y.y; xq[nt][4 * v + 2] = y.z; xq[nt][4 * v + 3] = y.w;
+      }
+    }
+  };
+  ask_q(cur);
 
   uint8_t *ring = smem + (size_t)warp * S * F::kStage;
   const uint32_t ring_u = smem_u32(ring);
   int ids = 0, ids_b = -1, ids_at = 0;              // this lane's entry of 32 of the page table
   const int page_mask = (1 << p.page_shift) - 1;
 
-  // The copies' place: this warp's units, every kWarps-th of the span.
-  Cursor ahead = cur;
-  int left = (int)min(u_end - u_begin, (int64_t)0x7FFFFFFF) - warp;   // units of the span from there on
-  auto forward = [&](int n) {
-    ahead.u += n;
-    while (ahead.u >= ahead.g.units) {
-      ahead.u -= ahead.g.units;
-      if (!ahead.next(p)) {
-        left = 0;
-        return;
-      }
-    }
+  Cursor ahead = cur;                               // the copies' place
+  bool more = true;
+  auto settle = [&] {                               // on to this warp's next unit, where it has none left here
+    while (more && ahead.u >= ahead.end) more = ahead.next(p, line, warp);
   };
-  forward(warp);
+  settle();
   // Copies of the unit at `ahead` into a stage; keys outside [0, n) and pages
-  // outside the cache are zero-filled and left out by their limit.
-  auto copy_unit = [&](int stage) {
-    int64_t oc[2], os[2];
-    uint32_t bytes[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int key = (ahead.g.u0 + ahead.u) * kKeys + 16 * i, page = key >> p.page_shift;
-      if (ids_b != ahead.b || page < ids_at || page >= ids_at + 32) {
-        ids_b = ahead.b;
-        ids_at = page & ~31;
-        ids = ids_at + lane < p.max_pages ? __ldg(p.table + (int64_t)ids_b * p.table_ld + ids_at + lane) : -1;
-      }
-      const int id = __shfl_sync(0xffffffffu, ids, page - ids_at);
-      int limit = min(16, ahead.g.s.n - key);
-      if (limit <= 0 || !NVFP4_NOTE(id >= 0 && id < p.num_pages, p.status)) limit = 0;
-      const int row = (ahead.h << p.page_shift) + (key & page_mask);
-      oc[i] = limit ? id * p.codes_stride + row * (HD / 2) : 0;
-      os[i] = limit ? id * p.sf_stride + row * (HD / 16) : 0;
-      bytes[i] = limit ? 16u : 0u;
-      if (lane == 0) limits[warp][stage][i] = limit;
+  // outside the cache are zero-filled and left out by their limits.  (Kept to
+  // few instructions: address arithmetic once took half of a unit's time.)
+  const uint8_t *kc0 = p.k_codes + lane * 16, *vc0 = p.v_codes + lane * 16;
+  constexpr int kR = F::kSf / 16;                   // 16-byte runs of a unit's K scales: lanes 0 .. kR - 1, V's follow
+  const uint8_t *sf0 = (lane < kR ? p.k_sf : p.v_sf) + lane % kR * 16;
+  // The keys from `key` on, kN of them, all in one page: stage bytes at `dst`, runs `part` of kParts of the unit.
+  auto copy_keys = [&](int key, uint32_t dst, auto parts, int part) {
+    constexpr int kParts = decltype(parts)::value, kN = kKeys / kParts, kC = F::kCodes / 512 / kParts;
+    const int page = key >> p.page_shift;
+    if (ids_b != ahead.b || (uint32_t)(page - ids_at) >= 32u) {
+      ids_b = ahead.b;
+      ids_at = page & ~31;
+      ids = ids_at + lane < p.max_pages ? __ldg(p.table + (int64_t)ids_b * p.table_ld + ids_at + lane) : -1;
     }
-    const uint32_t dst = ring_u + stage * F::kStage;
-    constexpr int kC = F::kCodes / 512;             // 16-byte runs of K's codes per lane
+    const int id = __shfl_sync(0xffffffffu, ids, page & 31);
+    const bool in = key < ahead.g.s.n && NVFP4_NOTE((uint32_t)id < (uint32_t)p.num_pages, p.status);
+    const int row = (ahead.h << p.page_shift) + (key & page_mask);
+    const int64_t oc = in ? id * p.codes_stride + row * (HD / 2) : 0;
+    const int64_t os = in ? id * p.sf_stride + row * (HD / 16) : 0;
+    const uint32_t bytes = in ? 16u : 0u, at = dst + part * (F::kCodes / kParts);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int hf = i / (kC / 2), at = ((i % (kC / 2)) * 32 + lane) * 16;
-      cp_async_16(dst + (i * 32 + lane) * 16, p.k_codes + oc[hf] + at, bytes[hf]);
-      cp_async_16(dst + F::kCodes + (i * 32 + lane) * 16, p.v_codes + oc[hf] + at, bytes[hf]);
+      cp_async_16(at + i * 512, kc0 + oc + i * 512, bytes);
+      cp_async_16(at + F::kCodes + i * 512, vc0 + oc + i * 512, bytes);
     }
-    constexpr int kR = F::kSf / 16;                 // 16-byte runs of K's scales
-    if (lane < 2 * kR) {
-      const int c = lane % kR, hf = c / (kR / 2);
-      cp_async_16(dst + 2 * F::kCodes + lane * 16,
-                  (lane < kR ? p.k_sf : p.v_sf) + (hf ? os[1] : os[0]) + (c % (kR / 2)) * 16, hf ? bytes[1] : bytes[0]);
+    // (a part's scales are the lanes' whose runs lie in it)
+    if (lane < 2 * kR && lane % kR / (kR / kParts) == part)
+      cp_async_16(dst + 2 * F::kCodes, sf0 + os - part * (kR / kParts) * 16, bytes);
+    return in ? min(kN, ahead.g.s.n - key) : 0;
+  };
+  auto copy_unit = [&](int stage) {
+    const int key = (ahead.g.u0 + ahead.u) * kKeys;
+    const uint32_t dst = ring_u + stage * F::kStage + lane * 16;
+    int l0, l1;
+    if (p.page_shift >= 5) {
+      const int l = copy_keys(key, dst, std::integral_constant<int, 1>(), 0);
+      l0 = min(l, 16);
+      l1 = l - l0;
+    } else {
+      l0 = copy_keys(key, dst, std::integral_constant<int, 2>(), 0);
+      l1 = copy_keys(key + 16, dst, std::integral_constant<int, 2>(), 1);
     }
+    if (lane == 0) limits[warp][stage] = l0 | l1 << 8;
   };
   auto fetch = [&](int stage) {
-    if (left > 0) {
+    if (more) {
       copy_unit(stage);
-      left -= kWarps;
-      if (left > 0) forward(kWarps);
+      ahead.u += ahead.step;
+      settle();
     }
     cp_async_commit();
   };
@@ -257,29 +337,18 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   uint32_t qf[NT][kMt][2];
   float sc[NT][2], m[NT][2], l[NT][2], o[kMt][NT][4];
   int see_lo[NT][2], see_hi[NT][2];                 // keys [see_lo, see_hi) of this lane's rows (8 nt + 2 t, + 1)
-  int64_t u = u_begin + warp, first = u_begin;      // this warp's next unit; the span's first of the segment
   int stage = 0, fill = S - 1;
 
 #pragma unroll 1
   while (true) {
-    // ------------------------------------------------------- a segment's rows --
+    // --------------------------------------------------------- an item's rows --
     const int rows = cur.g.rows;
     int all_lo = 0, all_hi = 0x7FFFFFFF;            // keys that every row sees
     {
-      const float gsc = p.scale_log2 * p.gk[cur.h];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        uint32_t x[HD / 8];
-        const int r = nt * 8 + g;
-        const int tok = r / p.group, head = cur.h * p.group + r % p.group;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(cur.g.s.q0 + tok) * p.q_ld +
-                                                           (int64_t)head * p.q_head_ld + t * (HD / 4));
+        uint32_t (&x)[HD / 8] = xq[nt];
         uint32_t m2 = 0;
-#pragma unroll
-        for (int v = 0; v < HD / 32; ++v) {
-          const uint4 y = r < rows ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
-          x[4 * v] = y.x; x[4 * v + 1] = y.y; x[4 * v + 2] = y.z; x[4 * v + 3] = y.w;
-        }
         // the order of |x| is that of its bits, infinities and NaNs last
 #pragma unroll
         for (int v = 0; v < HD / 8; ++v) m2 = __vmaxu2(m2, x[v] & 0x7FFF7FFFu);
@@ -321,28 +390,28 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, x));
       }
     }
-    const int64_t seg_end = seg0 + cur.g.units, end = min(seg_end, u_end);
 
     // -------------------------------------------------------- its units, in turn --
 #pragma unroll 1
-    for (; u < end; u += kWarps) {
+    for (int u = cur.u; u < cur.end; u += cur.step) {
       fetch(fill);
       cp_async_wait<S - 1>();
       __syncwarp();
 
       const uint8_t *st = ring + stage * F::kStage;
-      const int limit0 = limits[warp][stage][0], limit1 = limits[warp][stage][1];
-      const int key = (cur.g.u0 + (int)(u - seg0)) * kKeys;
+      const int limit0 = limits[warp][stage] & 255, limit1 = limits[warp][stage] >> 8;
+      const int key = (cur.g.u0 + u) * kKeys;
       const bool whole = limit0 + limit1 == kKeys && key >= all_lo && key + kKeys <= all_hi;
 
       // S^T = K Q^T: keys g and g + 8 of both tiles
       float s[2][NT][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        float s2[NT][4];                            // every other step's sum: half the chain
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[i][nt][k] = 0.0f;
+          for (int k = 0; k < 4; ++k) s[i][nt][k] = s2[nt][k] = 0.0f;
         uint32_t w[2][kKw], sf[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -375,9 +444,13 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(s[i][nt], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1], qf[nt][2 * j + k][0],
-                      qf[nt][2 * j + k][1]);
+              mma_f16(k ? s2[nt] : s[i][nt], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1],
+                      qf[nt][2 * j + k][0], qf[nt][2 * j + k][1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[i][nt][k] += s2[nt][k];
       }
 
 #pragma unroll
@@ -510,8 +583,38 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
       fill = fill + 1 == S ? 0 : fill + 1;
     }
 
+    // the next item's rows on their way, meanwhile
+    Cursor nxt = cur;
+    const bool another = nxt.next(p, line, warp);
+    if (NT == 1 && another) ask_q(nxt);              // (more rows have no registers for it)
+    if (cur.j0 >= cur.j1) {
+      // (nothing of this item for this span, or for this warp)
+    } else if (cur.solo) {
+      // ------------------------------------------------------- a warp's own head --
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float sum_l = l[nt][k];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) sum_l += __shfl_xor_sync(0xffffffffu, sum_l, d);
+          const int r = nt * 8 + 2 * t + k;
+          if (r >= rows) continue;
+          const int64_t q = cur.g.s.q0 + r / p.group;
+          const int head = cur.h * p.group + r % p.group;
+          const float f = sum_l == 0.0f ? 0.0f : p.gv[cur.h] / sum_l;
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + q * p.out_ld + (int64_t)head * p.out_head_ld + g * (HD / 8));
+#pragma unroll
+          for (int j = 0; j < kVw; ++j)
+            dst[j] = make_uint4(pack_bf2(o[4 * j][nt][k] * f, o[4 * j][nt][k + 2] * f),
+                                pack_bf2(o[4 * j + 1][nt][k] * f, o[4 * j + 1][nt][k + 2] * f),
+                                pack_bf2(o[4 * j + 2][nt][k] * f, o[4 * j + 2][nt][k + 2] * f),
+                                pack_bf2(o[4 * j + 3][nt][k] * f, o[4 * j + 3][nt][k + 2] * f));
+          if (p.lse && g == 0) p.lse[q * p.kv_heads * p.group + head] = (m[nt][k] + __log2f(sum_l)) * CUDART_LN2_F;
+        }
+    } else {
     // --------------------------------------------------- the warps' results, joined --
-    __syncthreads();                                // (the last segment's have been read)
+    __syncthreads();                                // (the last item's have been read)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,6 +623,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum_l += __shfl_xor_sync(0xffffffffu, sum_l, d);
         const int r = nt * 8 + 2 * t + k;
+        if (r >= rows) continue;
         float4 *dst = reinterpret_cast<float4 *>(warp_o + (warp * F::kRows + r) * F::kPitch + g * (HD / 8));
 #pragma unroll
         for (int j = 0; j < HD / 32; ++j)
@@ -527,8 +631,8 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         if (g == 0) warp_ml[warp][r] = make_float2(m[nt][k], sum_l);
       }
     __syncthreads();
-    const bool full = first == seg0 && end == seg_end;
-    const int64_t slot = 2 * span + (first == u_begin ? 0 : 1);
+    const bool full = cur.j0 == 0 && cur.j1 == cur.g.units;
+    const int64_t slot = 2 * span + (cur.at > line.begin ? 1 : 0);   // (an item cut at the span's start, at its end)
     for (int i = tid; i < rows * (HD / 8); i += kWarps * 32) {
       const int r = i / (HD / 8), c = i % (HD / 8) * 8;
       float mm = -CUDART_INF_F, ll = 0.0f, y[8];
@@ -562,9 +666,10 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * F::kRows + r) * 2) = make_float2(mm, ll);
       }
     }
-    if (end == u_end) break;
-    seg0 = first = end;
-    cur.next(p);
+    }
+    if (!another) break;
+    cur = nxt;
+    if (NT > 1) ask_q(cur);
   }
   cp_async_wait<0>();
 }
@@ -573,8 +678,8 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
 // the border behind a segment's first span stands for it.  The spans' partial
 // results are dealt to the block's warps in order.
 template <int HD, int NT>
-__global__ void __launch_bounds__(128) k_kv_sum(const KvAttnParams p) {
-  constexpr int kRows = 8 * NT, kV = HD / 32, kW = 4;
+__global__ void __launch_bounds__(256) k_kv_sum(const KvAttnParams p) {
+  constexpr int kRows = 8 * NT, kV = HD / 32, kW = 8;
   __shared__ float sh_o[kW][HD];
   __shared__ float2 sh_ml[kW];
   griddep_launch_dependents();
@@ -585,12 +690,19 @@ __global__ void __launch_bounds__(128) k_kv_sum(const KvAttnParams p) {
   const int c0 = blockIdx.x, c1 = bd.z, h = bd.y;
   const KvSeq s = kv_seq(p, bd.x);
   if (r >= s.qn * p.group) return;
+  auto row_of = [&](int c) { return (2ll * c + (c == c0 ? bd.w : 0)) * kRows + r; };
+  // this warp's spans: c0 + warp, kW apart; their maximum and sum first, so that the rows' loads are independent
   float m = -CUDART_INF_F, l = 0.0f, o[kV];
+  for (int c = c0 + warp + lane * kW; c <= c1; c += 32 * kW)
+    m = fmaxf(m, __ldg(reinterpret_cast<const float2 *>(p.part_ml) + row_of(c)).x);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float top = m == -CUDART_INF_F ? 0.0f : m;
 #pragma unroll
   for (int v = 0; v < kV; ++v) o[v] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = c0 + warp; c <= c1; c += kW) {
-    const int64_t row = (2ll * c + (c == c0 ? bd.w : 0)) * kRows + r;
+    const int64_t row = row_of(c);
     const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.part_ml) + row);
     const float *src = p.part_o + row * HD + lane * kV;
     float y[kV];
@@ -601,12 +713,10 @@ __global__ void __launch_bounds__(128) k_kv_sum(const KvAttnParams p) {
       const float2 v = __ldg(reinterpret_cast<const float2 *>(src));
       y[0] = v.x; y[1] = v.y;
     }
-    const float m2 = fmaxf(m, ml.x), ref = m2 == -CUDART_INF_F ? 0.0f : m2;
-    const float f0 = ex2(m - ref), f1 = ex2(ml.x - ref);
-    m = m2;
-    l = l * f0 + ml.y * f1;
+    const float f = ex2(ml.x - top);
+    l += ml.y * f;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) o[v] = o[v] * f0 + y[v] * f1;
+    for (int v = 0; v < kV; ++v) o[v] += y[v] * f;
   }
 #pragma unroll
   for (int v = 0; v < kV; ++v) sh_o[warp][lane * kV + v] = o[v];
@@ -645,12 +755,12 @@ cudaError_t run_few(const KvAttnParams &p, int num_sms, cudaStream_t st) {
   const int ctas = num_sms * F::kCtas;
   if (cudaError_t e = launch_pdl(k_kv_few<HD, NT>, dim3(ctas), dim3(kWarps * 32), F::kSmem, st, p); e != cudaSuccess)
     return e;
-  return launch_pdl(k_kv_sum<HD, NT>, dim3(ctas - 1, std::min(F::kRows, p.few_rows_most)), dim3(128), 0, st, p);
+  return launch_pdl(k_kv_sum<HD, NT>, dim3(ctas - 1, std::min(F::kRows, p.few_rows_most)), dim3(256), 0, st, p);
 }
 
 }  // namespace
 
-int kv_few_spans(int nt, int num_sms) { return num_sms * kv_few_ctas(nt); }
+int kv_few_spans(int head_dim, int nt, int num_sms) { return num_sms * kv_few_ctas(head_dim, nt); }
 
 cudaError_t launch_kv_few(const KvAttnParams &p, int head_dim, int nt, int num_sms, cudaStream_t st) {
   if (head_dim == 128)

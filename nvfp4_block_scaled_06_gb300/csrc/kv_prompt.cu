@@ -126,11 +126,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
-__device__ __forceinline__ int64_t pr_start(int64_t c, int64_t total, int64_t spans) { return c * total / spans; }
-__device__ __forceinline__ int64_t pr_owner(int64_t u, int64_t total, int64_t spans) {
-  return ((u + 1) * spans - 1) / total;
-}
-
 // ------------------------------------------------------------------- listing --
 // Row tiles of the sequences with more than few_rows rows, in order: {sequence,
 // tile, first key tile, key tiles}, and the key tiles before each.  One block.
@@ -312,27 +307,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
 
   const int count = *p.item_count;
   const int64_t total = count > 0 ? p.item_prefix[count] * p.kv_heads : 0;
-  const int64_t spans = min((int64_t)gridDim.x, total), cta = blockIdx.x;
-  if (cta < spans && note_bounds(tmem == 0, p.status)) {
+  const KvCut cut(total, gridDim.x);
+  const int64_t cta = blockIdx.x;
+  if (cta < cut.spans && note_bounds(tmem == 0, p.status)) {
     Walk w;
     bool any;
     {
-      const int64_t u0 = pr_start(cta, total, spans);
-      w.left = (int)(pr_start(cta + 1, total, spans) - u0);
-      w.item = find_item(p.item_prefix, count, u0 / p.kv_heads);
+      const int64_t u0 = cut.start(cta);
+      w.left = (int)(cut.start(cta + 1) - u0);
+      w.item = find_item(p.item_prefix, count, kv_div(u0, p.kv_heads));
       // (prefix counts the units of one head: item i's lie from prefix[i] * kv_heads on)
       w.load(p);
       const int64_t base = p.item_prefix[w.item] * p.kv_heads;
-      w.h = (int)((u0 - base) / (w.nt + kOver));
+      w.h = (int)kv_div(u0 - base, w.nt + kOver);
       const int64_t first = base + (int64_t)w.h * (w.nt + kOver);
       w.r = (int)(u0 - first);
       w.clip();
       // the first border inside a segment stands for it in the joining kernel
       if (tid == 0) {
-        const int64_t c0 = pr_owner(first + kOver, total, spans);
+        const int64_t c0 = cut.owner(first + kOver);
         p.borders[cta] = make_int4(w.j0 > 0 && c0 == cta - 1 ? w.item : -1, w.h,
-                                   (int)pr_owner(first + w.nt + kOver - 1, total, spans),
-                                   pr_start(c0, total, spans) < first ? 1 : 0);
+                                   (int)cut.owner(first + w.nt + kOver - 1),
+                                   cut.start(c0) < first ? 1 : 0);
       }
       any = w.j0 < w.j1 || w.next(p);
     }
