@@ -45,7 +45,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kMaxEntries = 256;    // prefix entries held in shared memory
 constexpr int kKeys = 32;           // of a unit: two 16-key tiles of the MMA, each in one page
-constexpr int kOver = 4;            // what an item costs beside its units, in units
+constexpr int kOver = 8;            // what an item costs beside its units, in units
 constexpr int kSoloMost = 32;       // units of a sequence whose heads may go to one warp each
 constexpr float kRaise = 8.0f;
 

@@ -7,15 +7,17 @@
 // Infinities saturate; a block that holds a NaN gets byte 0x7F (NaN), codes 0.
 // Blocks run along the channels, so a token is written without its neighbours.
 //
-// HBM-bound: 2 B read + 0.5625 B written per element, and back.  A warp takes
-// consecutive tokens of one head: its codes are one run of a page where the
-// slots are consecutive, while consecutive warps take the heads of the same
-// tokens, whose bf16 rows are neighbours.
+// HBM-bound: 2 B read + 0.5625 B written per element, and back.  A lane takes 32
+// channels (64 bytes of bf16, 16 of codes, two scales) of two tokens at a time,
+// all loads first; a warp consecutive tokens of one head, whose codes are one run
+// of a page where the slots are consecutive, while consecutive warps take the
+// heads of the same tokens, whose bf16 rows are neighbours.
 #include <float.h>
 
 #include "encode.cuh"
 #include "internal.h"
 #include "kv.cuh"
+#include "mxfp4.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4 {
@@ -32,109 +34,175 @@ __device__ __forceinline__ bool kv_at(const KvPages &c, int64_t slot, int h, int
   return true;
 }
 
-// Grid (ctas, 2): y = 0 the keys, 1 the values.  A lane takes one 16-channel
-// block; kLanes = head_dim / 16 lanes a row.
-template <int kLanes>
+constexpr int kTokens = 2;            // of a lane at a time
+
+// What this warp works on: grid (ctas, 2), y = 0 the keys, 1 the values; items of
+// kRows x kTokens tokens and one head, heads fastest.
+struct KvWalk {
+  int64_t group, groups;              // of tokens
+  int head, heads, step_head;
+  int64_t step_group;
+  __device__ __forceinline__ KvWalk(const KvCopyParams &p, int tokens) {
+    const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+    heads = p.c.kv_heads;
+    groups = kv_div(p.tokens + tokens - 1, tokens);
+    group = kv_div(warp, heads);
+    head = (int)(warp - group * heads);
+    step_group = kv_div(warps, heads);
+    step_head = (int)(warps - step_group * heads);
+  }
+  __device__ __forceinline__ bool on() const { return group < groups; }
+  __device__ __forceinline__ void next() {
+    group += step_group;
+    head += step_head;
+    if (head >= heads) {
+      head -= heads;
+      ++group;
+    }
+  }
+};
+
+template <int HD>
 __global__ void __launch_bounds__(256) k_kv_write(const KvCopyParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
-  constexpr int kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, blk = lane % kLanes;
+  constexpr int kLanes = HD / 32, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, q = lane % kLanes;
   const bool val = blockIdx.y != 0;
-  const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(val ? p.v : p.k);
+  const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(val ? p.v : p.k) + q * 32;
   const int64_t ld = val ? p.v_ld : p.k_ld, hld = val ? p.v_head_ld : p.k_head_ld;
-  uint8_t *codes = val ? p.c.v_codes : p.c.k_codes, *sf = val ? p.c.v_sf : p.c.k_sf;
-  const int64_t items = (p.tokens + kRows - 1) / kRows * p.c.kv_heads;
-  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += nwarps) {
-    const int64_t t = it / p.c.kv_heads * kRows + lane / kLanes;
-    const int h = (int)(it % p.c.kv_heads);
-    int64_t oc = 0, os = 0;
-    const bool on = t < p.tokens && kv_at(p.c, p.slots[t], h, oc, os);
-    uint32_t sb = 0;
-    if (on) {
-      const float g = (val ? p.gv : p.gk)[h];
-      const uint4 *s4 = reinterpret_cast<const uint4 *>(src + t * ld + h * hld + blk * 16);
-      const uint4 a = __ldg(s4), b = __ldg(s4 + 1);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t m2 = w[0] & 0x7FFF7FFFu;
+  uint8_t *codes = (val ? p.c.v_codes : p.c.k_codes) + q * 16, *sf = (val ? p.c.v_sf : p.c.k_sf) + q * 2;
+  const bool wide = ((reinterpret_cast<uintptr_t>(src) >> 1 | ld | hld) & 15) == 0;   // whole 32-byte sectors
+  for (KvWalk w(p, kRows * kTokens); w.on(); w.next()) {
+    int64_t oc[kTokens], os[kTokens];
+    bool on[kTokens];
+    uint32_t x[kTokens][16];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
-      const float amax = __uint_as_float(max(m2 & 0xFFFFu, m2 >> 16) << 16);
-      if (g > 0.0f) sb = cvt_e4m3(__fdiv_rn(amax, __fmul_rn(6.0f, g)));
-      uint64_t c = 0;
-      if (sb != 0 && sb != 0x7Fu) c = encode16(w, fminf(__frcp_rn(__fmul_rn(e4m3_to_f32(sb), g)), FLT_MAX));
-      *reinterpret_cast<uint2 *>(codes + oc + blk * 8) = make_uint2((uint32_t)c, (uint32_t)(c >> 32));
+    for (int i = 0; i < kTokens; ++i) {
+      const int64_t t = (w.group * kTokens + i) * kRows + lane / kLanes;
+      on[i] = t < p.tokens && kv_at(p.c, __ldg(p.slots + t), w.head, oc[i], os[i]);
+      if (on[i]) {
+        if (wide)
+          load32<true>(src + t * ld + w.head * hld, x[i]);
+        else
+          load32<false>(src + t * ld + w.head * hld, x[i]);
+      }
     }
-    uint32_t v = sb;
-    v |= __shfl_down_sync(0xffffffffu, sb, 1) << 8;
-    v |= __shfl_down_sync(0xffffffffu, sb, 2) << 16;
-    v |= __shfl_down_sync(0xffffffffu, sb, 3) << 24;
-    if (on && (blk & 3) == 0) *reinterpret_cast<uint32_t *>(sf + os + blk) = v;
+    const float g = (val ? p.gv : p.gk)[w.head], g6 = __fmul_rn(6.0f, g);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      uint32_t sb2 = 0;
+      if (on[i]) {
+        uint64_t c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t b[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) b[e] = x[i][8 * k + e];
+          uint32_t m2 = b[0] & 0x7FFF7FFFu;
+#pragma unroll
+          for (int e = 1; e < 8; ++e) m2 = __vmaxu2(m2, b[e] & 0x7FFF7FFFu);
+          const float amax = __uint_as_float(max(m2 & 0xFFFFu, m2 >> 16) << 16);
+          const uint32_t sb = g > 0.0f ? cvt_e4m3(__fdiv_rn(amax, g6)) : 0u;
+          c[k] = 0;
+          if (sb != 0 && sb != 0x7Fu) c[k] = encode16(b, fminf(__frcp_rn(__fmul_rn(e4m3_to_f32(sb), g)), FLT_MAX));
+          sb2 |= sb << (8 * k);
+        }
+        *reinterpret_cast<uint4 *>(codes + oc[i]) = make_uint4((uint32_t)c[0], (uint32_t)(c[0] >> 32), (uint32_t)c[1],
+                                                               (uint32_t)(c[1] >> 32));
+      }
+      sb2 |= __shfl_down_sync(0xffffffffu, sb2, 1) << 16;
+      if (on[i] && (q & 1) == 0) *reinterpret_cast<uint32_t *>(sf + os[i]) = sb2;
+    }
   }
 }
 
-template <int kLanes, bool kF32>
+template <int HD, bool kF32>
 __global__ void __launch_bounds__(256) k_kv_read(const KvCopyParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
-  constexpr int kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, blk = lane % kLanes;
+  constexpr int kLanes = HD / 32, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, q = lane % kLanes;
   const bool val = blockIdx.y != 0;
   const int64_t ld = val ? p.v_ld : p.k_ld, hld = val ? p.v_head_ld : p.k_head_ld;
-  const uint8_t *codes = val ? p.c.v_codes : p.c.k_codes, *sf = val ? p.c.v_sf : p.c.k_sf;
-  const int64_t items = (p.tokens + kRows - 1) / kRows * p.c.kv_heads;
-  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += nwarps) {
-    const int64_t t = it / p.c.kv_heads * kRows + lane / kLanes;
-    const int h = (int)(it % p.c.kv_heads);
-    int64_t oc = 0, os = 0;
-    if (!(t < p.tokens && kv_at(p.c, p.slots[t], h, oc, os))) continue;
-    const float s = __fmul_rn(e4m3_to_f32(__ldg(sf + os + blk)), (val ? p.gv : p.gk)[h]);
-    const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + oc) + blk);
-    uint32_t h2[2][4];
-    e2m1x8_to_h2(c.x, h2[0]);
-    e2m1x8_to_h2(c.y, h2[1]);
-    float f[16];
+  const uint8_t *codes = (val ? p.c.v_codes : p.c.k_codes) + q * 16, *sf = (val ? p.c.v_sf : p.c.k_sf) + q * 2;
+  for (KvWalk w(p, kRows * kTokens); w.on(); w.next()) {
+    uint4 c[kTokens];
+    uint32_t s2[kTokens];
+    bool on[kTokens];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h2[i >> 2][i & 3]));
-      f[2 * i] = __fmul_rn(x.x, s);
-      f[2 * i + 1] = __fmul_rn(x.y, s);
+    for (int i = 0; i < kTokens; ++i) {
+      const int64_t t = (w.group * kTokens + i) * kRows + lane / kLanes;
+      int64_t oc = 0, os = 0;
+      on[i] = t < p.tokens && kv_at(p.c, __ldg(p.slots + t), w.head, oc, os);
+      if (on[i]) {
+        c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + oc));
+        s2[i] = __ldg(reinterpret_cast<const uint16_t *>(sf + os));
+      }
     }
-    const int64_t at = t * ld + h * hld + blk * 16;
-    if (kF32) {
-      float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(val ? p.v : p.k) + at);
+    const float g = (val ? p.gv : p.gk)[w.head];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    } else {
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(val ? p.v : p.k) + at);
+    for (int i = 0; i < kTokens; ++i) {
+      if (!on[i]) continue;
+      const int64_t t = (w.group * kTokens + i) * kRows + lane / kLanes, at = t * ld + w.head * hld + q * 32;
+      const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      uint32_t o[16];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        dst[i] = make_uint4(pack_bf2(f[8 * i], f[8 * i + 1]), pack_bf2(f[8 * i + 2], f[8 * i + 3]),
-                            pack_bf2(f[8 * i + 4], f[8 * i + 5]), pack_bf2(f[8 * i + 6], f[8 * i + 7]));
+      for (int k = 0; k < 4; ++k) {
+        const float s = __fmul_rn(e4m3_to_f32(s2[i] >> (8 * (k >> 1))), g);
+        uint32_t h2[4];
+        e2m1x8_to_h2(cw[k], h2);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h2[e]));
+          f[2 * e] = __fmul_rn(v.x, s);
+          f[2 * e + 1] = __fmul_rn(v.y, s);
+        }
+        if constexpr (kF32) {
+          float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(val ? p.v : p.k) + at) + 2 * k;
+          dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+          dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[4 * k + e] = pack_bf2(f[2 * e], f[2 * e + 1]);
+        }
+      }
+      if constexpr (!kF32) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(val ? p.v : p.k) + at);
+        if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            st_global_v8(dst + 2 * k, o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3], o[8 * k + 4], o[8 * k + 5],
+                         o[8 * k + 6], o[8 * k + 7]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
     }
   }
 }
 
 dim3 kv_grid(const KvCopyParams &p, int num_sms) {
-  const int64_t rows = 512 / p.c.head_dim;   // tokens per warp
-  const int64_t warps = (p.tokens + rows - 1) / rows * p.c.kv_heads;
+  const int64_t tokens = 32 / (p.c.head_dim / 32) * kTokens;   // of a warp at a time
+  const int64_t warps = (p.tokens + tokens - 1) / tokens * p.c.kv_heads;
   return dim3((unsigned)std::min<int64_t>((warps + 7) / 8, (int64_t)num_sms * 4), 2);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_write(const KvCopyParams &p, int num_sms, cudaStream_t st) {
-  return p.c.head_dim == 128 ? launch_pdl(k_kv_write<8>, kv_grid(p, num_sms), dim3(256), 0, st, p)
-                             : launch_pdl(k_kv_write<4>, kv_grid(p, num_sms), dim3(256), 0, st, p);
+  return p.c.head_dim == 128 ? launch_pdl(k_kv_write<128>, kv_grid(p, num_sms), dim3(256), 0, st, p)
+                             : launch_pdl(k_kv_write<64>, kv_grid(p, num_sms), dim3(256), 0, st, p);
 }
 
 cudaError_t launch_kv_read(const KvCopyParams &p, bool fp32, int num_sms, cudaStream_t st) {
   const dim3 g = kv_grid(p, num_sms), b(256);
   if (p.c.head_dim == 128)
-    return fp32 ? launch_pdl(k_kv_read<8, true>, g, b, 0, st, p) : launch_pdl(k_kv_read<8, false>, g, b, 0, st, p);
-  return fp32 ? launch_pdl(k_kv_read<4, true>, g, b, 0, st, p) : launch_pdl(k_kv_read<4, false>, g, b, 0, st, p);
+    return fp32 ? launch_pdl(k_kv_read<128, true>, g, b, 0, st, p) : launch_pdl(k_kv_read<128, false>, g, b, 0, st, p);
+  return fp32 ? launch_pdl(k_kv_read<64, true>, g, b, 0, st, p) : launch_pdl(k_kv_read<64, false>, g, b, 0, st, p);
 }
 
 }  // namespace nvfp4
