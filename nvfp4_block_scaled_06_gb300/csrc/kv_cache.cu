@@ -64,7 +64,7 @@ struct KvWalk {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(256) k_kv_write(const KvCopyParams p) {
+__global__ void __launch_bounds__(256, 3) k_kv_write(const KvCopyParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   constexpr int kLanes = HD / 32, kRows = 32 / kLanes;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) k_kv_write(const KvCopyParams p) {
 }
 
 template <int HD, bool kF32>
-__global__ void __launch_bounds__(256) k_kv_read(const KvCopyParams p) {
+__global__ void __launch_bounds__(256, 6) k_kv_read(const KvCopyParams p) {
   griddep_launch_dependents();
   griddep_wait();   // inputs may come from the previous kernel in the stream
   constexpr int kLanes = HD / 32, kRows = 32 / kLanes;
@@ -185,21 +185,22 @@ __global__ void __launch_bounds__(256) k_kv_read(const KvCopyParams p) {
   }
 }
 
-dim3 kv_grid(const KvCopyParams &p, int num_sms) {
+// CTAs for half of `per_sm` on each SM in each of the two rows of the grid: one wave.
+dim3 kv_grid(const KvCopyParams &p, int num_sms, int per_sm) {
   const int64_t tokens = 32 / (p.c.head_dim / 32) * kTokens;   // of a warp at a time
   const int64_t warps = (p.tokens + tokens - 1) / tokens * p.c.kv_heads;
-  return dim3((unsigned)std::min<int64_t>((warps + 7) / 8, (int64_t)num_sms * 4), 2);
+  return dim3((unsigned)std::min<int64_t>((warps + 7) / 8, std::max<int64_t>(1, (int64_t)num_sms * per_sm / 2)), 2);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_write(const KvCopyParams &p, int num_sms, cudaStream_t st) {
-  return p.c.head_dim == 128 ? launch_pdl(k_kv_write<128>, kv_grid(p, num_sms), dim3(256), 0, st, p)
-                             : launch_pdl(k_kv_write<64>, kv_grid(p, num_sms), dim3(256), 0, st, p);
+  return p.c.head_dim == 128 ? launch_pdl(k_kv_write<128>, kv_grid(p, num_sms, 3), dim3(256), 0, st, p)
+                             : launch_pdl(k_kv_write<64>, kv_grid(p, num_sms, 3), dim3(256), 0, st, p);
 }
 
 cudaError_t launch_kv_read(const KvCopyParams &p, bool fp32, int num_sms, cudaStream_t st) {
-  const dim3 g = kv_grid(p, num_sms), b(256);
+  const dim3 g = kv_grid(p, num_sms, 6), b(256);
   if (p.c.head_dim == 128)
     return fp32 ? launch_pdl(k_kv_read<128, true>, g, b, 0, st, p) : launch_pdl(k_kv_read<128, false>, g, b, 0, st, p);
   return fp32 ? launch_pdl(k_kv_read<64, true>, g, b, 0, st, p) : launch_pdl(k_kv_read<64, false>, g, b, 0, st, p);
