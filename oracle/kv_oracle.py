@@ -30,7 +30,7 @@ def values(codes: np.ndarray, sf: np.ndarray, g: np.ndarray) -> np.ndarray:
 
 
 def gather(codes, sf, g, table, n: int, page: int):
-    """[n, heads, hd] values of a sequence (keys of pages outside the cache: NaN mask False) and their mask."""
+    """[n, heads, hd] values of a sequence and a mask that leaves out keys of pages outside the cache."""
     j = np.arange(n)
     ids = table[j // page].astype(np.int64) if n else np.zeros(0, np.int64)
     ok = (ids >= 0) & (ids < codes.shape[0])
@@ -59,6 +59,9 @@ def attention(q, k, v, ok, pos, scale: float, causal: bool, window: int):
         for h in range(Hq):
             kk, vv = k[see, h // G], v[see, h // G]
             s = scale * (kk @ q[r, h])
+            if np.isnan(s).any():
+                out[r, h], lse[r, h] = np.nan, np.nan
+                continue
             m = s.max()
             e = np.exp(s - m)
             w = e / e.sum()

@@ -183,15 +183,19 @@ class Case:
             w_out, w_lse, S, V, qk = ko.attention(q, k, v, ok, n - nq + np.arange(nq), scale, causal, window)
             y = out[r0:r0 + nq].double().cpu().numpy()
             z = lse[r0:r0 + nq].double().cpu().numpy()
-            empty = np.isinf(w_lse)
+            empty, undefined = np.isinf(w_lse), np.isnan(w_out)
             assert np.array_equal(np.isneginf(z), empty), what
             assert np.all(y[empty] == 0)
+            assert np.array_equal(np.isnan(y), undefined), what
+            assert np.array_equal(np.isnan(z), np.isnan(w_lse)), what
+            empty, y, w_out = empty | np.isnan(w_lse), np.where(undefined, 0, y), np.where(undefined, 0, w_out)
             s_max = np.where(empty, 0, np.abs(w_lse) + np.log(max(n, 2)))
             d = (self.hd / 16 + 2) * 2.0 ** -22 * scale * qk + 2.0 ** -22 * (s_max + 2)
-            assert np.all(np.abs(z - w_lse)[~empty] <= (d + 2.0 ** -21 * (np.abs(w_lse) + 2))[~empty]), what
+            s_max, d = np.where(empty, 0, s_max), np.where(empty, 0, d)
+            assert np.all(np.abs(z[~empty] - w_lse[~empty]) <= (d + 2.0 ** -21 * (np.abs(w_lse) + 2))[~empty]), what
             tol = ((2.0 ** -11 + 2 * d[..., None] + (n / 16 + 2) * 2.0 ** -22) * S + 2.0 ** -25 * V
                    + 2.0 ** -8 * np.abs(w_out))
-            bad = ~(np.abs(y - w_out) <= tol * 1.0001 + 1e-30)
+            bad = ~(np.abs(y - w_out) <= tol * 1.0001 + 1e-30) & ~undefined
             assert not bad.any(), (what, b, np.argwhere(bad)[:4], y[bad][:4], w_out[bad][:4], tol[bad][:4])
 
 
