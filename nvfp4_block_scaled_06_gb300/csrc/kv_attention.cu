@@ -171,41 +171,49 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   Line line;
   int64_t total;
   {
-    const Seg seg0 = seg_of(p, min(b0, p.seqs - 1));
-    auto seg = [&](int b) { return b == b0 ? seg0 : seg_of(p, b); };
-    int64_t units = 0;
-    for (int b = b0; b < b1; ++b) units += seg(b).units;
+    // (passes over the same loop, for little code: what runs once waits for the instruction cache)
+    int64_t units = 0, sum = 0, base = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+#pragma unroll 1
+      for (int b = b0; b < b1; ++b) {
+        const Seg g2 = seg_of(p, b);
+        if (pass == 0) {
+          units += g2.units;
+        } else {
+          if (pass == 2 && (per == 1 || b % per == 0)) pre[per == 1 ? b : b / per] = base;
+          const int64_t places = (int64_t)line.items(p, g2) * line.places(g2);
+          sum += places;
+          base += places;
+        }
+      }
+      if (pass == 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-    if (lane == 0) wsum[0][warp] = units;
-    __syncthreads();
-    units = 0;
-    for (int w = 0; w < kWarps; ++w) units += wsum[0][w];
-    // four heads of a sequence are at most a span of the units
-    line.solo = p.kv_heads < kWarps ? 0 : (int)min(kv_div(units * p.kv_heads, (int64_t)gridDim.x * kWarps), (int64_t)kSoloMost);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const Seg g2 = seg(b);
-      sum += (int64_t)line.items(p, g2) * line.places(g2);
-    }
-    int64_t scan = sum;
+        for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+        if (lane == 0) wsum[0][warp] = units;
+        __syncthreads();
+        units = 0;
+        for (int w = 0; w < kWarps; ++w) units += wsum[0][w];
+        // four heads of a sequence are at most a span of the units
+        line.solo = p.kv_heads < kWarps
+                        ? 0
+                        : (int)min(kv_div(units * p.kv_heads, (int64_t)gridDim.x * kWarps), (int64_t)kSoloMost);
+      } else if (pass == 1) {
+        int64_t scan = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += v;
-    }
-    if (lane == 31) wsum[1][warp] = scan;
-    __syncthreads();
-    int64_t base = scan - sum;
-    total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) base += wsum[1][w];
-      total += wsum[1][w];
-    }
-    for (int b = b0; b < b1; ++b) {
-      if (b % per == 0) pre[b / per] = base;
-      const Seg g2 = seg(b);
-      base += (int64_t)line.items(p, g2) * line.places(g2);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+          if (lane >= o) scan += v;
+        }
+        if (lane == 31) wsum[1][warp] = scan;
+        __syncthreads();
+        base = scan - sum;
+        total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) base += wsum[1][w];
+          total += wsum[1][w];
+        }
+      }
     }
     __syncthreads();
   }
@@ -276,7 +284,6 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   auto settle = [&] {                               // on to this warp's next unit, where it has none left here
     while (more && ahead.u >= ahead.end) more = ahead.next(p, line, warp);
   };
-  settle();
   // Copies of the unit at `ahead` into a stage; keys outside [0, n) and pages
   // outside the cache are zero-filled and left out by their limits.  (Kept to
   // few instructions: address arithmetic once took half of a unit's time.)
@@ -323,10 +330,10 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
     if (lane == 0) limits[warp][stage] = l0 | l1 << 8;
   };
   auto fetch = [&](int stage) {
+    settle();
     if (more) {
       copy_unit(stage);
       ahead.u += ahead.step;
-      settle();
     }
     cp_async_commit();
   };
