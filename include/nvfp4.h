@@ -21,7 +21,8 @@
  * Conventions shared by every entry point:
  *   - Every pointer is caller-owned DEVICE memory unless stated otherwise; the
  *     library never allocates.  Scratch space is the caller's `workspace`,
- *     sized with the matching *_workspace_bytes query, 256-byte aligned; its
+ *     sized with the matching *_workspace_bytes query (the attention over a
+ *     cache: nvfp4_kv_attention_workspace_size), 256-byte aligned; its
  *     first 4 bytes (the device status word) must be zero before first use.
  *     Calls that share a workspace must be ordered (same stream).
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t; 0 = the
@@ -734,7 +735,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
  *   out = sum_j softmax_j(s) V_j,  lse = ln sum_j exp(s_j)
  * A query that sees no key gets zeros and lse = -inf.  Scores and sums are
  * fp32; K and V enter the products exactly, q too (to 2^-28 of its row's
- * largest magnitude), the softmax's numerators rounded to f16; out is rounded
+ * largest magnitude), the softmax's numerators rounded to f16 (zero below 2^-29
+ * of the largest among the row's first keys); out is rounded
  * to bf16 once.  What a query does not see does not reach it, NaN neither;
  * scores are finite for finite inputs below 2^100.
  *   Device data are clamped, not checked: offsets to [0, total_q] and ascending
@@ -779,7 +781,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_attention_args *args, nvfp4_strea
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_attention_args *args);
 
 /* ------------------------------------------------------------------------ *
- * Size queries and status.  (The *_workspace_bytes queries above answer 0 for
+ * Size queries and status.  (The workspace queries above answer 0 for
  * NULL and for sizes below 1, which their calls refuse.)
  * ------------------------------------------------------------------------ */
 /* Bytes of packed codes of a [rows][cols] matrix: rows * cols / 2. */

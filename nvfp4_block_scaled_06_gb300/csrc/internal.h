@@ -336,7 +336,8 @@ struct KvAttnParams {
   uint64_t timeout_ns;
   int stall_probe;                   // test hook: first wait on a barrier nothing arrives at
 };
-// Few rows (8 * nt, nt up to 3) per sequence and key-value head.  Spans: CTAs of the kernel.
+// Few rows (8 * nt, nt up to 3) per sequence and key-value head.  Spans: CTAs of the
+// kernel, per SM as many as its registers leave room for (one fewer: no gain).
 constexpr int kv_few_ctas(int head_dim, int nt) { return nt == 1 ? (head_dim == 64 ? 4 : 3) : 2; }   // per SM
 int kv_few_spans(int head_dim, int nt, int num_sms);
 cudaError_t launch_kv_few(const KvAttnParams &p, int head_dim, int nt, int num_sms, cudaStream_t st);

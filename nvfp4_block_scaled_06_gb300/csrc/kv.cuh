@@ -47,6 +47,12 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// ln(l 2^m): log2 is taken of l's mantissa, where its error is least (2^-22).
+__device__ __forceinline__ float kv_lse(float m, float l) {
+  const int e = min((int)(__float_as_uint(l) >> 23), 253) - 127;   // (NaN and infinity stay what they are)
+  return (m + (float)e + __log2f(l * __uint_as_float((uint32_t)(127 - e) << 23))) * 0.693147181f;
+}
+
 // A sequence's sizes as the kernels use them.  q_offsets and kv_lens are device
 // data that the host cannot check: offsets are clamped to [0, total_q] and to
 // ascending order, lengths to the page table's width, so inconsistent ones give

@@ -19,9 +19,10 @@
 // P is rounded to f16 (2^-11 relative, half of what bf16 results keep), sums and
 // accumulators are fp32.
 //
-// The reference m is raised only when a score exceeds it by more than 8 (in
-// units of log2): P stays below 2^8, and the usual step needs no reduction
-// over lanes and no rescaling.
+// The reference m is 7 (in units of log2) below the row's maximum and is raised
+// only when a score exceeds it by more than 15: P stays below 2^15, keys count
+// down to 2^-32 of the maximum (f16 ends at 2^-25), and the usual step needs no
+// reduction over lanes and no rescaling.
 //
 // Work: a line of items, cut into equal spans, one per CTA.  An item is a
 // (sequence, head) with its 32-key units, which the span's warps take in turn and
@@ -30,6 +31,12 @@
 // sequences are short against a span an item is four heads of one, a warp each,
 // with nothing to join.  A warp's ring of asynchronous copies runs on over the
 // items' borders.
+//
+// Measured (calls, cold L2): 4 x 131072 keys of 8 heads 123 us, 4.9 TB/s (6 in its
+// steady state, 7 us of start); 32 ragged contexts up to 8192 35 us; 256 up to
+// 1024 of 16 heads of 64 58 us.  26 instructions per key and head at head_dim 128
+// with 8 rows, half of the issue slots: between HBM and the cores, where contexts
+// are short the start's latency.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -45,9 +52,16 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kMaxEntries = 256;    // prefix entries held in shared memory
 constexpr int kKeys = 32;           // of a unit: two 16-key tiles of the MMA, each in one page
-constexpr int kOver = 8;            // what an item costs beside its units, in units
-constexpr int kSoloMost = 32;       // units of a sequence whose heads may go to one warp each
-constexpr float kRaise = 8.0f;
+// What an item costs beside its units, in units (2 or 4: slower for 256 short
+// sequences, nothing gained on long ones).
+constexpr int kOver = 8;
+// Units of a sequence whose heads may go to one warp each.  Beyond, and where four
+// heads are more than a span, the warps share a head: 256 sequences up to 1024 keys
+// take 57 us with the rule and 64 to 72 with the bound at a half or a quarter of a
+// span, 256 of 16 keys 19 us and 41 with shared heads.
+constexpr int kSoloMost = 32;
+constexpr float kLift = 7.0f;       // log2 of the numerator at the maximum
+constexpr float kRaise = kLift + 8.0f;
 
 template <int HD, int NT>
 struct Few {
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
       ids = ids_at + lane < p.max_pages ? __ldg(p.table + (int64_t)ids_b * p.table_ld + ids_at + lane) : -1;
     }
     const int id = __shfl_sync(0xffffffffu, ids, page & 31);
-    const bool in = key < ahead.g.s.n && NVFP4_NOTE((uint32_t)id < (uint32_t)p.num_pages, p.status);
+    const bool in = key < ahead.g.s.n && (uint32_t)id < (uint32_t)p.num_pages;
     const int row = (ahead.h << p.page_shift) + (key & page_mask);
     const int64_t oc = in ? id * p.codes_stride + row * (HD / 2) : 0;
     const int64_t os = in ? id * p.sf_stride + row * (HD / 16) : 0;
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
             float x = top[nt][k];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            const float m2 = fmaxf(m[nt][k], x);
+            const float m2 = fmaxf(m[nt][k], x - kLift);
             const float f = m2 == m[nt][k] ? 1.0f : ex2(m[nt][k] - m2);
             m[nt][k] = m2;
             l[nt][k] *= f;
@@ -617,7 +631,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
                                 pack_bf2(o[4 * j + 1][nt][k] * f, o[4 * j + 1][nt][k + 2] * f),
                                 pack_bf2(o[4 * j + 2][nt][k] * f, o[4 * j + 2][nt][k + 2] * f),
                                 pack_bf2(o[4 * j + 3][nt][k] * f, o[4 * j + 3][nt][k + 2] * f));
-          if (p.lse && g == 0) p.lse[q * p.kv_heads * p.group + head] = (m[nt][k] + __log2f(sum_l)) * CUDART_LN2_F;
+          if (p.lse && g == 0) p.lse[q * p.kv_heads * p.group + head] = kv_lse(m[nt][k], sum_l);
         }
     } else {
     // --------------------------------------------------- the warps' results, joined --
@@ -665,7 +679,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         *reinterpret_cast<uint4 *>(p.out + q * p.out_ld + (int64_t)head * p.out_head_ld + c) =
             make_uint4(pack_bf2(y[0] * f, y[1] * f), pack_bf2(y[2] * f, y[3] * f), pack_bf2(y[4] * f, y[5] * f),
                        pack_bf2(y[6] * f, y[7] * f));
-        if (p.lse && c == 0) p.lse[q * p.kv_heads * p.group + head] = (mm + __log2f(ll)) * CUDART_LN2_F;
+        if (p.lse && c == 0) p.lse[q * p.kv_heads * p.group + head] = kv_lse(mm, ll);
       } else {
         float4 *dst = reinterpret_cast<float4 *>(p.part_o + (slot * F::kRows + r) * HD + c);
         dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -692,7 +706,7 @@ __global__ void __launch_bounds__(256) k_kv_sum(const KvAttnParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
-  const int4 bd = __ldg(p.few_borders + blockIdx.x + 1);
+  const int4 bd = p.few_borders[blockIdx.x + 1];
   if (bd.x < 0) return;
   const int c0 = blockIdx.x, c1 = bd.z, h = bd.y;
   const KvSeq s = kv_seq(p, bd.x);
@@ -751,7 +765,7 @@ __global__ void __launch_bounds__(256) k_kv_sum(const KvAttnParams p) {
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf2(o[0] * f, o[1] * f), pack_bf2(o[2] * f, o[3] * f));
   else
     *reinterpret_cast<uint32_t *>(dst) = pack_bf2(o[0] * f, o[1] * f);
-  if (p.lse && lane == 0) p.lse[q * p.kv_heads * p.group + head] = (mm + __log2f(ll)) * CUDART_LN2_F;
+  if (p.lse && lane == 0) p.lse[q * p.kv_heads * p.group + head] = kv_lse(mm, ll);
 }
 
 template <int HD, int NT>

@@ -11,7 +11,10 @@
 // channels (64 bytes of bf16, 16 of codes, two scales) of two tokens at a time,
 // all loads first; a warp consecutive tokens of one head, whose codes are one run
 // of a page where the slots are consecutive, while consecutive warps take the
-// heads of the same tokens, whose bf16 rows are neighbours.
+// heads of the same tokens, whose bf16 rows are neighbours.  65521 tokens of 16
+// heads of 64: the write 65 us for 344 MB (5.3 TB/s, cold), the read 55 us
+// (6.2 TB/s); a call of both 125 us in grids of one wave, 133 with a warp's items
+// spread over more CTAs.
 #include <float.h>
 
 #include "encode.cuh"

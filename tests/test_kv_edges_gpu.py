@@ -128,6 +128,30 @@ def test_growing_scores(qlens, G, hd, shape):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("qn,G", [(1, 4), (3, 8), (40, 8)])
+def test_many_keys_far_below_the_largest(qn, G):
+    """65535 keys of 2^-27 each beside one of 1 are a 2^-11 part of the sum, and of the result too.
+    Tolerance: f16 holds the numerators, lifted by 2^4 or more, exactly up to the scores' error (2^-18, then
+    half a step of the smallest f16 rounds it away); sums over 2^12 steps of 2^-22; bf16's half step 2^-8."""
+    n, pages = 65536, 1024
+    one = torch.ones(1, device="cuda")
+    cache = nv.nvfp4_kv_cache(pages, 1, 64, 64)
+    k = torch.zeros((n, 1, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[1:, 0, 0], v[1:] = -27.0, 6.0
+    nv.nvfp4_kv_write(k, v, torch.arange(n, device="cuda"), cache, one, one)
+    q = torch.zeros((qn, G, 64), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out, lse = nv.nvfp4_kv_attention(q, cache, one, one, table, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                     q_offsets=torch.tensor([0, qn], dtype=torch.int32, device="cuda"), max_q_len=qn,
+                                     scale=float(np.log(2.0)), causal=False, want_lse=True)
+    part = (n - 1) * 2.0 ** -27
+    want = 6.0 * part / (1 + part)
+    assert float((out.double() - want).abs().max()) <= (2.0 ** -8 + 2.0 ** -9) * want
+    assert float((lse.double() - np.log1p(part)).abs().max()) <= 2.0 ** -18
+
+
 def test_extreme_queries():
     """Rows of tiny, huge and zero queries, and an infinity and a NaN in rows of their own."""
     c = Case([200, 90], [40, 1], 2, 4, 128, 16)
