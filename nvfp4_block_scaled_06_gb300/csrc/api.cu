@@ -1906,6 +1906,11 @@ void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
   const int64_t few = rows <= 24 ? rows : group;      // beyond: single tokens' rows
   pl->nt = few <= 24 ? (int)ceil_div(few, 8) : 0;
   pl->prompt = rows > 8 * pl->nt;
+  // Where offsets that cover q leave every sequence more rows than few, the kernel for
+  // few (which finds nothing to do in 5 us) is left out; should they not cover it,
+  // the other takes what there is.
+  const int64_t least = a->q_offsets ? a->total_q - (a->num_seqs - 1) * std::min(a->max_q_len, a->total_q) : 1;
+  if (pl->prompt && least > 0 && least * group > 8 * pl->nt) pl->nt = 0;
   const int sms = plan_sms();
   Carve c(a->workspace);
   if (pl->nt > 0) {

@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
     __syncthreads();
   }
 
-  const KvCut cut(total, gridDim.x);
+  // (a warp has a unit at least: spans of a place each take 1 us more for the sum of one sequence's 1021 keys)
+  const KvCut cut(total, min((int64_t)gridDim.x, max(total / kWarps, (int64_t)1)));
   const int64_t span = blockIdx.x;
   if (span >= cut.spans) {
     if (tid == 0) p.few_borders[span] = make_int4(-1, 0, 0, 0);

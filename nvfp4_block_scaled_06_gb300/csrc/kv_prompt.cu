@@ -25,8 +25,8 @@
 // fill the GPU; segments in several spans leave partial (o, m, l), joined in
 // order by a second kernel.  A first kernel lists the row tiles.
 //
-// Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 810 us = 1.33 PFLOP/s
-// (69% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 274 us = 1.0.  A
+// Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 794 us = 1.36 PFLOP/s
+// (71% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 266 us = 1.0.  A
 // key tile takes 3470 cycles: a half's softmax about 1950 and its MMAs' wait and
 // issue 1430 in turn, the other half beside it; the tensor pipe is busy 53%.
 #include <float.h>
@@ -239,7 +239,7 @@ struct Walk {
   int left, r;              // units of the span from the segment's place r on
   bool two;                 // rows in both halves
   __device__ __forceinline__ void load(const KvAttnParams &p) {
-    const int4 it = __ldg(p.items + item);
+    const int4 it = p.items[item];
     seq = it.x;
     tile = it.y;
     t0 = it.z;
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
                 tc_fence_after();
                 const uint64_t b = vd + (uint32_t)(st * (T::kHalf >> 4));
                 const uint32_t d = T::kO + half * HD, a = half * 128;
-#pragma unroll 8
+#pragma unroll 4
                 for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, a + k * 8, b + k * 128, id_o, j > w.j0 || k ? 1u : 0u);
               } else {
                 if (!(ok = twait(q_ready + 8 * half, (q_seen >> half) & 1))) break;
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
                   tc_fence_after();
                 }
                 const uint64_t a = qd + (uint32_t)(half * (T::kHalf >> 4)), b = kd + (uint32_t)(next * (T::kHalf >> 4));
-#pragma unroll 8
+#pragma unroll 4
                 for (int k = 0; k < HD / 16; ++k)
                   tc_mma_bf16(half * 128, a + ((k >> 2) * 1024 + (k & 3) * 2), b + ((k >> 2) * 1024 + (k & 3) * 2), id_s, k ? 1u : 0u);
                 tc_commit_u(s_ready + 8 * half);
