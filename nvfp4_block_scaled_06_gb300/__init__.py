@@ -892,7 +892,8 @@ def prepare_kv_attention(q, cache, k_global_scale, v_global_scale, page_table, k
     known (rows beyond it are not computed).  scale: 1/sqrt(head_dim) by default;
     causal: query at position p sees keys up to p, with window w only the last w
     of them.  Returns (Prepared call, (out bf16 [rows, heads, head_dim], lse fp32
-    [rows, heads] or None)); a query without keys gets zeros and -inf."""
+    [rows, heads] or None)); a query without keys gets zeros and -inf, rows of no
+    sequence stay as they are (out given) or are undefined."""
     lib = load()
     c, keep = _kv_pages(cache, k_global_scale, v_global_scale)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:

@@ -60,6 +60,7 @@ constexpr int kOver = 8;
 // take 57 us with the rule and 64 to 72 with the bound at a half or a quarter of a
 // span, 256 of 16 keys 19 us and 41 with shared heads.
 constexpr int kSoloMost = 32;
+constexpr int kSumWarps = 8;        // of a block that adds up partial results
 constexpr float kLift = 7.0f;       // log2 of the numerator at the maximum
 constexpr float kRaise = kLift + 8.0f;
 
@@ -696,77 +697,113 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
   cp_async_wait<0>();
 }
 
-// Segments that lie in several spans: block = (border between two spans, row);
-// the border behind a segment's first span stands for it.  The spans' partial
-// results are dealt to the block's warps in order.
-template <int HD, int NT>
-__global__ void __launch_bounds__(256) k_kv_sum(const KvAttnParams p) {
-  constexpr int kRows = 8 * NT, kV = HD / 32, kW = 8;
-  __shared__ float sh_o[kW][HD];
-  __shared__ float2 sh_ml[kW];
+// Segments that lie in several spans: block = (border between two spans, rows);
+// the border behind a segment's first span stands for it.  A row's partial results
+// are added in order by W warps: one, eight results at a time, where items have
+// few (256 short sequences 57.5 -> 53 us, 16 x 5 drafted tokens 44 -> 41.5: most
+// blocks find no border, fewer of them end sooner), or the block's eight (one
+// sequence of 131072 keys 44 us, 58 with one warp; 4 of them 123 and 125).
+template <int HD, int NT, int W>
+__global__ void __launch_bounds__(kSumWarps * 32) k_kv_sum(const KvAttnParams p) {
+  static_assert(W == 1 || W == kSumWarps);
+  constexpr int kRows = 8 * NT, kV = HD / 32, kBatch = 8;
+  __shared__ float sh_o[W > 1 ? kSumWarps : 1][HD];
+  __shared__ float2 sh_ml[kSumWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = W > 1 ? blockIdx.y : blockIdx.y * kSumWarps + warp;
   const int4 bd = p.few_borders[blockIdx.x + 1];
   if (bd.x < 0) return;
   const int c0 = blockIdx.x, c1 = bd.z, h = bd.y;
   const KvSeq s = kv_seq(p, bd.x);
-  if (r >= s.qn * p.group) return;
+  if (r >= s.qn * p.group) return;                  // (the whole block, or a warp that waits for no other)
   auto row_of = [&](int c) { return (2ll * c + (c == c0 ? bd.w : 0)) * kRows + r; };
-  // this warp's spans: c0 + warp, kW apart; their maximum and sum first, so that the rows' loads are independent
   float m = -CUDART_INF_F, l = 0.0f, o[kV];
-  for (int c = c0 + warp + lane * kW; c <= c1; c += 32 * kW)
-    m = fmaxf(m, __ldg(reinterpret_cast<const float2 *>(p.part_ml) + row_of(c)).x);
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float top = m == -CUDART_INF_F ? 0.0f : m;
 #pragma unroll
   for (int v = 0; v < kV; ++v) o[v] = 0.0f;
-#pragma unroll 8
-  for (int c = c0 + warp; c <= c1; c += kW) {
+  // partial result c of the row
+  auto load = [&](int c, float2 &ml, float (&y)[kV]) {
     const int64_t row = row_of(c);
-    const float2 ml = __ldg(reinterpret_cast<const float2 *>(p.part_ml) + row);
+    ml = reinterpret_cast<const float2 *>(p.part_ml)[row];
     const float *src = p.part_o + row * HD + lane * kV;
-    float y[kV];
     if constexpr (kV == 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(src));
+      const float4 v = *reinterpret_cast<const float4 *>(src);
       y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
     } else {
-      const float2 v = __ldg(reinterpret_cast<const float2 *>(src));
+      const float2 v = *reinterpret_cast<const float2 *>(src);
       y[0] = v.x; y[1] = v.y;
     }
-    const float f = ex2(ml.x - top);
-    l += ml.y * f;
+  };
+  if constexpr (W == 1) {
+#pragma unroll 1
+    for (int c = c0; c <= c1; c += kBatch) {
+      float2 ml[kBatch];
+      float y[kBatch][kV], top = m;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) o[v] += y[v] * f;
-  }
+      for (int i = 0; i < kBatch; ++i) load(min(c + i, c1), ml[i], y[i]);
 #pragma unroll
-  for (int v = 0; v < kV; ++v) sh_o[warp][lane * kV + v] = o[v];
-  if (lane == 0) sh_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  if (warp != 0) return;
-  float mm = -CUDART_INF_F, ll = 0.0f;
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);   // (the last one's again at most)
+      const float ref = top == -CUDART_INF_F ? 0.0f : top, f0 = ex2(m - ref);
+      m = top;
+      l *= f0;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) mm = fmaxf(mm, sh_ml[w].x);
-  const float ref = mm == -CUDART_INF_F ? 0.0f : mm;
+      for (int v = 0; v < kV; ++v) o[v] *= f0;
 #pragma unroll
-  for (int v = 0; v < kV; ++v) o[v] = 0.0f;
+      for (int i = 0; i < kBatch; ++i) {
+        if (c + i > c1) break;
+        const float f = ex2(ml[i].x - ref);
+        l += ml[i].y * f;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    const float f = ex2(sh_ml[w].x - ref);
-    ll += sh_ml[w].y * f;
+        for (int v = 0; v < kV; ++v) o[v] += y[i][v] * f;
+      }
+    }
+  } else {
+    // this warp's: c0 + warp, W apart; their maximum first, so that the rows' loads are independent
+    for (int c = c0 + warp + lane * W; c <= c1; c += 32 * W)
+      m = fmaxf(m, reinterpret_cast<const float2 *>(p.part_ml)[row_of(c)].x);
 #pragma unroll
-    for (int v = 0; v < kV; ++v) o[v] += sh_o[w][lane * kV + v] * f;
+    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float top = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll 8
+    for (int c = c0 + warp; c <= c1; c += W) {
+      float2 ml;
+      float y[kV];
+      load(c, ml, y);
+      const float f = ex2(ml.x - top);
+      l += ml.y * f;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[v] += y[v] * f;
+    }
+#pragma unroll
+    for (int v = 0; v < kV; ++v) sh_o[warp][lane * kV + v] = o[v];
+    if (lane == 0) sh_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp != 0) return;
+    m = -CUDART_INF_F;
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, sh_ml[w].x);
+    const float ref = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) o[v] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = ex2(sh_ml[w].x - ref);
+      l += sh_ml[w].y * f;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[v] += sh_o[w][lane * kV + v] * f;
+    }
   }
   const int64_t q = s.q0 + r / p.group;
   const int head = h * p.group + r % p.group;
-  const float f = ll == 0.0f ? 0.0f : p.gv[h] / ll;
+  const float f = l == 0.0f ? 0.0f : p.gv[h] / l;
   __nv_bfloat16 *dst = p.out + q * p.out_ld + (int64_t)head * p.out_head_ld + lane * kV;
   if constexpr (kV == 4)
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf2(o[0] * f, o[1] * f), pack_bf2(o[2] * f, o[3] * f));
   else
     *reinterpret_cast<uint32_t *>(dst) = pack_bf2(o[0] * f, o[1] * f);
-  if (p.lse && lane == 0) p.lse[q * p.kv_heads * p.group + head] = kv_lse(mm, ll);
+  if (p.lse && lane == 0) p.lse[q * p.kv_heads * p.group + head] = kv_lse(m, l);
 }
 
 template <int HD, int NT>
@@ -777,7 +814,11 @@ cudaError_t run_few(const KvAttnParams &p, int num_sms, cudaStream_t st) {
   const int ctas = num_sms * F::kCtas;
   if (cudaError_t e = launch_pdl(k_kv_few<HD, NT>, dim3(ctas), dim3(kWarps * 32), F::kSmem, st, p); e != cudaSuccess)
     return e;
-  return launch_pdl(k_kv_sum<HD, NT>, dim3(ctas - 1, std::min(F::kRows, p.few_rows_most)), dim3(256), 0, st, p);
+  const int rows = std::min(F::kRows, p.few_rows_most);
+  return (int64_t)p.seqs * p.kv_heads * kSumWarps <= ctas
+             ? launch_pdl(k_kv_sum<HD, NT, kSumWarps>, dim3(ctas - 1, rows), dim3(kSumWarps * 32), 0, st, p)
+             : launch_pdl(k_kv_sum<HD, NT, 1>, dim3(ctas - 1, (rows + kSumWarps - 1) / kSumWarps),
+                          dim3(kSumWarps * 32), 0, st, p);
 }
 
 }  // namespace
