@@ -1901,7 +1901,7 @@ struct KvAttnPlan {
 void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
   const int64_t group = a->num_heads / a->cache.num_kv_heads, hd = a->cache.head_dim;
   // Up to 24 rows the kernel for few takes a sequence (16 sequences of 5 tokens x 4
-  // heads over 16384 keys: 46 us, on the 256-row tiles 74 to 93), beyond the other.
+  // heads over 16384 keys: 44 us, on the 256-row tiles 74 to 93), beyond the other.
   const int64_t rows = group * (a->q_offsets ? std::min(a->max_q_len, a->total_q) : 1);
   const int64_t few = rows <= 24 ? rows : group;      // beyond: single tokens' rows
   pl->nt = few <= 24 ? (int)ceil_div(few, 8) : 0;

@@ -33,8 +33,8 @@
 // items' borders.
 //
 // Measured (calls, cold L2): 4 x 131072 keys of 8 heads 123 us, 4.9 TB/s (6 in its
-// steady state, 7 us of start); 32 ragged contexts up to 8192 35 us; 256 up to
-// 1024 of 16 heads of 64 58 us.  26 instructions per key and head at head_dim 128
+// steady state, 7 us of start); 32 ragged contexts up to 8192 36 us; 256 up to
+// 1024 of 16 heads of 64 54 us.  26 instructions per key and head at head_dim 128
 // with 8 rows, half of the issue slots: between HBM and the cores, where contexts
 // are short the start's latency.
 #include <math_constants.h>
@@ -57,8 +57,8 @@ constexpr int kKeys = 32;           // of a unit: two 16-key tiles of the MMA, e
 constexpr int kOver = 8;
 // Units of a sequence whose heads may go to one warp each.  Beyond, and where four
 // heads are more than a span, the warps share a head: 256 sequences up to 1024 keys
-// take 57 us with the rule and 64 to 72 with the bound at a half or a quarter of a
-// span, 256 of 16 keys 19 us and 41 with shared heads.
+// took 57 us with the rule (54 since) and 64 to 72 with the bound at a half or a
+// quarter of a span, 256 of 16 keys 19 us and 41 with shared heads.
 constexpr int kSoloMost = 32;
 constexpr int kSumWarps = 8;        // of a block that adds up partial results
 constexpr float kLift = 7.0f;       // log2 of the numerator at the maximum

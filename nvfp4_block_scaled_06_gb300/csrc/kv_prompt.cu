@@ -25,8 +25,8 @@
 // fill the GPU; segments in several spans leave partial (o, m, l), joined in
 // order by a second kernel.  A first kernel lists the row tiles.
 //
-// Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 794 us = 1.36 PFLOP/s
-// (71% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 266 us = 1.0.  A
+// Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 796 us = 1.36 PFLOP/s
+// (71% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 267 us = 1.0.  A
 // key tile takes 3470 cycles: a half's softmax about 1950 and its MMAs' wait and
 // issue 1430 in turn, the other half beside it; the tensor pipe is busy 53%.
 #include <float.h>
