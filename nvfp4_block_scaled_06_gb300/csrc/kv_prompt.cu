@@ -45,7 +45,12 @@ namespace {
 constexpr int kRowsTile = 256;
 constexpr int kThreads = 13 * 32;
 constexpr int kLift = 4;              // log2 of the numerator at the maximum of a row's first keys
+constexpr float kMostF16 = 65504.0f;  // a sum of numerators up to it leaves them all in f16
 constexpr float kRaiseSum = 4096.0f;  // of a tile's numerators, beyond which the next raises the reference
+// References from here on are compared with products that were rounded like them (half a step of fp32 is 2^-2
+// here): an unrounded product and a reference made of the rounded one differ by 2^4 and more from 2^28 on, and the
+// row's largest numerator with them.
+constexpr float kLarge = 4194304.0f;
 constexpr int kTwo = 1 << 30;       // in an item's key tiles: it has rows in both halves
 // What a segment costs beside its key tiles, in key tiles: 1, 2, 3, 4, 6 give 424,
 // 326, 272, 270, 278 us for the 4096 prompt.
@@ -85,6 +90,11 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -135,6 +145,89 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+// 2^-e of a whole number e >= 0, 0 beyond fp32's normal range.
+__device__ __forceinline__ float down(float e) {
+  return e < 127.0f ? __uint_as_float((uint32_t)(127 - (int)e) << 23) : 0.0f;
+}
+// The O of these lanes' rows times f.
+template <int HD>
+__device__ __forceinline__ void scale_o(uint32_t o_col, float f) {
+#pragma unroll 1
+  for (int c = 0; c < HD / 32; ++c) {
+    uint32_t x[32];
+    tmem_ld_32x32b_x32(o_col + c * 32, x);
+    tmem_ld_wait_for(x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+    tmem_st_x32(o_col + c * 32, x);
+  }
+  tmem_st_wait();
+}
+
+// The numerators of a tile's chunks (32 keys) from c on, where a reference is large or a numerator may be beyond f16
+// (2^16 times the reference's): such a row is raised to its chunk's largest score, and O (unless it starts with this
+// tile), l and the numerators written before follow.  The chunks' scores are all still there: numerators take half
+// their columns, from the front.  Returns (m, l, sum of the tile's numerators).  All lanes of a warp; a row's own
+// chunks decide what happens to it and sums go in the loop's order, so that the rows around it change nothing.  16
+// columns at a time, since the registers are the loop's around (32 spilled there: 4096 prompt 266 -> 275 us).
+template <int HD>
+__device__ __forceinline__ float4 finish_tile(uint32_t s_col, uint32_t o_col, int c, bool starts, float sc, float m,
+                                              float l, float sum) {
+#pragma unroll 1
+  for (; c < 4; ++c) {
+    float mx = -CUDART_INF_F, part = 0.0f;
+    // first without storing, for the sum; then with the reference that it calls for
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      uint32_t x[16];
+      const float ref = m == -CUDART_INF_F ? 0.0f : m;
+      const bool large = fabsf(ref) >= kLarge;
+      float acc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[8];
+        tmem_ld_32x32b_x16(s_col + c * 32 + h * 16, x);
+        tmem_ld_wait_for(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float e[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float v = __uint_as_float(x[2 * i + k]);
+            mx = fmaxf(mx, v);
+            e[k] = ex2(large ? __fmul_rn(v, sc) - ref : __fmaf_rn(v, sc, -ref));
+            acc[2 * (i & 3) + k] += e[k];
+          }
+          pk[i] = pack_h2(e[0], e[1]);
+        }
+        if (pass == 1) tmem_st_x8(s_col + c * 16 + h * 8, pk);
+      }
+      part = ((acc[0] + acc[2]) + (acc[4] + acc[6])) + ((acc[1] + acc[3]) + (acc[5] + acc[7]));
+      if (pass == 1 || !__any_sync(0xffffffffu, part > kMostF16)) continue;
+      const float to = part > kMostF16 ? fmaxf(ceilf(__fmul_rn(mx, sc)) - kLift, m) : m;
+      const float f = to > m ? down(to - m) : 1.0f;
+      m = to;
+      l *= f;
+      sum *= f;
+      if (!starts) scale_o<HD>(o_col, f);
+      tmem_st_wait();                                // (the numerators' stores)
+      const uint32_t f2 = pack_h2(f, f);
+#pragma unroll 1
+      for (int d = 0; d < c; ++d) {
+        tmem_ld_32x32b_x16(s_col + d * 16, x);
+        tmem_ld_wait_for(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = hmul2(x[i], f2);
+        tmem_st_32x32b_x16(s_col + d * 16, x);
+      }
+    }
+    sum += part;
+  }
+  return make_float4(m, l, sum, 0.0f);
+}
+
 // ------------------------------------------------------------------- listing --
 // Row tiles of the sequences with more than few_rows rows, in order: {sequence,
 // tile, first key tile, key tiles}, and the key tiles before each.  One block.
@@ -446,17 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           // O and l follow a raised reference: times f, a power of two (or 0 for a first maximum)
           auto rescale = [&](float f) {
             l *= f;
-            if (j == w.j0) return;                   // O starts with this tile
-#pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-              uint32_t x[32];
-              tmem_ld_32x32b_x32(o_col + c * 32, x);
-              tmem_ld_wait_for(x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-              tmem_st_x32(o_col + c * 32, x);
-            }
-            tmem_st_wait();
+            if (j > w.j0) scale_o<HD>(o_col, f);     // (O starts with the first tile)
           };
           // numerators are not negative, so a tile's sum bounds them
           const bool fresh = m == -CUDART_INF_F, over = last > kRaiseSum;
@@ -473,18 +556,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
                 for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
               }
               if (fresh && mx > -CUDART_INF_F) {
-                m = ceilf(mx * sc) - kLift;
+                m = ceilf(__fmul_rn(mx, sc)) - kLift;
                 f = 0.0f;
               }
             }
             if (!fresh && over) {                    // by the last tile's sum, to a power of two
               const int e = (int)(__float_as_uint(last) >> 23) - 126 - kLift;   // (at most 2^18 a tile: below 16)
+              const float was = m;
               m += (float)e;
-              f = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+              f = down(m - was);                     // (by what fp32 raised it)
             }
             rescale(f);
           }
-          float ref = m == -CUDART_INF_F ? 0.0f : m;
+          const float ref = m == -CUDART_INF_F ? 0.0f : m;
           const uint64_t sc2 = pack2(sc, sc);
           float sum = 0.0f;
           uint32_t x[32], pk[16];
@@ -502,37 +586,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
             acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
             return lo2(acc[0]) + hi2(acc[0]);
           };
+          // (one copy of the loop: a large reference leaves it before the first chunk)
+          int c = __any_sync(0xffffffffu, fabsf(ref) >= kLarge) ? 4 : 0;
+          bool rest = c != 0;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (; c < 4; ++c) {
             tmem_ld_32x32b_x32(s_col + c * 32, x);
             tmem_ld_wait_for(x);
-            float part = numerators();
-            if (__any_sync(0xffffffffu, part > 65504.0f)) {
-              // A numerator may be beyond f16 (2^16 times the reference's): the row's reference is raised to this
-              // chunk's largest score, O, l and the numerators written before follow, and the chunk is done again.
-              float mx = -CUDART_INF_F;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
-              const float e = part > 65504.0f ? fmaxf(ceilf(mx * sc - m) - kLift, 0.0f) : 0.0f;
-              const float f = e < 127.0f ? __uint_as_float((uint32_t)(127 - (int)e) << 23) : 0.0f;
-              m += e;
-              ref = m == -CUDART_INF_F ? 0.0f : m;
-              rescale(f);
-              sum *= f;
-              const uint32_t f2 = pack_h2(f, f);
-#pragma unroll 1
-              for (int d = 0; d < c; ++d) {
-                uint32_t y[16];
-                tmem_ld_32x32b_x16(s_col + d * 16, y);
-                tmem_ld_wait_for(y);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = hmul2(y[i], f2);
-                tmem_st_32x32b_x16(s_col + d * 16, y);
-              }
-              part = numerators();
-            }
+            const float part = numerators();
+            if ((rest = __any_sync(0xffffffffu, part > kMostF16))) break;
             sum += part;
             tmem_st_32x32b_x16(s_col + c * 16, pk);
+          }
+          if (rest) {
+            const float4 y = finish_tile<HD>(s_col, o_col, c & 3, j == w.j0, sc, m, l, sum);
+            m = y.x;
+            l = y.y;
+            sum = y.z;
           }
           l += sum;
           last = sum;

@@ -1,0 +1,142 @@
+"""Attention over the key-value cache where a block works through many key tiles:
+many sequences over the same pages, scores that climb, fall and jump between
+tiles and within one, very large scores, NaN values.
+
+Reference in 64 bits by torch on the GPU, from the packed bytes; the tolerances
+are those that test_kv_gpu.py derives."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_06_gb300 as nv
+from oracle import kv_oracle as ko
+from test_kv_gpu import normal, scales
+
+pytestmark = pytest.mark.gpu
+
+LN2 = float(np.log(2.0))
+
+
+class Shared:
+    """`lens` sequences of qn new tokens each (qn: a number or one per sequence), all on the same pages, which hold
+    the keys k and values v, bf16 [n, kv heads, head_dim]."""
+
+    def __init__(self, k, v, lens, qn, G, page=64, seed=0, g=None, q=None):
+        n, H, hd = k.shape
+        self.lens, self.H, self.G, self.hd, self.page = list(lens), H, G, hd, page
+        self.qlens = [qn] * len(lens) if isinstance(qn, int) else list(qn)
+        pages = (n + page - 1) // page
+        order = np.random.default_rng(seed).permutation(pages + 1)[:pages]
+        self.row = order.astype(np.int32)
+        self.gk, self.gv = (scales(H, seed + 1), scales(H, seed + 2)) if g is None else (np.full(H, g, np.float32),) * 2
+        self.dgk, self.dgv = torch.from_numpy(self.gk).cuda(), torch.from_numpy(self.gv).cuda()
+        self.cache = nv.nvfp4_kv_cache(pages + 1, H, page, hd)
+        j = np.arange(n)
+        self.slots = torch.from_numpy(order[j // page].astype(np.int64) * page + j % page).cuda()
+        nv.nvfp4_kv_write(k, v, self.slots, self.cache, self.dgk, self.dgv)
+        self.offsets = np.concatenate([[0], np.cumsum(self.qlens)]).astype(np.int32)
+        self.q = normal((int(self.offsets[-1]), H * G, hd), seed + 5) if q is None else q
+        self.values()
+
+    def values(self):
+        """What the packed rows stand for, in 64 bits, [n, heads, hd]."""
+        rows = self.slots.cpu().numpy()
+        at, off = rows // self.page, rows % self.page
+        c = {m: t.cpu().numpy() for m, t in self.cache.items()}
+        self.k, self.v = (torch.from_numpy(ko.values(c[m + "_codes"][at, :, off], c[m + "_sf"][at, :, off], g)).cuda()
+                          for m, g in (("k", self.gk), ("v", self.gv)))
+
+    def prepare(self, **form):
+        B = len(self.lens)
+        table = torch.from_numpy(self.row)[None].expand(B, -1).contiguous().cuda()
+        return nv.prepare_kv_attention(
+            self.q, self.cache, self.dgk, self.dgv, table, torch.tensor(self.lens, dtype=torch.int32, device="cuda"),
+            q_offsets=torch.from_numpy(self.offsets).cuda(), max_q_len=max(self.qlens), want_lse=True, **form)
+
+    def run(self, **form):
+        call, got = self.prepare(**form)
+        call()
+        assert nv.read_device_status(call.workspace) == 0
+        return got
+
+    def scores(self, b, scale, causal, window):
+        """[tokens, kv heads, group, keys] in 64 bits, -inf where a row does not see a key."""
+        n, nq = self.lens[b], self.qlens[b]
+        q = self.q[self.offsets[b]:self.offsets[b + 1]].double().reshape(nq, self.H, self.G, self.hd)
+        s = torch.einsum("tkgd,nkd->tkgn", q, self.k[:n]) * scale
+        j, pos = torch.arange(n, device="cuda"), (n - nq + torch.arange(nq, device="cuda"))[:, None]
+        see = j <= pos if causal else torch.ones(nq, n, dtype=torch.bool, device="cuda")
+        if window:
+            see = see & (j > pos - window)
+        return s.masked_fill(~see[:, None, None], -float("inf")), see, q
+
+    def check(self, got, causal=True, window=0, scale=None, seqs=None):
+        scale = self.hd ** -0.5 if scale is None else scale
+        for b in (range(len(self.lens)) if seqs is None else seqs):
+            rows = slice(int(self.offsets[b]), int(self.offsets[b + 1]))
+            s, see, q = self.scores(b, scale, causal, window)
+            k, v = self.k[:self.lens[b]], self.v[:self.lens[b]]
+            top = s.amax(-1, keepdim=True)
+            e = torch.exp(s - top)
+            total = e.sum(-1, keepdim=True)
+            w = e / total
+            want = torch.einsum("tkgn,nkd->tkgd", w, v)
+            lse = (top + torch.log(total)).squeeze(-1)
+            S = torch.einsum("tkgn,nkd->tkgd", w, v.abs())
+            V = torch.einsum("tn,nkd->tkd", see.double(), v.abs())[:, :, None] / total
+            qk = torch.einsum("tkgd,nkd->tkgn", q.abs(), k.abs()).masked_fill(~see[:, None, None], 0).amax(-1)
+            n = self.lens[b]
+            d = (self.hd / 16 + 2) * 2.0 ** -22 * scale * qk + 2.0 ** -22 * (lse.abs() + np.log(max(n, 2)) + 2)
+            tol = ((2.0 ** -11 + 2 * d[..., None] + (n / 16 + 2) * 2.0 ** -22) * S + 2.0 ** -25 * V
+                   + 2.0 ** -8 * want.abs())
+            y, z = got[0][rows].double().reshape(want.shape), got[1][rows].double().reshape(lse.shape)
+            bad = ~((y - want).abs() <= tol * 1.0001)
+            assert not bool(bad.any()), (b, int(bad.sum()), bad.nonzero()[:3], y[bad][:4], want[bad][:4], tol[bad][:4])
+            far = ~((z - lse).abs() <= d + 2.0 ** -21 * (lse.abs() + 2))
+            assert not bool(far.any()), (b, z[far][:4], lse[far][:4])
+
+
+def along(height, H, hd):
+    """Keys whose first channel is `height` [n], bf16: with a query of ones there, their scores."""
+    k = torch.zeros(len(height), H, hd)
+    k[:, :, 0] = height[:, None]
+    return k.to(torch.bfloat16).cuda()
+
+
+def first_channel(rows, heads, hd, value=1.0):
+    q = torch.zeros(rows, heads, hd, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = value
+    return q
+
+
+# ------------------------------------------------------------- large scores --
+
+@pytest.mark.parametrize("power", [20, 24, 27, 28, 29, 31, 34, 40, 60, 90])
+@pytest.mark.parametrize("qn,G,hd", [(1, 4, 128), (3, 8, 64), (8, 8, 128), (32, 8, 64), (5, 64, 128)])
+def test_large_scores(qn, G, hd, power):
+    """Scores about 2^power: the softmax is 1 at the largest, 0 elsewhere, where the largest leads by more than what
+    fp32 sums of such products can be off by (d, twice) and 40.  The result is that key's value: the numerator's
+    rounding to f16 (2^-11) and the result's to bf16 (2^-8), 1000 others times e^-40 times less than 2^8; the
+    logarithm is its score, to d and three roundings."""
+    n, H, B = 1000, 2, 6
+    k, v = normal((n, H, hd), power), normal((n, H, hd), power + 1)
+    c = Shared(k, v, [n, n, 700, 513, 129, 64], qn, G, seed=power)
+    size = c.q.float() * 2.0 ** (power - 4 + 4 * torch.rand(c.q.shape[:2], device="cuda"))[..., None]
+    c.q = size.to(torch.bfloat16)
+    scale = hd ** -0.5
+    out, lse = c.run(scale=scale, causal=False)
+    checked = 0
+    for b in range(B):
+        rows = slice(int(c.offsets[b]), int(c.offsets[b + 1]))
+        s, _, q = c.scores(b, scale, False, 0)
+        qk = scale * torch.einsum("tkgd,nkd->tkgn", q.abs(), c.k[:c.lens[b]].abs()).amax(-1)
+        two, at = s.topk(2, -1)
+        d = (hd / 16 + 4) * 2.0 ** -22 * qk
+        sure = two[..., 0] - two[..., 1] > 2 * d + 40
+        checked += int(sure.sum())
+        want = c.v[:c.lens[b]].permute(1, 0, 2)[torch.arange(H, device="cuda")[None, :, None], at[..., 0]]
+        y, z = out[rows].double().reshape(want.shape), lse[rows].double().reshape(sure.shape)
+        ok = ((y - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * 1.001 * want.abs() + 2.0 ** -39).all(-1)
+        assert bool(ok[sure].all()), (b, int((~ok & sure).sum()), int(sure.sum()))
+        assert bool(((z - two[..., 0]).abs() <= d + 2.0 ** -22 * two[..., 0].abs())[sure].all())
+    assert checked > 0.9 * c.q.shape[0] * H * G
