@@ -62,7 +62,7 @@ constexpr int kOver = 8;
 constexpr int kSoloMost = 32;
 constexpr int kSumWarps = 8;        // of a block that adds up partial results
 constexpr float kLift = 7.0f;       // log2 of the numerator at the maximum
-constexpr float kRaise = kLift + 8.0f;
+constexpr float kRaise = kLift + 8.0f;   // a score further above the reference raises it
 
 template <int HD, int NT>
 struct Few {
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           top[nt][k] = fmaxf(fmaxf(s[0][nt][k], s[0][nt][k + 2]), fmaxf(s[1][nt][k], s[1][nt][k + 2]));
-          raise |= top[nt][k] > m[nt][k] + kRaise;
+          raise |= top[nt][k] - m[nt][k] > kRaise;     // (near m exact, as m + kRaise is not from 2^24 on)
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll

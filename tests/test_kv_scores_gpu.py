@@ -140,3 +140,31 @@ def test_large_scores(qn, G, hd, power):
         assert bool(ok[sure].all()), (b, int((~ok & sure).sum()), int(sure.sum()))
         assert bool(((z - two[..., 0]).abs() <= d + 2.0 ** -22 * two[..., 0].abs())[sure].all())
     assert checked > 0.9 * c.q.shape[0] * H * G
+
+
+@pytest.mark.parametrize("qn,G", [(1, 8), (5, 4)])
+@pytest.mark.parametrize("low,step", [(14, 8), (18, 8), (18, 10), (19, 8), (20, 8), (21, 16), (23, 64)])
+@pytest.mark.parametrize("H,n,B", [(4, 1024, 120), (2, 4096, 130)])
+def test_exact_steps_between_large_scores(H, n, B, low, step, qn, G):
+    """Scores 96 * 2^low, and `step` more from some key on, which fp32 holds exactly (its spacing there is
+    2^(low - 17)), but not sums of a score and 7 or 15.  In powers of two (scale ln 2, all factors exact)."""
+    k = torch.zeros(n, H, 64)
+    k[:, :, 0], k[:, :, 16] = 96.0, 6.0           # blocks' scale bytes 16 and 1
+    late = torch.arange(n) % 512 >= 300
+    k[late, :, 17] = 4.0
+    q = first_channel(B * qn, H * G, 64, 2.0 ** low)
+    q[:, :, 17] = step / 4
+    c = Shared(k.to(torch.bfloat16).cuda(), normal((n, H, 64), 1), [n - 7 * (i % 5) for i in range(B)], qn, G, g=1.0, q=q)
+    assert torch.equal(c.k.float().cpu(), k)
+    out, lse = c.run(scale=LN2, causal=False)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    for b in (0, 1, B // 2, B - 2, B - 1):
+        rows = slice(int(c.offsets[b]), int(c.offsets[b + 1]))
+        e = torch.exp2(step * late[:c.lens[b]].double() - step).cuda()
+        v = c.v[:c.lens[b]]
+        want = torch.einsum("n,nkd->kd", e, v) / e.sum()
+        bound = torch.einsum("n,nkd->kd", e, v.abs()) / e.sum()
+        y = out[rows].double().reshape(-1, H, G, 64)
+        # every difference of scores is exact: the numerators' rounding, the sums', the result's
+        tol = (2.0 ** -11 + (n / 16 + 4) * 2.0 ** -22) * bound + 2.0 ** -25 * v.abs().sum(0) / e.sum() + 2.0 ** -8 * want.abs()
+        assert bool(((y - want[None, :, None]).abs() <= tol[None, :, None] * 1.0001).all())
