@@ -735,9 +735,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
  *   out = sum_j softmax_j(s) V_j,  lse = ln sum_j exp(s_j)
  * A query that sees no key gets zeros and lse = -inf.  Scores and sums are
  * fp32; K and V enter the products exactly, q too (to 2^-28 of its row's
- * largest magnitude), the softmax's numerators rounded to f16 (zero below 2^-29
- * of the largest among the row's first keys); out is rounded
- * to bf16 once.  What a query does not see does not reach it, NaN neither;
+ * largest magnitude), the softmax's numerators rounded to f16 (with many rows zero
+ * below 2^-28 of the row's largest, with few below 2^-32); out is rounded to bf16
+ * once.  What a query does not see does not reach it, NaN neither;
  * scores are finite for finite inputs below 2^100.
  *   Device data are clamped, not checked: offsets to [0, total_q] and ascending
  *   order, lengths to [0, max_pages * page_size]; keys of a page outside

@@ -5,9 +5,10 @@
 // and key-value head, 256 to a tile (two M = 128 halves), its keys come 128 at a
 // time:  S = Q K^T (f16 operands, exact K, q scaled by a power of two per row),
 // P = exp2(S - m), O += P V, m a running reference of the row: 4 below its first
-// keys' maximum (so that keys count down to 2^-29 of it; f16 ends at 2^-25),
-// raised, with O and l rescaled, when a step's numerators sum to more than 2^12,
-// and within a step before one would leave f16.
+// keys' maximum, to a whole number, raised, with O and l rescaled, when a step's
+// numerators sum to more than 2^12, and within a step before one would leave f16,
+// so that the row's largest stays 2^3 or more: keys count down to 2^-28 of it
+// (f16 ends at 2^-25).
 //
 // Bound: the tensor cores, 4 x 128 x 256 x head_dim operations per step and 4096
 // multiply-adds a cycle; next to them 32768 exponentials (32 a cycle) and the
@@ -560,8 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
                 f = 0.0f;
               }
             }
-            if (!fresh && over) {                    // by the last tile's sum, to a power of two
-              const int e = (int)(__float_as_uint(last) >> 23) - 126 - kLift;   // (at most 2^18 a tile: below 16)
+            if (!fresh && over) {
+              // By the last tile's sum, to a power of two: the largest of its 128 numerators, 2^-7 of the sum or
+              // more, stays 2^(kLift - 1) or more, where a row's first largest may lie too.  (The sum is at most 2^18.)
+              const int e = (int)(__float_as_uint(last) >> 23) - 127 - 7 - (kLift - 1);
               const float was = m;
               m += (float)e;
               f = down(m - was);                     // (by what fp32 raised it)

@@ -168,3 +168,19 @@ def test_exact_steps_between_large_scores(H, n, B, low, step, qn, G):
         # every difference of scores is exact: the numerators' rounding, the sums', the result's
         tol = (2.0 ** -11 + (n / 16 + 4) * 2.0 ** -22) * bound + 2.0 ** -25 * v.abs().sum(0) / e.sum() + 2.0 ** -8 * want.abs()
         assert bool(((y - want[None, :, None]).abs() <= tol[None, :, None] * 1.0001).all())
+
+
+# --------------------------------------------- references that have to follow --
+
+@pytest.mark.parametrize("low", [20.25, 21.0])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_many_keys_below_many_of_the_largest(hd, low):
+    """A tile whose 128 keys are all the row's largest, after a tile slightly below, both without a value, and
+    thousands of keys 2^-low of them: the whole result is theirs."""
+    n = 8192
+    height = torch.full((n,), -low)
+    height[:128], height[128:256] = -2.0, 0.0
+    v = torch.zeros(n, 1, hd, dtype=torch.bfloat16, device="cuda")
+    v[256:] = 6.0
+    c = Shared(along(height, 1, hd), v, [n] * 170, 32, 8, g=1.0, q=first_channel(170 * 32, 8, hd))
+    c.check(c.run(scale=LN2, causal=False), causal=False, scale=LN2, seqs=range(0, 170, 13))
