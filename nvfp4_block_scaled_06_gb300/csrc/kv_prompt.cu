@@ -214,13 +214,16 @@ __device__ __forceinline__ float4 finish_tile(uint32_t s_col, uint32_t o_col, in
       sum *= f;
       if (!starts) scale_o<HD>(o_col, f);
       tmem_st_wait();                                // (the numerators' stores)
-      const uint32_t f2 = pack_h2(f, f);
+      // (in fp32: f itself may be below f16's range, where 96 numerators of up to 2^11 times f still count)
 #pragma unroll 1
       for (int d = 0; d < c; ++d) {
         tmem_ld_32x32b_x16(s_col + d * 16, x);
         tmem_ld_wait_for(x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = hmul2(x[i], f2);
+        for (int i = 0; i < 16; ++i) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
+          x[i] = pack_h2(v.x * f, v.y * f);
+        }
         tmem_st_32x32b_x16(s_col + d * 16, x);
       }
     }

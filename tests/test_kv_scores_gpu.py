@@ -184,3 +184,17 @@ def test_many_keys_below_many_of_the_largest(hd, low):
     v[256:] = 6.0
     c = Shared(along(height, 1, hd), v, [n] * 170, 32, 8, g=1.0, q=first_channel(170 * 32, 8, hd))
     c.check(c.run(scale=LN2, causal=False), causal=False, scale=LN2, seqs=range(0, 170, 13))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("top", [13.5, 20.0, 27.0, 39.0])
+def test_a_jump_behind_others_in_a_tile(hd, top):
+    """Within one tile 96 keys of 2^6.75 and then one of 2^top: the first ones' numerators, written already, follow
+    the reference, and the result is theirs (the top key has no value)."""
+    n = 256
+    height = torch.zeros(n)
+    height[128:224], height[240] = 6.75, top
+    v = torch.zeros(n, 2, hd, dtype=torch.bfloat16, device="cuda")
+    v[128:224] = 6.0
+    c = Shared(along(height, 2, hd), v, [n] * 300, 32, 8, g=1.0, q=first_channel(300 * 32, 16, hd))
+    c.check(c.run(scale=LN2, causal=False), causal=False, scale=LN2, seqs=range(0, 300, 17))
