@@ -378,8 +378,9 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
         m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
         m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
         const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7);
-        // a power of two that brings the row's maximum to [2^13, 2^14); 1 for rows with an infinity or a NaN
-        const int up = e == 255 ? 127 : min(267 - e, 190);
+        // a power of two that brings the row's maximum to [2^13, 2^14); 1 for rows with an infinity or a NaN; at most
+        // 2^126, which makes f16 numbers of all that bf16 holds below 2^-113
+        const int up = e == 255 ? 127 : min(267 - e, 253);
         const float mul = __uint_as_float((uint32_t)up << 23);
         const float back = __uint_as_float((uint32_t)(254 - up) << 23) * gsc;
 #pragma unroll

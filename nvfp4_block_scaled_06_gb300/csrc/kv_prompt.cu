@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
         }
         const int all_lo = __reduce_max_sync(0xffffffffu, see_lo), all_hi = __reduce_min_sync(0xffffffffu, see_hi);
         // this thread's row to f16, times a power of two that brings its maximum to [2^13, 2^14) (1 for a row with
-        // an infinity or a NaN)
+        // an infinity or a NaN; at most 2^126, which makes f16 numbers of all that bf16 holds below 2^-113)
         cp_async_wait<0>();
         __syncwarp();
         const uint32_t mine = sq + lane * 128, xr = (lane & 7) << 4;
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnParams p)
           m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                      __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
         }
-        const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), up = e == 255 ? 127 : min(267 - e, 190);
+        const int e = (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), up = e == 255 ? 127 : min(267 - e, 253);
         const float mul = __uint_as_float((uint32_t)up << 23);
         const float sc = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * (p.scale_log2 * p.gk[w.h]), FLT_MIN);
 #pragma unroll 4

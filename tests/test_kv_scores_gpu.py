@@ -198,3 +198,16 @@ def test_a_jump_behind_others_in_a_tile(hd, top):
     v[128:224] = 6.0
     c = Shared(along(height, 2, hd), v, [n] * 300, 32, 8, g=1.0, q=first_channel(300 * 32, 16, hd))
     c.check(c.run(scale=LN2, causal=False), causal=False, scale=LN2, seqs=range(0, 300, 17))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("size", [-30, -70, -100, -120, -126])
+@pytest.mark.parametrize("qn,G", [(1, 8), (12, 8)])
+def test_small_queries_under_a_large_scale(qn, G, hd, size):
+    """Queries of 2^size under a scale of 2^-size: the products are ordinary.  (bf16 holds less than eight bits of
+    numbers below 2^-126: the reference takes what it holds.)"""
+    n = 300
+    c = Shared(normal((n, 2, hd), 1), normal((n, 2, hd), 2), [n, 100], qn, G, seed=3)
+    c.q = (c.q.double() * 2.0 ** size).to(torch.bfloat16)
+    scale = 2.0 ** -size * hd ** -0.5
+    c.check(c.run(scale=scale), scale=scale)
