@@ -211,3 +211,69 @@ def test_small_queries_under_a_large_scale(qn, G, hd, size):
     c.q = (c.q.double() * 2.0 ** size).to(torch.bfloat16)
     scale = 2.0 ** -size * hd ** -0.5
     c.check(c.run(scale=scale), scale=scale)
+
+
+# --------------------------------------------------------------- NaN values --
+
+def test_nan_of_one_sequence_does_not_hold_up_the_others():
+    """A value with a NaN scale in two long sequences among others: its channels of the rows that see it are NaN,
+    every other row has the same bits as without it, and no wait runs out that is far longer than the work."""
+    n, H, hd, qn = 32768, 2, 128, 32
+    lens = [n - 64 * (b % 12) for b in range(96)]
+    c = Shared(normal((n, H, hd), 1), normal((n, H, hd), 2), lens, qn, 8)
+    page = torch.arange(c.cache["k_codes"].shape[0], device="cuda")
+    spare = int(page[~torch.isin(page, torch.from_numpy(c.row).cuda())][0])
+    call, (out, lse) = c.prepare()
+    call()
+    assert nv.read_device_status(call.workspace) == 0
+    want = out.clone(), lse.clone()
+    # page 40 of the third sequence and of another becomes a copy whose key 7 has a NaN in head 1, channels 48 to 63
+    at = 40
+    for t in c.cache.values():
+        t[spare] = t[int(c.row[at])]
+    c.cache["v_sf"][spare, 1, 7, 3] = 0x7F
+    table = torch.from_numpy(c.row)[None].expand(len(lens), -1).contiguous().cuda()
+    table[[2, 60], at] = spare
+    call, (out, lse) = nv.prepare_kv_attention(
+        c.q, c.cache, c.dgk, c.dgv, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+        q_offsets=torch.from_numpy(c.offsets).cuda(), max_q_len=qn, want_lse=True)
+    old = nv.set_wait_timeout_ns(2_000_000)
+    try:
+        call()
+        assert nv.read_device_status(call.workspace) == 0
+    finally:
+        nv.set_wait_timeout_ns(old)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    for b in (2, 60):
+        hit[b * qn:(b + 1) * qn, 8:, 48:64] = True
+    assert bool(torch.isnan(out[hit]).all())
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 700), (False, 0)])
+@pytest.mark.parametrize("qn,G", [(1, 8), (3, 8), (40, 8)])
+def test_nan_values_in_long_sequences(qn, G, causal, window, hd):
+    """NaN scales at tiles' borders, in the first key and the last: NaN for the rows that see them, in their
+    16 channels, and the other channels right."""
+    n, H = 1500, 2
+    c = Shared(normal((n, H, hd), 1), normal((n, H, hd), 2), [n, 1400, 513, 300] * 12, qn, G, seed=hd)
+    spots = [(0, 0, 0), (127, 1, 1), (128, 0, hd // 16 - 1), (777, 1, 2), (1399, 0, 1), (1485, 0, 0), (1499, 1, 3)]
+    for j, h, block in spots:
+        slot = int(c.slots[j])
+        c.cache["v_sf"][slot // c.page, h, slot % c.page, block] = 0x7F
+    out, lse = c.run(causal=causal, window=window)
+    for b in range(len(c.lens)):
+        rows, m = slice(int(c.offsets[b]), int(c.offsets[b + 1])), c.lens[b]
+        s, see, _ = c.scores(b, hd ** -0.5, causal, window)
+        y = out[rows].double().reshape(qn, H, G, hd)
+        nan = torch.zeros(qn, H, G, hd, dtype=torch.bool, device="cuda")
+        for j, h, block in spots:
+            if j < m:
+                nan[:, h, :, 16 * block:16 * block + 16] |= see[:, j, None, None]
+        assert torch.equal(torch.isnan(y), nan)
+        w = torch.softmax(s, -1)
+        want = torch.einsum("tkgn,nkd->tkgd", w, c.v[:m])
+        # unit scores: f16 numerators, bf16 results, the sums of some thousand fp32 terms (2^-12 in all)
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12) * torch.einsum("tkgn,nkd->tkgd", w, c.v[:m].abs())
+        assert bool(((y - want).abs() <= tol)[~nan].all())
