@@ -737,8 +737,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
  * fp32; K and V enter the products exactly, q too (to 2^-28 of its row's
  * largest magnitude), the softmax's numerators rounded to f16 (with many rows zero
  * below 2^-28 of the row's largest, with few below 2^-32); out is rounded to bf16
- * once.  What a query does not see does not reach it, NaN neither;
- * scores are finite for finite inputs below 2^100.
+ * once.  What a query does not see does not reach it, NaN neither.  Scores
+ * are finite, and off by fp32 roundings only, where scale * g lies in
+ * [2^-100, 2^108] and scale * g * |q| stays below 2^108.
  *   Device data are clamped, not checked: offsets to [0, total_q] and ascending
  *   order, lengths to [0, max_pages * page_size]; keys of a page outside
  *   [0, num_pages) are left out; of a sequence with more than max_q_len queries
@@ -752,7 +753,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
  * Requirements: those of the cache; num_heads a multiple of num_kv_heads, at
  *   most 1024 times of it; total_q, num_seqs < 2^31; q and out 16-byte
  *   aligned, strides % 8 == 0; page_table, kv_lens, q_offsets, lse 4-byte
- *   aligned.
+ *   aligned; scale > 0 with scale * log2(e) finite; window >= 0, 0 where not
+ *   causal.
  * Workspace: nvfp4_kv_attention_workspace_size(&args); it does not depend on
  *   the device data.
  * ------------------------------------------------------------------------ */

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
@@ -1888,6 +1889,8 @@ KvPages kv_pages(const nvfp4_kv_pages &c) {
   return q;
 }
 
+constexpr float kLog2E = 1.4426950408889634f;   // the kernels' exponentials are of base 2
+
 struct KvAttnPlan {
   size_t ws = 0;
   int nt = 0;                          // rows of the kernel for few rows / 8; 0: not run
@@ -1940,7 +1943,7 @@ nvfp4_status validate_kv_attention(const nvfp4_kv_attention_args *a) {
   if (!kv_rows_ok(a->num_heads, a->cache.head_dim, a->q_ld, a->q_head_ld) ||
       !kv_rows_ok(a->num_heads, a->cache.head_dim, a->out_ld, a->out_head_ld) || a->table_ld < a->max_pages ||
       (!a->q_offsets && a->total_q != a->num_seqs) || a->window < 0 || (a->window > 0 && !a->causal) ||
-      !(a->scale > 0.0f) || a->scale > 3.0e38f)
+      !(a->scale > 0.0f) || !std::isfinite(a->scale * kLog2E))
     return NVFP4_ERR_INVALID_ARG;
   if (a->num_heads % a->cache.num_kv_heads != 0 || a->num_heads / a->cache.num_kv_heads > 1024 ||
       a->total_q > 0x7FFFFFFFll || a->num_seqs > 0x7FFFFFFFll || a->max_pages > 0x7FFFFFFFll)
@@ -1976,7 +1979,7 @@ nvfp4_status run_kv_attention(const nvfp4_kv_attention_args *a, const KvAttnPlan
   p.table_ld = a->table_ld;
   p.max_pages = (int)a->max_pages;
   p.kv_lens = a->kv_lens;
-  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.scale_log2 = a->scale * kLog2E;
   p.causal = a->causal != 0;
   p.window = a->window;
   p.out = static_cast<__nv_bfloat16 *>(a->out);
