@@ -1981,7 +1981,7 @@ nvfp4_status run_kv_attention(const nvfp4_kv_attention_args *a, const KvAttnPlan
   p.kv_lens = a->kv_lens;
   p.scale_log2 = a->scale * kLog2E;
   p.causal = a->causal != 0;
-  p.window = a->window;
+  p.window = std::min<int64_t>(a->window, 1ll << 32);   // (wider than any sequence; position - window stays in range)
   p.out = static_cast<__nv_bfloat16 *>(a->out);
   p.out_ld = a->out_ld;
   p.out_head_ld = a->out_head_ld;

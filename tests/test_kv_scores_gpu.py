@@ -277,3 +277,15 @@ def test_nan_values_in_long_sequences(qn, G, causal, window, hd):
         # unit scores: f16 numerators, bf16 results, the sums of some thousand fp32 terms (2^-12 in all)
         tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12) * torch.einsum("tkgn,nkd->tkgd", w, c.v[:m].abs())
         assert bool(((y - want).abs() <= tol)[~nan].all())
+
+
+# ------------------------------------------------------------- wide windows --
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 40, 2 ** 63 - 1])
+@pytest.mark.parametrize("qn,G", [(1, 8), (5, 4), (400, 8)])
+def test_windows_wider_than_any_sequence(qn, G, window):
+    """They are no window, with more new tokens than keys too."""
+    n = 390
+    c = Shared(normal((n, 2, 64), 1), normal((n, 2, 64), 2), [n, 3, 200], qn, G)
+    want, got = c.run(), c.run(window=window)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
