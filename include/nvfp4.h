@@ -686,8 +686,9 @@ typedef struct {
  * nvfp4_kv_read  -- their rows back: E2M1 * (E4M3 * g), rounded to out_dtype.
  *
  *   k, v: [num_tokens][num_kv_heads][head_dim], rows k_ld / v_ld and heads
- *     k_head_ld / v_head_ld elements apart (parts of one fused projection
- *     will do); bf16 for the write, out_dtype for the read.
+ *     k_head_ld / v_head_ld elements apart, without overlap: a token's heads
+ *     within its row (parts of one fused projection will do) or a head's tokens
+ *     within its matrix; bf16 for the write, out_dtype for the read.
  *   slots: device int64[num_tokens], a token's slot.  Tokens whose slot is
  *     outside the cache (-1: padding) are left out; the read leaves their rows
  *     as they are.  The slots of one write are distinct: where two tokens share
@@ -746,7 +747,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
  *   the first max_q_len are computed.  Rows of q outside every sequence are
  *   left as they are in out and lse.
  *   q, out: bf16 [total_q][num_heads][head_dim], rows q_ld / out_ld and heads
- *     q_head_ld / out_head_ld elements apart; lse: float [total_q][num_heads]
+ *     q_head_ld / out_head_ld elements apart (as k and v above); lse: float [total_q][num_heads]
  *     or NULL; page_table: int32 [num_seqs][table_ld], the first max_pages
  *     columns used; max_q_len: the most queries of a sequence (a bound; it
  *     picks the kernels).

@@ -821,8 +821,8 @@ def _kv_rows(t, what: str, dtypes, heads: int, head_dim: int):
 
 def prepare_kv_write(k, v, slots, cache, k_global_scale, v_global_scale) -> tuple[Prepared, dict]:
     """Packs keys and values into the cache.  k, v bf16 [tokens, kv_heads,
-    head_dim] (rows and heads may be strided), slots int64 [tokens] = page *
-    page_size + offset (outside the cache, as -1: left out; otherwise distinct),
+    head_dim] (rows and heads may be strided, heads outermost too), slots int64
+    [tokens] = page * page_size + offset (outside the cache, as -1: left out; otherwise distinct),
     the scales fp32 [kv_heads], static.  Returns (Prepared call, cache)."""
     lib = load()
     c, keep = _kv_pages(cache, k_global_scale, v_global_scale)
@@ -885,7 +885,7 @@ def prepare_kv_attention(q, cache, k_global_scale, v_global_scale, page_table, k
                          max_q_len: int | None = None, scale: float | None = None, causal: bool = True,
                          window: int = 0, want_lse: bool = False, out=None) -> tuple[Prepared, tuple]:
     """Attention of new tokens over the cache.  q bf16 [rows, heads, head_dim]
-    (rows and heads may be strided); page_table int32 [seqs, pages], kv_lens
+    (strided as k and v above); page_table int32 [seqs, pages], kv_lens
     int32 [seqs]: a sequence's keys, the new tokens' among them; q_offsets int32
     [seqs+1]: the rows of each sequence's queries, the last positions of its keys
     (None: one query per sequence); max_q_len: the most queries of a sequence, if

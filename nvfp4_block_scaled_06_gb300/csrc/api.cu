@@ -1855,9 +1855,13 @@ int log2_of(int64_t v) {
   return s;
 }
 
-// Rows [tokens][heads][head_dim] with the given strides do not overlap.
-bool kv_rows_ok(int64_t heads, int64_t hd, int64_t ld, int64_t head_ld) {
-  return (heads == 1 || head_ld >= hd) && ld >= (heads - 1) * head_ld + hd;
+// Rows [tokens][heads][head_dim] with the given strides do not overlap: a token's heads lie within its row, or a
+// head's tokens within its matrix.
+bool kv_rows_ok(int64_t tokens, int64_t heads, int64_t hd, int64_t ld, int64_t head_ld) {
+  const auto holds = [hd](int64_t n, int64_t step, int64_t room) {   // n pieces of hd, `step` apart, in `room`
+    return n == 1 ? room >= hd : step >= hd && room >= hd && (room - hd) / step >= n - 1;
+  };
+  return holds(heads, head_ld, ld) || holds(tokens, ld, head_ld);
 }
 
 nvfp4_status validate_kv_copy(const nvfp4_kv_pages &c, const float *gk, const float *gv, int64_t tokens,
@@ -1865,7 +1869,8 @@ nvfp4_status validate_kv_copy(const nvfp4_kv_pages &c, const float *gk, const fl
                               int64_t v_ld, int64_t v_head_ld, int64_t item) {
   if (!gk || !gv || !slots || !k || !v || tokens < 1) return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = validate_kv_pages(c); s != NVFP4_OK) return s;
-  if (!kv_rows_ok(c.num_kv_heads, c.head_dim, k_ld, k_head_ld) || !kv_rows_ok(c.num_kv_heads, c.head_dim, v_ld, v_head_ld))
+  if (!kv_rows_ok(tokens, c.num_kv_heads, c.head_dim, k_ld, k_head_ld) ||
+      !kv_rows_ok(tokens, c.num_kv_heads, c.head_dim, v_ld, v_head_ld))
     return NVFP4_ERR_INVALID_ARG;
   if (tokens > 0x7FFFFFFFll) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(k, 16) || !aligned(v, 16) || (k_ld | k_head_ld | v_ld | v_head_ld) * item % 16 != 0 ||
@@ -1940,8 +1945,8 @@ nvfp4_status validate_kv_attention(const nvfp4_kv_attention_args *a) {
     return NVFP4_ERR_INVALID_ARG;
   if (any_empty({a->total_q, a->num_heads, a->num_seqs, a->max_pages, a->max_q_len})) return NVFP4_ERR_INVALID_ARG;
   if (nvfp4_status s = validate_kv_pages(a->cache); s != NVFP4_OK) return s;
-  if (!kv_rows_ok(a->num_heads, a->cache.head_dim, a->q_ld, a->q_head_ld) ||
-      !kv_rows_ok(a->num_heads, a->cache.head_dim, a->out_ld, a->out_head_ld) || a->table_ld < a->max_pages ||
+  if (!kv_rows_ok(a->total_q, a->num_heads, a->cache.head_dim, a->q_ld, a->q_head_ld) ||
+      !kv_rows_ok(a->total_q, a->num_heads, a->cache.head_dim, a->out_ld, a->out_head_ld) || a->table_ld < a->max_pages ||
       (!a->q_offsets && a->total_q != a->num_seqs) || a->window < 0 || (a->window > 0 && !a->causal) ||
       !(a->scale > 0.0f) || !std::isfinite(a->scale * kLog2E))
     return NVFP4_ERR_INVALID_ARG;

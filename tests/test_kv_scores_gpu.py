@@ -289,3 +289,32 @@ def test_windows_wider_than_any_sequence(qn, G, window):
     c = Shared(normal((n, 2, 64), 1), normal((n, 2, 64), 2), [n, 3, 200], qn, G)
     want, got = c.run(), c.run(window=window)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---------------------------------------------------------- heads outermost --
+
+@pytest.mark.parametrize("lens,qn,G", [([300, 40], 1, 4), ([300, 40], 5, 4), ([700, 128], 60, 8)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_rows_with_heads_outermost(lens, qn, G, hd):
+    """Queries, keys, values and results as transposes of [heads, tokens, head_dim] give the same bits."""
+    n, H = 700, 3
+    k, v = normal((n, H, hd), 1), normal((n, H, hd), 2)
+    c = Shared(k, v, lens, qn, G)
+    want, before = c.run(), {m: t.clone() for m, t in c.cache.items()}
+    turned = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (k, v, c.q)]
+    assert turned[0].stride(0) == hd
+    for t in c.cache.values():
+        t.zero_()
+    nv.nvfp4_kv_write(turned[0], turned[1], c.slots, c.cache, c.dgk, c.dgv)
+    assert all(torch.equal(c.cache[m][c.row], before[m][c.row]) for m in before)
+    c.q = turned[2]
+    out = torch.full((H * G, len(lens) * qn + 2, hd), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = c.run(out=out[:, 1:-1].transpose(0, 1))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((out[:, 0] == 7).all()) and bool((out[:, -1] == 7).all())
+    for dtype in (torch.bfloat16, torch.float32):
+        wide = torch.full((2, H, n + 2, hd), 7.0, dtype=dtype, device="cuda")
+        rows = nv.nvfp4_kv_read(c.slots, c.cache, c.dgk, c.dgv, out=tuple(t[:, 1:-1].transpose(0, 1) for t in wide))
+        plain = nv.nvfp4_kv_read(c.slots, c.cache, c.dgk, c.dgv, out_dtype=dtype)
+        assert all(torch.equal(a, b) for a, b in zip(rows, plain))
+        assert bool((wide[:, :, 0] == 7).all()) and bool((wide[:, :, -1] == 7).all())
