@@ -749,8 +749,10 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_read_args *args, nvfp4_stream stream);
  *   q, out: bf16 [total_q][num_heads][head_dim], rows q_ld / out_ld and heads
  *     q_head_ld / out_head_ld elements apart (as k and v above); lse: float [total_q][num_heads]
  *     or NULL; page_table: int32 [num_seqs][table_ld], the first max_pages
- *     columns used; max_q_len: the most queries of a sequence (a bound; it
- *     picks the kernels).
+ *     columns used; max_q_len: the most queries of a sequence, a bound.  It
+ *     picks the kernels: where max_q_len queries of a group are up to 24 rows the
+ *     one for few rows takes the batch, else sequences of about a single token's
+ *     rows only, so a bound far above the lengths costs time.
  * Requirements: those of the cache; num_heads a multiple of num_kv_heads, at
  *   most 1024 times of it; total_q, num_seqs < 2^31; q and out 16-byte
  *   aligned, strides % 8 == 0; page_table, kv_lens, q_offsets, lse 4-byte

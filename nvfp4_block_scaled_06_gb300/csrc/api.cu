@@ -1908,8 +1908,15 @@ struct KvAttnPlan {
 
 void plan_kv_attention(const nvfp4_kv_attention_args *a, KvAttnPlan *pl) {
   const int64_t group = a->num_heads / a->cache.num_kv_heads, hd = a->cache.head_dim;
-  // Up to 24 rows the kernel for few takes a sequence (16 sequences of 5 tokens x 4
-  // heads over 16384 keys: 44 us, on the 256-row tiles 74 to 93), beyond the other.
+  // Where the bound on a sequence's rows is up to 24, the kernel for few takes the
+  // batch.  Else it takes the sequences with no more rows than a single token's,
+  // rounded up to 8, if those are up to 24, and the other kernel the rest: drafted
+  // tokens beside a longer chunk, or under a bound far above them, go to the 256-row
+  // tiles too.  Both kernels, us with a warm L2, 8 heads of 128:
+  //   rows                            8       12      20      24      32, 40, 64, 128
+  //   16 sequences up to 16384 keys   31, 77  41, 83  41, 65  57, 85  91, 67, 106, 93 on the tiles
+  //   64 sequences up to 2048         29, 65  34, 64  52, 71  52, 67
+  //   one of 16384                    14, 22  16, 25  21, 27  20, 22
   const int64_t rows = group * (a->q_offsets ? std::min(a->max_q_len, a->total_q) : 1);
   const int64_t few = rows <= 24 ? rows : group;      // beyond: single tokens' rows
   pl->nt = few <= 24 ? (int)ceil_div(few, 8) : 0;

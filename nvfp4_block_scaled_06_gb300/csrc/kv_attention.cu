@@ -16,7 +16,7 @@
 // exact in f16; q is scaled by a power of two per row, which keeps bf16's 8 bits
 // down to 2^-28 of the row's maximum.  The scores' transpose S^T[keys][rows] is
 // in registers already; one 8x8 transpose per eight keys makes it P's operand.
-// P is rounded to f16 (2^-11 relative, half of what bf16 results keep), sums and
+// P is rounded to f16 (half a step is 2^-11, an eighth of a bf16 result's), sums and
 // accumulators are fp32.
 //
 // The reference m is 7 (in units of log2) below the row's maximum and is raised
@@ -34,7 +34,7 @@
 //
 // Measured (calls, cold L2): 4 x 131072 keys of 8 heads 123 us, 4.9 TB/s (6 in its
 // steady state, 7 us of start); 32 ragged contexts up to 8192 36 us; 256 up to
-// 1024 of 16 heads of 64 54 us.  26 instructions per key and head at head_dim 128
+// 1024 of 16 heads of 64 54 us; 16 x 5 drafted tokens over up to 16384 43 us.  26 instructions per key and head at head_dim 128
 // with 8 rows, half of the issue slots: between HBM and the cores, where contexts
 // are short the start's latency.
 #include <math_constants.h>
@@ -58,7 +58,10 @@ constexpr int kOver = 8;
 // Units of a sequence whose heads may go to one warp each.  Beyond, and where four
 // heads are more than a span, the warps share a head: 256 sequences up to 1024 keys
 // took 57 us with the rule (54 since) and 64 to 72 with the bound at a half or a
-// quarter of a span, 256 of 16 keys 19 us and 41 with shared heads.
+// quarter of a span, 256 of 16 keys 19 us and 41 with shared heads.  16, 32, 64 and 128 as
+// the most, us: 256 sequences of 2048 keys of 16 heads of 64 172, 172, 186, 186; 512 of them
+// 333, 333, 363, 366; 512 up to 4096 267, 271, 295, 311; 1024 up to 2048 270, 280, 266, 267;
+// of 8 heads of 128 1024 up to 1024 keys 167, 142, 144, 143, up to 2048 214, 264, 247, 245.
 constexpr int kSoloMost = 32;
 constexpr int kSumWarps = 8;        // of a block that adds up partial results
 constexpr float kLift = 7.0f;       // log2 of the numerator at the maximum
@@ -701,8 +704,8 @@ __global__ void __launch_bounds__(kWarps * 32, Few<HD, NT>::kCtas) k_kv_few(cons
 // Segments that lie in several spans: block = (border between two spans, rows);
 // the border behind a segment's first span stands for it.  A row's partial results
 // are added in order by W warps: one, eight results at a time, where items have
-// few (256 short sequences 57.5 -> 53 us, 16 x 5 drafted tokens 44 -> 41.5: most
-// blocks find no border, fewer of them end sooner), or the block's eight (one
+// few (256 short sequences 57.5 -> 53 us, 16 x 5 drafted tokens 44 -> 41.5, both with a
+// warm L2: most blocks find no border, fewer of them end sooner), or the block's eight (one
 // sequence of 131072 keys 44 us, 58 with one warp; 4 of them 123 and 125).
 template <int HD, int NT, int W>
 __global__ void __launch_bounds__(kSumWarps * 32) k_kv_sum(const KvAttnParams p) {

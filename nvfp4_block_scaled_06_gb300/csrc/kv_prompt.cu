@@ -26,10 +26,11 @@
 // fill the GPU; segments in several spans leave partial (o, m, l), joined in
 // order by a second kernel.  A first kernel lists the row tiles.
 //
-// Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 796 us = 1.36 PFLOP/s
-// (71% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 267 us = 1.0.  A
-// key tile takes 3470 cycles: a half's softmax about 1950 and its MMAs' wait and
-// issue 1430 in turn, the other half beside it; the tensor pipe is busy 53%.
+// Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 772 us = 1.40 PFLOP/s
+// (73% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 267 us = 1.03.
+// Traced when the former took 796 us, a key tile was 3470 cycles: a half's softmax
+// about 1950 and its MMAs' wait and issue 1430 in turn, the other half beside it;
+// the tensor pipe is busy 55%.
 #include <float.h>
 #include <math_constants.h>
 
@@ -53,8 +54,8 @@ constexpr float kRaiseSum = 4096.0f;  // of a tile's numerators, beyond which th
 // row's largest numerator with them.
 constexpr float kLarge = 4194304.0f;
 constexpr int kTwo = 1 << 30;       // in an item's key tiles: it has rows in both halves
-// What a segment costs beside its key tiles, in key tiles: 1, 2, 3, 4, 6 give 424,
-// 326, 272, 270, 278 us for the 4096 prompt.
+// What a segment costs beside its key tiles, in key tiles: 1, 2, 3, 4, 6 gave 424,
+// 326, 272, 270, 278 us for the 4096 prompt, which takes 267 with 3 by now.
 constexpr int kOver = 3;
 constexpr uint64_t kKvDrainNs = 200000000ull;
 

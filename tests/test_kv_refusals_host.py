@@ -16,7 +16,7 @@ def test_scales_that_the_kernels_can_hold(clib, scale):  # noqa: F811
 @pytest.mark.parametrize("scale", [2.4e38, 3.0e38, float(np.finfo(np.float32).max)])
 def test_scales_whose_base_2_form_overflows(clib, scale):  # noqa: F811
     """The kernels multiply by scale * log2(e): infinite, it would make NaN of every score of 0."""
-    assert scale * 1.4426950408889634 > np.finfo(np.float32).max
+    assert scale * 1.4426950408889634 > float(np.finfo(np.float32).max)
     assert attend(clib, scale=scale) == B.ERR_INVALID_ARG
 
 
