@@ -27,7 +27,7 @@
 // order by a second kernel.  A first kernel lists the row tiles.
 //
 // Measured: 2 x 1021 queries of 32 heads over 32768 keys of 4, 772 us = 1.40 PFLOP/s
-// (73% of cuBLAS's burst rate); a prompt of 4096, 64 heads on 8, 267 us = 1.03.
+// (73% of cuBLAS's burst rate; 769 to 787 over several GPUs); a prompt of 4096, 64 heads on 8, 267 us = 1.03.
 // Traced when the former took 796 us, a key tile was 3470 cycles: a half's softmax
 // about 1950 and its MMAs' wait and issue 1430 in turn, the other half beside it;
 // the tensor pipe is busy 55%.
